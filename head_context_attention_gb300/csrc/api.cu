@@ -242,7 +242,7 @@ using namespace loong;
 
 extern "C" {
 
-int loong_version(void) { return (0 << 16) | 3; }
+int loong_version(void) { return (0 << 16) | 4; }
 
 const char* loong_status_string(int status) {
   switch (status) {

@@ -32,6 +32,7 @@ EXPORTS = ("loong_version", "loong_status_string", "loong_last_cuda_error", "loo
            "loong_attn_workspace_size", "loong_ring_schedule", "loong_attn_fwd", "loong_attn_fwd_ranks",
            "loong_attn_bwd",
            "loong_attn_bwd_noalloc", "loong_lse_merge", "loong_headctx_pack", "loong_headctx_pack_n",
+           "loong_qk_norm_rope_fwd", "loong_qk_norm_rope_bwd_workspace_size", "loong_qk_norm_rope_bwd",
            "loong_attn_2d_host_workspace_size", "loong_attn_2d_host", "loong_host_alloc", "loong_host_free",
            "loong_set_timing_events", "loong_get_device_status", "loong_selftest_wait_timeout")
 NOALLOC_SCRATCH_BYTES = 32 << 20   # LOONG_NOALLOC_SCRATCH_BYTES
@@ -44,6 +45,15 @@ class LoongAttnDesc(ctypes.Structure):
                 ("ring_inner", ctypes.c_int32), ("ring_outer", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("placement", ctypes.c_int32), ("mode", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float), ("layout", ctypes.c_int32)]
+
+
+class LoongQkOpts(ctypes.Structure):
+    _fields_ = [("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64), ("dv_stride", ctypes.c_int64),
+                ("pos_begin", ctypes.c_int64), ("rot_base", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("rot_scale", ctypes.c_float),
+                ("norm", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class LoongError(RuntimeError):
@@ -85,6 +95,11 @@ def lib():
                                          P, P, P]
         L.loong_headctx_pack_n.argtypes = [I32, I64, I32, I32, I64, ctypes.POINTER(ctypes.c_int32), I32,
                                            ctypes.c_int, ctypes.c_int, ctypes.POINTER(P), ctypes.POINTER(P), P]
+        QO = ctypes.POINTER(LoongQkOpts)
+        L.loong_qk_norm_rope_fwd.argtypes = [D, QO, P, P, P, P, P, P, P, P, P, P]
+        L.loong_qk_norm_rope_bwd_workspace_size.restype = SZ
+        L.loong_qk_norm_rope_bwd_workspace_size.argtypes = [D, QO]
+        L.loong_qk_norm_rope_bwd.argtypes = [D, QO, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         L.loong_attn_2d_host_workspace_size.restype = SZ
         L.loong_attn_2d_host_workspace_size.argtypes = [D, ctypes.c_int]
         L.loong_attn_2d_host.argtypes = [D, I32, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
@@ -184,6 +199,24 @@ def loong_headctx_pack_n(xs, outs, batch, cp, P, s_local, heads, d, direction, g
     ous = (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
     return _check("loong_headctx_pack_n", lib().loong_headctx_pack_n(
         n, batch, cp, P, s_local, hs, d, direction, gather, ins, ous, _stream(stream)))
+
+
+def loong_qk_norm_rope_fwd(desc, opts, q, k, v, wq, wk, positions, q_out, k_out, v_out, stream=None):
+    return _check("loong_qk_norm_rope_fwd", lib().loong_qk_norm_rope_fwd(
+        ctypes.byref(desc), ctypes.byref(opts), _ptr(q), _ptr(k), _ptr(v), _ptr(wq), _ptr(wk), _ptr(positions),
+        _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def loong_qk_norm_rope_bwd_workspace_size(desc, opts):
+    return lib().loong_qk_norm_rope_bwd_workspace_size(ctypes.byref(desc), ctypes.byref(opts))
+
+
+def loong_qk_norm_rope_bwd(desc, opts, q, k, wq, wk, positions, dq_out, dk_out, dv_out, dq, dk, dv, dwq, dwk, ws,
+                           stream=None):
+    return _check("loong_qk_norm_rope_bwd", lib().loong_qk_norm_rope_bwd(
+        ctypes.byref(desc), ctypes.byref(opts), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(dq_out),
+        _ptr(dk_out), _ptr(dv_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dwq), _ptr(dwk), _ptr(ws), _nbytes(ws),
+        _stream(stream)))
 
 
 def loong_attn_2d_host_workspace_size(desc, pass_):
@@ -307,3 +340,131 @@ def headctx_unpack(y, batch, cp, P, gather=1, stream=None):
 
 def default_scale(d):
     return 1.0 / math.sqrt(d)
+
+
+def _same(name, t, shape, dtype, device):
+    """The tensor arguments of the calls below: what the C entry cannot see."""
+    if not torch.is_tensor(t):
+        raise TypeError(f"{name} must be a tensor")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, not {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+
+
+def _contiguous(name, t, shape, dtype, device):
+    _same(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _attn_shape(w, heads, layout):
+    if layout == LAYOUT_RANK_MAJOR:
+        return (w.batch * w.cp, w.hp, w.seqlen // w.cp, heads // w.hp, w.head_dim)
+    return (w.batch, w.seqlen, heads, w.head_dim)
+
+
+def _on(device, stream):
+    """The calls below run on the tensors' device, on its current stream unless one is given."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, not {device}")
+    return torch.cuda.device(device), torch.cuda.current_stream(device) if stream is None else stream
+
+
+class QkOpts:
+    """What qk_norm_rope does to Q and K (loong_qk_opts, without the strides and
+    pos_begin, which belong to a call)."""
+
+    def __init__(self, head_dim, eps=1e-6, norm=True, w_offset=0.0, rot_dim=None, base=10000.0, inv_freq=None,
+                 interleaved=False, rot_scale=1.0):
+        self.rot_dim = head_dim if rot_dim is None else int(rot_dim)
+        self.norm = bool(norm)
+        self._inv = None
+        if inv_freq is not None:
+            inv = [float(x) for x in inv_freq]
+            if len(inv) != self.rot_dim // 2:
+                raise ValueError(f"inv_freq needs {self.rot_dim // 2} values")
+            self._inv = (ctypes.c_double * max(1, len(inv)))(*inv)
+        self._fixed = (float(base), float(eps), float(w_offset), float(rot_scale), 1 if norm else 0, self.rot_dim,
+                       1 if interleaved else 0)
+
+    def struct(self, x_strides=(0, 0, 0), dx_strides=(0, 0, 0), pos_begin=0):
+        base, eps, w_offset, rot_scale, norm, rot_dim, inter = self._fixed
+        inv = None if self._inv is None else ctypes.cast(self._inv, ctypes.POINTER(ctypes.c_double))
+        return LoongQkOpts(*x_strides, *dx_strides, pos_begin, base, inv, eps, w_offset, rot_scale, norm, rot_dim, inter)
+
+
+def make_qk_opts(head_dim, **kw):
+    return QkOpts(head_dim, **kw)
+
+
+def _token_stride(name, t, w, heads, device):
+    """Elements from token to token of a projection: a [B, S, heads, d] view
+    whose heads are contiguous and whose sequences follow each other."""
+    _same(name, t, (w.batch, w.seqlen, heads, w.head_dim), torch.bfloat16, device)
+    sb, ss, sh, sd = t.stride()
+    row = heads * w.head_dim
+    if w.seqlen == 1:  # the token's stride is the sequence's
+        ss = sb if w.batch > 1 else row
+    if sd != 1 or (sh != w.head_dim and heads > 1) or (w.batch > 1 and sb != w.seqlen * ss):
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, not strides {t.stride()}")
+    return ss
+
+
+def _token_strides(names, ts, w, device):
+    return [0 if t is None else _token_stride(n, t, w, h, device) for n, t, h in zip(names, ts, (w.hq, w.hkv, w.hkv))]
+
+
+def _qk_weights(w, wq, wk, positions, device):
+    for n, t in (("wq", wq), ("wk", wk)):
+        if t is not None:
+            _contiguous(n, t, (w.head_dim,), torch.float32, device)
+    if positions is not None:
+        _contiguous("positions", positions, (w.batch, w.seqlen), torch.int64, device)
+
+
+def qk_norm_rope(w, opts, q, k, v=None, wq=None, wk=None, positions=None, pos_begin=0, layout=LAYOUT_NATURAL,
+                 stream=None):
+    """RMS norm and position rotation of every query and key head and the
+    attention's layout, in one pass: projections [B, S, heads, d] (views of one
+    fused projection, or contiguous) -> (q, k, v) as attn_fwd takes them.  ``v``
+    is only brought into the layout; None leaves it out."""
+    desc = make_desc(w, layout=layout)
+    _check("loong_attn_check", loong_attn_check(desc))
+    _qk_weights(w, wq, wk, positions, q.device)
+    o = opts.struct(_token_strides(("q", "k", "v"), (q, k, v), w, q.device), pos_begin=pos_begin)
+    device, stream = _on(q.device, stream)
+    with device, torch.cuda.stream(stream):
+        out = [None if t is None else torch.empty(_attn_shape(w, h, layout), dtype=torch.bfloat16, device=q.device)
+               for t, h in ((q, w.hq), (k, w.hkv), (v, w.hkv))]
+        loong_qk_norm_rope_fwd(desc, o, q, k, v, wq, wk, positions, *out, stream)
+    return tuple(out)
+
+
+def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions=None, pos_begin=0,
+                     layout=LAYOUT_NATURAL, into=None, stream=None):
+    """Gradient of qk_norm_rope: from dq, dk, dv in the attention's layout to
+    (dq, dk, dv, dwq, dwk) of the projections and the norm weights (None where
+    there is none).  ``into``: the three projection gradients to write, e.g.
+    views of one fused gradient (the third None without dv); else they are made
+    contiguous."""
+    desc = make_desc(w, layout=layout)
+    _check("loong_attn_check", loong_attn_check(desc))
+    _qk_weights(w, wq, wk, positions, q.device)
+    for n, t, h in (("dq", dq, w.hq), ("dk", dk, w.hkv), ("dv", dv, w.hkv)):
+        if t is not None or n != "dv":
+            _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, q.device)
+    if into is not None and (into[2] is None) != (dv is None):
+        raise ValueError("into[2] belongs to dv: give both or neither")
+    device, stream = _on(q.device, stream)
+    with device, torch.cuda.stream(stream):
+        if into is None:
+            into = [None if t is None else torch.empty((w.batch, w.seqlen, h, w.head_dim), dtype=torch.bfloat16,
+                                                       device=q.device) for t, h in ((dq, w.hq), (dk, w.hkv), (dv, w.hkv))]
+        o = opts.struct(_token_strides(("q", "k", "v"), (q, k, None), w, q.device),
+                        _token_strides(("into[0]", "into[1]", "into[2]"), into, w, q.device), pos_begin)
+        dwq = None if wq is None or not opts.norm else torch.empty_like(wq)
+        dwk = None if wk is None or not opts.norm else torch.empty_like(wk)
+        n = loong_qk_norm_rope_bwd_workspace_size(desc, o)
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n and (dwq is not None or dwk is not None) else None
+        loong_qk_norm_rope_bwd(desc, o, q, k, wq, wk, positions, dq, dk, dv, *into, dwq, dwk, ws, stream)
+    return (*into, dwq, dwk)

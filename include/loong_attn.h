@@ -320,6 +320,84 @@ LOONG_API int loong_headctx_pack_n(int32_t n, int64_t batch, int32_t cp, int32_t
                                    const void* const* in, void* const* out, loong_stream_t stream);
 
 /*
+ * What loong_qk_norm_rope_fwd does to Q and K.
+ *   q/k/v_stride, elements from one token to the next of the projections q, k, v
+ *   dq/dk/dv_stride  and of their gradients, so that either can be slices of
+ *                 one fused [B, S, W] tensor: 0 = contiguous (heads *
+ *                 head_dim), else at least that and a multiple of 8, at most
+ *                 2^31.  A token's heads are contiguous; a sequence is seqlen
+ *                 strides.
+ *   norm          1: RMS norm of every head of Q and K (eps >= 0 finite, weight
+ *                 w + w_offset, e.g. w_offset 1 for weights stored around 0);
+ *                 0: none.
+ *   rot_dim       the first rot_dim elements of a head rotate, a multiple of 16
+ *                 from 0 (none) to head_dim, in pairs (i, i + rot_dim/2) or,
+ *                 interleaved = 1, (2i, 2i + 1).  Pair i turns by position *
+ *                 inv_freq[i] (HOST array of rot_dim/2 finite values, read
+ *                 during the call) or, inv_freq == NULL, by position *
+ *                 rot_base^(-2i/rot_dim), rot_base > 0 finite.
+ *   rot_scale     factor of every cosine and sine (1 for a plain rotation).
+ *   pos_begin     position of token 0 of every sequence, where no positions are
+ *                 given.
+ * Angles are reduced exactly in 64-bit fixed point: any 64-bit position turns
+ * by its angle to 2^-24, plus position * inv_freq * 2^-53.
+ */
+typedef struct {
+  int64_t q_stride, k_stride, v_stride;
+  int64_t dq_stride, dk_stride, dv_stride;
+  int64_t pos_begin;
+  double rot_base;
+  const double* inv_freq;
+  float eps, w_offset, rot_scale;
+  int32_t norm, rot_dim, interleaved;
+} loong_qk_opts;
+
+/*
+ * From a layer's projections to its attention's inputs in one pass: RMS norm
+ * and rotation of every head of Q and K, and the descriptor's layout.  The
+ * paper starts at the attention; this is the step in front of it, fused with
+ * loong_headctx_pack (direction 0; gather 1 for ZIGZAG, 2 for CONTIGUOUS) when
+ * the layout is RANK_MAJOR.  The descriptor's mode, causal flag and scale do
+ * not matter.
+ *   q, k, v          bf16 projections [B, S, heads, d], token-strided (above).
+ *   wq, wk           fp32 [head_dim] norm weights, or NULL: all ones (w_offset
+ *                    is then not added).
+ *   positions        int64 [B, S], or NULL: pos_begin + token index.
+ *   q_out, k_out,    bf16, the descriptor's layout, contiguous.  v_out is a copy
+ *   v_out            of v; v and v_out may both be NULL.
+ * Norm, rotation and weights are applied in fp32 and rounded to bf16 once.
+ * Outputs must not overlap inputs.
+ */
+LOONG_API int loong_qk_norm_rope_fwd(const loong_attn_desc* desc, const loong_qk_opts* opts, const void* q,
+                                     const void* k, const void* v, const float* wq, const float* wk,
+                                     const int64_t* positions, void* q_out, void* k_out, void* v_out,
+                                     loong_stream_t stream);
+
+/*
+ * Device workspace of loong_qk_norm_rope_bwd, in bytes (0 when opts.norm is 0,
+ * or for invalid arguments).  Host-only.
+ */
+LOONG_API size_t loong_qk_norm_rope_bwd_workspace_size(const loong_attn_desc* desc, const loong_qk_opts* opts);
+
+/*
+ * Gradient of loong_qk_norm_rope_fwd.
+ *   q, k               the forward's inputs (may be NULL when opts.norm is 0).
+ *   dq_out, dk_out,    gradients of the forward's outputs, the descriptor's
+ *   dv_out             layout.
+ *   dq, dk, dv         gradients of the projections, token-strided (elements
+ *                      between a token's heads and the next token are left as
+ *                      they are).  dv_out and dv may both be NULL.
+ *   dwq, dwk           fp32 [head_dim], written, or NULL where not wanted (both
+ *                      NULL when opts.norm is 0).  Summed in a fixed order.
+ *   ws                 needed when dwq or dwk is given.
+ */
+LOONG_API int loong_qk_norm_rope_bwd(const loong_attn_desc* desc, const loong_qk_opts* opts, const void* q,
+                                     const void* k, const float* wq, const float* wk, const int64_t* positions,
+                                     const void* dq_out, const void* dk_out, const void* dv_out, void* dq, void* dk,
+                                     void* dv, float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                                     loong_stream_t stream);
+
+/*
  * Device workspace, in bytes, of loong_attn_2d_host for `desc`: pass 0 runs
  * the forward alone, pass 1 the forward and the backward; 0 for an invalid
  * descriptor.  Host-only.  It holds two sets of natural-layout inputs (the

@@ -1,0 +1,90 @@
+"""Host-side checks of the norm-and-rotation pass: refusals before any CUDA call
+and the workspace size."""
+import ctypes
+
+import pytest
+import torch
+
+from head_context_attention_gb300 import inputs, ops
+
+W = inputs.WORKLOADS["tiny-gqa-s1k"]
+PTR = 1 << 20    # never dereferenced: every call below fails before any CUDA call
+
+
+def _desc(**kw):
+    d = ops.make_desc(W)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def _opts(**kw):
+    o = ops.make_qk_opts(64).struct()
+    for k, v in kw.items():
+        setattr(o, k, v)
+    return o
+
+
+@pytest.mark.parametrize("field,value", [
+    ("rot_dim", 24), ("rot_dim", 80), ("rot_dim", -16), ("norm", 2), ("interleaved", -1), ("eps", -1e-6),
+    ("eps", float("nan")), ("eps", float("inf")), ("w_offset", float("nan")), ("rot_scale", float("inf")),
+    ("rot_base", 0.0), ("rot_base", float("inf")), ("q_stride", 128), ("q_stride", 260), ("k_stride", -8),
+    ("dv_stride", 64), ("v_stride", (1 << 31) + 8)])
+def test_options_refused(loong_lib, field, value):
+    L, p, d = ops.lib(), ctypes.c_void_p(PTR), _desc()
+    o = _opts(**{field: value})
+    assert L.loong_qk_norm_rope_fwd(ctypes.byref(d), ctypes.byref(o), p, p, p, p, p, None, p, p, p, None) == \
+        ops.LOONG_ERR_INVALID_ARG
+    assert ops.loong_qk_norm_rope_bwd_workspace_size(d, o) == 0
+    assert ops.loong_qk_norm_rope_bwd_workspace_size(d, _opts()) > 0
+    assert ops.loong_qk_norm_rope_bwd_workspace_size(d, _opts(norm=0)) == 0
+
+
+def test_frequencies_refused(loong_lib):
+    bad = ops.make_qk_opts(64, inv_freq=[1.0] * 31 + [float("nan")]).struct()
+    assert ops.loong_qk_norm_rope_bwd_workspace_size(_desc(), bad) == 0
+    with pytest.raises(ValueError):
+        ops.make_qk_opts(64, inv_freq=[1.0] * 31)
+
+
+def test_calls_refuse_before_any_cuda_call(loong_lib):
+    L, d, p, odd = ops.lib(), _desc(), ctypes.c_void_p(PTR), ctypes.c_void_p(PTR + 8)
+    o = _opts()
+    # q, k, v, wq, wk, positions, q_out, k_out, v_out
+    fwd = lambda **b: L.loong_qk_norm_rope_fwd(ctypes.byref(d), ctypes.byref(o), *[b.get(n, p) for n in (
+        "q", "k", "v", "wq", "wk", "positions", "q_out", "k_out", "v_out")], None)
+    for n in ("q", "k", "q_out", "k_out", "v", "v_out"):          # v alone or v_out alone
+        assert fwd(**{n: None}) == ops.LOONG_ERR_INVALID_ARG
+    for n in ("q", "wq", "wk", "v_out"):
+        assert fwd(**{n: odd}) == ops.LOONG_ERR_INVALID_ARG
+    assert fwd(positions=ctypes.c_void_p(PTR + 4)) == ops.LOONG_ERR_INVALID_ARG
+    names = ("q", "k", "wq", "wk", "positions", "dq_out", "dk_out", "dv_out", "dq", "dk", "dv", "dwq", "dwk", "ws")
+    bwd = lambda n=1 << 40, o=o, **b: L.loong_qk_norm_rope_bwd(ctypes.byref(d), ctypes.byref(o),
+                                                             *[b.get(x, p) for x in names], n, None)
+    for n in ("q", "k", "dq_out", "dk_out", "dq", "dk", "dv", "dv_out"):
+        assert bwd(**{n: None}) == ops.LOONG_ERR_INVALID_ARG
+    assert bwd(o=_opts(norm=0)) == ops.LOONG_ERR_INVALID_ARG     # a weight gradient without a norm
+    need = ops.loong_qk_norm_rope_bwd_workspace_size(d, o)
+    assert bwd(n=need - 1) == ops.LOONG_ERR_WORKSPACE
+    assert bwd(ws=None) == ops.LOONG_ERR_WORKSPACE
+    assert bwd(ws=odd) == ops.LOONG_ERR_WORKSPACE
+    assert bwd(dwq=ctypes.c_void_p(PTR + 2)) == ops.LOONG_ERR_INVALID_ARG
+
+
+def test_tensor_calls_refuse_wrong_tensors(loong_lib):
+    x = inputs.make_inputs(W)
+    opts = ops.make_qk_opts(64)
+    w1 = torch.ones(64)
+    for kw in (dict(q=x["q"].transpose(1, 2)), dict(k=x["k"].float()), dict(wq=w1[:32]), dict(wk=w1.double()),
+               dict(positions=torch.zeros((1, 1024), dtype=torch.int32)),
+               dict(positions=torch.zeros((1, 1023), dtype=torch.int64)), dict(v=x["v"][..., ::2])):
+        with pytest.raises(ValueError):
+            ops.qk_norm_rope(W, opts, **{**dict(q=x["q"], k=x["k"], v=x["v"]), **kw})
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.qk_norm_rope(W, opts, x["q"], x["k"], x["v"])
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.qk_norm_rope_bwd(W, opts, x["q"], x["k"], x["q"], x["k"], x["v"])
+    with pytest.raises(ValueError, match="into"):
+        ops.qk_norm_rope_bwd(W, opts, x["q"], x["k"], x["q"], x["k"], x["v"], into=(x["q"], x["k"], None))
+    with pytest.raises(ValueError):
+        ops.qk_norm_rope_bwd(W, opts, x["q"], x["k"], x["q"], x["k"][:, 1:], x["v"])
