@@ -223,6 +223,36 @@ static FwdScratch fwd_scratch(const loong_attn_desc& d, void* ws, void* o_res) {
   return sc;
 }
 
+int run_attn_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
+                 void* o_res, void* ws, cudaStream_t stream, const BiasView* bias) {
+  const FwdScratch sc = fwd_scratch(d, ws, o_res);
+  if (d.mode == LOONG_MODE_FUSED) return launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias);
+  const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
+  cudaError_t e = cudaMemsetAsync(sc.o_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  int st;
+  if ((st = launch_fill_f32(lse, d.batch * d.hq * d.seqlen, -INFINITY, stream)) != LOONG_OK) return st;
+  if ((st = launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias)) != LOONG_OK) return st;
+  return launch_f32_to_bf16(sc.o_acc, o, q_elems, stream, o_res);
+}
+
+int run_attn_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
+                 const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
+                 cudaStream_t stream, const BiasView* bias, float* dbias_part) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t q_elems = static_cast<size_t>(d.batch) * d.seqlen * d.hq * d.head_dim;
+  const size_t kv_elems = static_cast<size_t>(d.batch) * d.seqlen * d.hkv * d.head_dim;
+  const size_t stats = 2 * static_cast<size_t>(d.batch) * d.hq * stat_row_len(ring_geom(d));
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  float* dq_acc = reinterpret_cast<float*>(w);
+  float* dvec = reinterpret_cast<float*>(w + up(q_elems * 4));
+  float* dk_acc = reinterpret_cast<float*>(w + up(q_elems * 4) + up(stats * 4));
+  float* dv_acc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dk_acc) + up(kv_elems * 4));
+  void* recv = is_copy_mode(d) ? reinterpret_cast<uint8_t*>(dv_acc) + up(kv_elems * 4) : nullptr;
+  return launch_bwd(d, q, k, v, o, o_res, lse, dout, dq, dk, dv, dq_acc, dvec, dk_acc, dv_acc, stream, recv, bias,
+                    dbias_part);
+}
+
 Layout layout_of(const loong_attn_desc& d) {
   const RingGeom g = ring_geom(d);
   Layout l;
@@ -321,15 +351,7 @@ int loong_attn_fwd(const loong_attn_desc* d, const void* q, const void* k, const
   if (!ws || ws_bytes < need || !aligned16(ws)) return LOONG_ERR_WORKSPACE;
   if ((st = device_ready()) != LOONG_OK) return st;
   if (!all_on_device(q, k, v, o, lse, ws) || (o_res && !on_device(o_res))) return LOONG_ERR_INVALID_ARG;
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const FwdScratch sc = fwd_scratch(*d, ws, o_res);
-  if (d->mode == LOONG_MODE_FUSED) return launch_fwd(*d, q, k, v, o, lse, sc, stream);
-  const int64_t q_elems = d->batch * d->seqlen * d->hq * d->head_dim;
-  cudaError_t e = cudaMemsetAsync(sc.o_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if ((st = launch_fill_f32(lse, d->batch * d->hq * d->seqlen, -INFINITY, stream)) != LOONG_OK) return st;
-  if ((st = launch_fwd(*d, q, k, v, o, lse, sc, stream)) != LOONG_OK) return st;
-  return launch_f32_to_bf16(sc.o_acc, o, q_elems, stream, o_res);
+  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, reinterpret_cast<cudaStream_t>(stream_), nullptr);
 }
 
 int loong_attn_fwd_ranks(const loong_attn_desc* d, int32_t rank_begin, int32_t rank_end, const void* q,
@@ -367,18 +389,8 @@ int loong_attn_bwd(const loong_attn_desc* d, const void* q, const void* k, const
   for (const void* p : ptrs)
     if (!on_device(p)) return LOONG_ERR_INVALID_ARG;
   if (!on_device(ws) || (o_res && !on_device(o_res))) return LOONG_ERR_INVALID_ARG;
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t q_elems = static_cast<size_t>(d->batch) * d->seqlen * d->hq * d->head_dim;
-  const size_t kv_elems = static_cast<size_t>(d->batch) * d->seqlen * d->hkv * d->head_dim;
-  const size_t stats = 2 * static_cast<size_t>(d->batch) * d->hq * stat_row_len(ring_geom(*d));
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  float* dq_acc = reinterpret_cast<float*>(w);
-  float* dvec = reinterpret_cast<float*>(w + up(q_elems * 4));
-  float* dk_acc = reinterpret_cast<float*>(w + up(q_elems * 4) + up(stats * 4));
-  float* dv_acc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dk_acc) + up(kv_elems * 4));
-  void* recv = is_copy_mode(*d) ? reinterpret_cast<uint8_t*>(dv_acc) + up(kv_elems * 4) : nullptr;
-  return launch_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, dq_acc, dvec, dk_acc, dv_acc, stream, recv);
+  return run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, reinterpret_cast<cudaStream_t>(stream_),
+                      nullptr, nullptr);
 }
 
 int loong_lse_merge(int64_t rows, int32_t d, int32_t n_parts, const float* o_parts, const float* lse_parts,

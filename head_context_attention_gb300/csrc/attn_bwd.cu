@@ -56,9 +56,9 @@ struct BwdCfg {
   static constexpr int STAT_BYTES = 2 * kTile * 4;  // LSE*log2e and D of one query tile
   // Tiles first (1024-byte aligned, checked at run time), then the row
   // statistics stages, the barriers, the TMEM base address and the abort
-  // flag, then one iteration descriptor per stage.
+  // flag, then two iteration descriptors per stage (the second for the bias).
   static constexpr int SMEM_BYTES =
-      (2 + 2 * NS) * TILE_BYTES + DS_BYTES + NS * STAT_BYTES + NBARS * 8 + 16 + NS * 16;
+      (2 + 2 * NS) * TILE_BYTES + DS_BYTES + NS * STAT_BYTES + NBARS * 8 + 16 + 2 * NS * 16;
   // Compute groups of four warps, each covering all 128 TMEM lanes: group g
   // owns query columns [GW g, GW (g+1)) of S^T / dP^T and head-dim columns
   // [GD g, GD (g+1)) of dQ.  Four groups (four compute warps per scheduler)
@@ -73,6 +73,7 @@ struct BwdCfg {
   static constexpr int GD = D / GROUPS;      // dQ head-dim columns per group
   static constexpr int ACC_COLS = 2 * D / GROUPS;  // dV / dK columns each group folds
   static constexpr int CW = 4 * GROUPS;      // compute warps; then producer, MMA, reducer
+  static_assert(CW == kBwdComputeWarps, "rows of the bias gradient's parts");
   static constexpr int THREADS = 32 * (CW + 3);
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t R0 = 0, R1 = 128, RV = 256, RK = 256 + D;
@@ -114,12 +115,23 @@ struct BwdArgs {
   __nv_bfloat16* dv;
   float* dk_acc;      // fp32 accumulators, the layout of K (zeroed by the launcher)
   float* dv_acc;
+  BiasView bias;      // BIAS: the bias by distance
+  float* dbias_part;  // BIAS: [blocks][compute warps][G][intervals], zeroed
   unsigned* err;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, bool STEP>
+// BIAS: the scores carry the bias of their distance (see attn_fwd.cu) and the
+// kernel sums dS by interval of distances, the gradient of the bias.  A tile
+// inside one interval adds its constant to the exponent's offset and its dS sum
+// to one number: a warp sums its part by shuffles and lane g keeps the running
+// sum of the group's head g, written out when the interval changes.  In a tile
+// that a boundary crosses, dS is summed along the diagonals (the sum for a
+// distance moves one lane up with every column) and the diagonals' sums are
+// added up by interval.  Every warp adds to numbers of its own, so the sums do
+// not depend on the order in which blocks run.
+template <int D, bool STEP, bool BIAS>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     ring_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -164,6 +176,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // q_full arrival, so everyone who waited for the stage's data sees it; the
   // compute and reducer warps then need no walk of their own.
   int4* sInfo = reinterpret_cast<int4*>(bars + C::NBARS + 2);
+  // BIAS, per stage: the constant bias in log2 units, the tile's interval (-1: a
+  // boundary crosses it), the place of distance q0 - k0, the head in its group.
+  int4* sBias = sInfo + C::NS;
 
   // ---- work item: (batch, kv head, key tile); early (heavy) key tiles first
   const RingGeom& g = a.ring;
@@ -261,8 +276,18 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // checked build: a reduction never starts outside the accumulator (skipped if it would)
         const bool red_ok =
             in_bounds(qrow64 >= 0 && qrow64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
+        int4 tb;
+        if constexpr (BIAS) {
+          const int i0 = a.bias.off + walk.q0() - k0;
+          const int lo = a.bias.interval[i0 - (kTile - 1)], hi = a.bias.interval[i0 + (kTile - 1)];
+          const float c = lo == hi ? a.bias.lut[head * a.bias.len + i0] * a.scale_log2 : 0.f;
+          tb = make_int4(__float_as_int(c), lo == hi ? lo : -1, i0, walk.head);
+        }
         if (i >= C::NS && !warp_wait(&q_empty[s], (u - 1) & 1, abort_flag, a.err)) break;
-        if (leader) sInfo[s] = make_int4(qrow, hc, walk.qlen(), (walk.diag() ? 1 : 0) | (red_ok ? 2 : 0));
+        if (leader) {
+          sInfo[s] = make_int4(qrow, hc, walk.qlen(), (walk.diag() ? 1 : 0) | (red_ok ? 2 : 0));
+          if constexpr (BIAS) sBias[s] = tb;
+        }
         mbar_expect_tx_p(leader, &q_full[s], 2 * C::TILE_BYTES + C::STAT_BYTES);
         for (int at = 0; at < C::ATOMS; ++at) {
           tma_load_3d_p(leader, sQ + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, &q_full[s], at * 64, hc, qrow);
@@ -439,6 +464,17 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err));
     };
+    // BIAS: this warp's sums of dS, [G][intervals]; lane g keeps the running sum
+    // of head 32 sum_block + g in interval sum_ivl
+    float* part = BIAS ? a.dbias_part + (static_cast<int64_t>(blockIdx.x) * C::CW + warp) * a.G * a.bias.intervals
+                       : nullptr;
+    float run_sum = 0.f;
+    int sum_ivl = -1, sum_block = 0;
+    auto flush_sum = [&]() {
+      if (sum_ivl >= 0 && sum_block * 32 + lane < a.G)
+        atomicAdd(part + (sum_block * 32 + lane) * a.bias.intervals + sum_ivl, run_sum);
+      run_sum = 0.f;
+    };
     for (int i = 0; i < n; ++i) {
       // row statistics of this tile, staged by the producer with Q and dO
       const float* lse_row = sStat + (i % C::NS) * (2 * kTile);
@@ -453,6 +489,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       const int4 info = sInfo[i % C::NS];
       const int qlen = info.z;
       const bool dg = info.w & 1;
+      int4 tb = make_int4(0, 0, 0, 0);
+      if constexpr (BIAS) tb = sBias[i % C::NS];
+      const float tile_b = __int_as_float(tb.x);
       float pv[C::GCH][32];
       {
         uint32_t sv[C::GCH][32];
@@ -464,6 +503,17 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) pv[ch][e] = __uint_as_float(sv[ch][e]);
       }
+      if constexpr (BIAS) {
+        if (tb.y < 0) {
+          const float* lp = a.bias.lut + static_cast<int64_t>(kvh * a.G + tb.w) * a.bias.len + tb.z - row + grp * C::GW;
+#pragma unroll
+          for (int ch = 0; ch < C::GCH; ++ch)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pv[ch][e] += __ldg(lp + ch * 32 + e);
+        }
+      }
+      // the exponent's offset of a query: the tile's bias minus its LSE
+      auto ofs = [&](float lse2) { return BIAS ? tile_b - lse2 : -lse2; };
       // Query columns c with lo <= c < hi are live for this key row (causal
       // diagonal, ragged query tile, key row past the block).  Interior tiles
       // have every column live and skip the per-element mask.
@@ -479,10 +529,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           for (int e = 0; e < 32; e += 4) {
             // the same query indices in every lane: broadcast shared-memory reads
             const float4 l4 = *reinterpret_cast<const float4*>(lse_row + cbase + e);
-            pv[ch][e] = fast_exp2(fmaf(pv[ch][e], a.scale_log2, -l4.x));
-            pv[ch][e + 1] = fast_exp2(fmaf(pv[ch][e + 1], a.scale_log2, -l4.y));
-            pv[ch][e + 2] = fast_exp2(fmaf(pv[ch][e + 2], a.scale_log2, -l4.z));
-            pv[ch][e + 3] = fast_exp2(fmaf(pv[ch][e + 3], a.scale_log2, -l4.w));
+            pv[ch][e] = fast_exp2(fmaf(pv[ch][e], a.scale_log2, ofs(l4.x)));
+            pv[ch][e + 1] = fast_exp2(fmaf(pv[ch][e + 1], a.scale_log2, ofs(l4.y)));
+            pv[ch][e + 2] = fast_exp2(fmaf(pv[ch][e + 2], a.scale_log2, ofs(l4.z)));
+            pv[ch][e + 3] = fast_exp2(fmaf(pv[ch][e + 3], a.scale_log2, ofs(l4.w)));
           }
         } else {
 #pragma unroll
@@ -493,7 +543,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             for (int u = 0; u < 4; ++u) {
               const int c = cbase + e + u;
               // masked columns may hold statistics of other rows or padding: select
-              const float x = fast_exp2(fmaf(pv[ch][e + u], a.scale_log2, -lv[u]));
+              const float x = fast_exp2(fmaf(pv[ch][e + u], a.scale_log2, ofs(lv[u])));
               pv[ch][e + u] = (c >= lo && c < hi) ? x : 0.f;
             }
           }
@@ -540,6 +590,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             const float x = p * (__uint_as_float(dpv[e + u]) - dv4[u]);
             // masked columns: p is 0 and D may be another row's or padding
             ds[u] = unmasked ? x : (p != 0.f ? x : 0.f);
+            if constexpr (BIAS) pv[ch][e + u] = ds[u];  // kept for the bias gradient
           }
           dsk[e / 2] = pack_bf16(ds[0], ds[1]);
           dsk[e / 2 + 1] = pack_bf16(ds[2], ds[3]);
@@ -563,6 +614,56 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       tc_fence_before();
       __syncwarp();
       mbar_arrive_p(lane == 0, ds_full);
+
+      // ---- the bias gradient's sums of dS, while dQ is computed
+      if constexpr (BIAS) {
+        if (tb.y >= 0) {
+          if (tb.y != sum_ivl || (tb.w >> 5) != sum_block) {
+            flush_sum();
+            sum_ivl = tb.y;
+            sum_block = tb.w >> 5;
+          }
+          float s4[4] = {};
+#pragma unroll
+          for (int ch = 0; ch < C::GCH; ++ch)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s4[e & 3] += pv[ch][e];
+          float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane == (tb.w & 31)) run_sum += s;
+        } else {
+          float* ph = part + tb.w * a.bias.intervals;
+#pragma unroll
+          for (int ch = 0; ch < C::GCH; ++ch) {
+            // lane l, column c: distance at place base + c - l
+            const uint8_t* at = a.bias.interval + tb.z + grp * C::GW + ch * 32 - quarter * 32;
+            float acc = 0.f, fin = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              acc += pv[ch][c];
+              const float done = __shfl_sync(0xffffffffu, acc, 31);  // distance base + c - 31
+              if (lane == c) fin = done;
+              acc = __shfl_up_sync(0xffffffffu, acc, 1);
+              if (lane == 0) acc = 0.f;
+            }
+            // now lane l holds the sums of distances base + l - 31 (fin) and,
+            // l > 0, base + 32 - l (acc); intervals are runs of lanes
+            auto add_runs = [&](float v, int id) {
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const float v2 = __shfl_down_sync(0xffffffffu, v, o);
+                const int id2 = __shfl_down_sync(0xffffffffu, id, o);
+                if (lane + o < 32 && id2 == id) v += v2;
+              }
+              const int before = __shfl_up_sync(0xffffffffu, id, 1);
+              if (lane == 0 || before != id) atomicAdd(ph + id, v);
+            };
+            add_runs(fin, at[lane - 31]);
+            add_runs(acc, at[32 - (lane > 0 ? lane : 1)]);
+          }
+        }
+      }
 
       // ---- drain dQ (queries on lanes): TMEM -> registers, R1 released, then
       // staged (fp32, 128-byte swizzled boxes of 32 columns) into this
@@ -652,6 +753,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         mbar_arrive_p(lane == 0, acc_empty);
       }
     }
+    if constexpr (BIAS) flush_sum();
     // ---------------------------------------------------------- epilogue
     if (ok) ok = warp_wait(done_bar, 0);
     if (ok) {
@@ -708,10 +810,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool STEP>
+template <int D, bool STEP, bool BIAS>
 int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* dout,
                  const float* stats, float* dq_acc, void* dk, void* dv, float* dk_acc,
-                 float* dv_acc, cudaStream_t stream, void* kv_recv) {
+                 float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias, float* dbias_part) {
   using C = BwdCfg<D>;
   const Layout lay = layout_of(d);
   const int64_t rows = lay.view_rows(d.batch);
@@ -744,9 +846,11 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dk_acc = dk_acc;
   a.dv_acc = dv_acc;
+  a.bias = BIAS ? *bias : BiasView{};
+  a.dbias_part = dbias_part;
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
-  auto kern = ring_bwd_kernel<D, STEP>;
+  auto kern = ring_bwd_kernel<D, STEP, BIAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(a.ring.nblocks) * a.ring.ntile;
@@ -797,11 +901,30 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   return LOONG_OK;
 }
 
+template <bool BIAS>
+int launch_bwd_b(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* dout,
+                 const float* stats, float* dq_acc, void* dk, void* dv, float* dk_acc, float* dv_acc,
+                 cudaStream_t stream, void* kv_recv, const BiasView* bias, float* part) {
+  const bool step = d.mode != LOONG_MODE_FUSED;
+  if (d.head_dim == 128)
+    return step ? launch_bwd_t<128, true, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                kv_recv, bias, part)
+                : launch_bwd_t<128, false, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                 kv_recv, bias, part);
+  if (d.head_dim == 64)
+    return step ? launch_bwd_t<64, true, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                               kv_recv, bias, part)
+                : launch_bwd_t<64, false, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                kv_recv, bias, part);
+  return LOONG_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
 int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
                const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, float* dq_acc, float* dvec,
-               float* dk_acc, float* dv_acc, cudaStream_t stream, void* kv_recv) {
+               float* dk_acc, float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias,
+               float* dbias_part) {
   const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
   const int64_t kv_elems = d.batch * d.seqlen * d.hkv * d.head_dim;
   const bool step = d.mode != LOONG_MODE_FUSED;
@@ -812,14 +935,10 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
       (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess)
     return cuda_fail(e);
   if ((st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream)) != LOONG_OK) return st;
-  if (d.head_dim == 128)
-    st = step ? launch_bwd_t<128, true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv)
-              : launch_bwd_t<128, false>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv);
-  else if (d.head_dim == 64)
-    st = step ? launch_bwd_t<64, true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv)
-              : launch_bwd_t<64, false>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv);
-  else
-    return LOONG_ERR_UNSUPPORTED;
+  st = bias ? launch_bwd_b<true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,
+                                 dbias_part)
+            : launch_bwd_b<false>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, nullptr,
+                                  nullptr);
   if (st != LOONG_OK) return st;
   if ((st = launch_f32_to_bf16(dq_acc, dq, q_elems, stream)) != LOONG_OK) return st;
   if (step) {

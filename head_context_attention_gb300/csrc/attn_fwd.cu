@@ -66,6 +66,11 @@ struct FwdCfg {
   static constexpr int TILE_BYTES = kTile * D * 2;
   static constexpr int NSB = D == 64 ? 3 : 2;      // score buffers in tensor memory
   static constexpr int NBARS = 1 + 4 * NS + 3 + 3 + 2 + 2;
+  // Bias: what the producer knows about the last NINFO key tiles.  Entry j is
+  // rewritten for tile j + NINFO once K(j + NINFO - NS) has been read, which is
+  // after the softmax of tiles up to j + NINFO - NS - 2.
+  static constexpr int NINFO = 8;
+  static_assert(NINFO >= NS + 2, "a tile's entry is read before it is rewritten");
   static constexpr int SMEM_BYTES = (NQ + 2 * NS) * TILE_BYTES + NBARS * 8 + 1024;
   static constexpr int THREADS = 320;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -87,6 +92,7 @@ struct FwdArgs {
   float* lse;
   float* o_acc;            // STEPWISE accumulator, else null
   const unsigned* v_amax;  // bit pattern of max |V|: V was stored as V * 2^-v16_shift
+  BiasView bias;           // BIAS: the bias by distance
   unsigned* err;
 };
 
@@ -101,7 +107,14 @@ constexpr float kPBias = 7.0f;
 constexpr float kSumBound = 32768.0f;
 static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bound = 2^(bias + threshold)");
 
-template <int D, bool STEP>
+// BIAS adds bias(q - k) of the query's head to every scaled score.  Most tiles
+// lie inside one interval of distances: their bias is a constant that goes into
+// the exponent's offset and the tile maximum, at no cost per score.  In a tile
+// that an interval boundary crosses, each score gets its own value from the
+// bias by distance (in units of the unscaled score), where neighbouring rows
+// read neighbouring words.  A bias of -inf masks like a causal mask; a row that
+// it leaves nothing gets O = 0 and LSE = -inf.
+template <int D, bool STEP, bool BIAS>
 __global__ void __launch_bounds__(320, 1)
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
@@ -109,6 +122,9 @@ __global__ void __launch_bounds__(320, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  // BIAS, per tile: the constant bias of head slots 0 and 1 in log2 units, and
+  // whether the tile is crossed by an interval boundary
+  __shared__ float4 tile_bias[BIAS ? C::NINFO : 1];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -218,7 +234,18 @@ __global__ void __launch_bounds__(320, 1)
                                        : a.lay.view_row(b, walk.k0(), kvh, a.hkv, kvc);
         in_bounds(k064 >= 0 && k064 < a.lay.view_rows(a.batch) && kvc >= 0 && kvc < a.lay.view_heads(a.hkv), a.err);
         const int k0 = static_cast<int>(k064);
+        float4 tb;
+        if constexpr (BIAS) {
+          const int64_t i0 = a.bias.off + q0 - walk.k0();  // place of distance q0 - k0
+          const bool mixed = a.bias.interval[i0 - (kTile - 1)] != a.bias.interval[i0 + (kTile - 1)];
+          tb.x = mixed ? 0.f : a.bias.lut[head0 * a.bias.len + i0] * a.scale_log2;
+          tb.y = mixed ? 0.f : a.bias.lut[head1 * a.bias.len + i0] * a.scale_log2;
+          tb.z = mixed ? 1.f : 0.f;
+          tb.w = 0.f;
+        }
         if (j >= C::NS && !mbar_wait(&k_empty[s], (u - 1) & 1, abort_flag, a.err)) break;
+        // written before the tile's arrival, so whoever waited for its scores sees it
+        if constexpr (BIAS) tile_bias[j % C::NINFO] = tb;
         mbar_expect_tx(&k_full[s], C::TILE_BYTES);
         for (int at = 0; at < C::ATOMS; ++at)
           tma_load_3d(sK + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmK, &k_full[s], at * 64, kvc, k0);
@@ -316,6 +343,9 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tO = tbase + t_lane + C::O_COL(h);
     const float sl2 = a.scale_log2;
+    // BIAS: the bias of this row's query at distance off from the row
+    const float* lut_row =
+        BIAS ? a.bias.lut + static_cast<int64_t>(h ? head1 : head0) * a.bias.len + a.bias.off + q0 + row : nullptr;
     float m_run = -INFINITY;
     float l_run = 0.f;
     bool ok = true;
@@ -331,11 +361,28 @@ __global__ void __launch_bounds__(320, 1)
       uint32_t sr[4][32];
       const int klen = walk.klen();
       const bool dg = walk.diag();
+      float tile_b = 0.f;  // the tile's constant bias (log2 units)
+      bool mixed = false;
+      if constexpr (BIAS) {
+        const float4 tb = tile_bias[j % C::NINFO];
+        tile_b = h ? tb.y : tb.x;
+        mixed = tb.z != 0.f;
+      }
       // the tile's scores, masked columns at -inf (read again by the full path)
       auto load_s = [&]() {
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) tmem_ld32(tS + cb * 32, sr[cb]);
         tmem_wait_ld();
+        if constexpr (BIAS) {
+          if (mixed) {
+            const float* lp = lut_row - walk.k0();
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sr[cb][i] = __float_as_uint(__uint_as_float(sr[cb][i]) + __ldg(lp - (cb * 32 + i)));
+          }
+        }
         if (dg || klen < kTile) {
           const int lim = dg ? min(row, klen - 1) : klen - 1;
 #pragma unroll
@@ -351,7 +398,8 @@ __global__ void __launch_bounds__(320, 1)
       // (l carries the factor 2^bias as well)
       uint32_t pk[2][32];
       auto form_p = [&](float ref) {
-        const float2 sl2v = make_float2(sl2, sl2), nref = make_float2(kPBias - ref, kPBias - ref);
+        const float off = BIAS ? kPBias - ref + tile_b : kPBias - ref;
+        const float2 sl2v = make_float2(sl2, sl2), nref = make_float2(off, off);
         float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb)
@@ -390,7 +438,7 @@ __global__ void __launch_bounds__(320, 1)
             mx0 = fmax3(mx0, __uint_as_float(sr[cb][i]), __uint_as_float(sr[cb][i + 1]));
             mx1 = fmax3(mx1, __uint_as_float(sr[cb][i + 2]), __uint_as_float(sr[cb][i + 3]));
           }
-        const float m_tile = fmaxf(mx0, mx1) * sl2;
+        const float m_tile = BIAS ? fmaf(fmaxf(mx0, mx1), sl2, tile_b) : fmaxf(mx0, mx1) * sl2;
         const float m_new = fmaxf(m_run, m_tile);
         // A row whose sum reached the bound takes the new maximum even below the
         // threshold (its maximum is then above the reference): a reference
@@ -499,7 +547,7 @@ __global__ void __launch_bounds__(320, 1)
           const float tot = wa + wp;
           if (tot > 0.f) {
             ca = wa / tot;
-            cpart = wp * o_mul / (tot * l_run);
+            cpart = wp > 0.f ? wp * o_mul / (tot * l_run) : 0.f;  // an empty part has l_run = 0
             lse_new = mm + log2f(tot) * kLn2;
           }
         }
@@ -535,9 +583,10 @@ __global__ void __launch_bounds__(320, 1)
   }
 }
 
-template <int D, bool STEP>
+template <int D, bool STEP, bool BIAS>
 int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o,
-                 float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end) {
+                 float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end,
+                 const BiasView* bias) {
   using C = FwdCfg<D>;
   const Layout lay = layout_of(d);
   const int64_t rows = lay.view_rows(d.batch);
@@ -569,10 +618,11 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   a.lse = lse;
   a.o_acc = sc.o_acc;
   a.v_amax = sc.v_amax;
+  a.bias = BIAS ? *bias : BiasView{};
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
 
-  auto kern = ring_fwd_kernel<D, STEP>;
+  auto kern = ring_fwd_kernel<D, STEP, BIAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring) *
@@ -622,22 +672,30 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   return LOONG_OK;
 }
 
+template <bool BIAS>
+int launch_fwd_b(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
+                 cudaStream_t stream, int rank_begin, int rank_end, const BiasView* bias) {
+  const bool step = d.mode != LOONG_MODE_FUSED;
+  if (d.head_dim == 128)
+    return step ? launch_fwd_t<128, true, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
+                : launch_fwd_t<128, false, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+  if (d.head_dim == 64)
+    return step ? launch_fwd_t<64, true, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
+                : launch_fwd_t<64, false, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+  return LOONG_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
-               float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end) {
-  const bool step = d.mode != LOONG_MODE_FUSED;
+               float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end,
+               const BiasView* bias) {
   if (rank_end < 0) rank_end = d.cp;
   int st;
   if ((st = launch_v_to_f16(v, sc.v16, sc.v_amax, d.batch * d.seqlen * d.hkv * d.head_dim, stream)) != LOONG_OK)
     return st;
-  if (d.head_dim == 128)
-    return step ? launch_fwd_t<128, true>(d, q, k, o, lse, sc, stream, rank_begin, rank_end)
-                : launch_fwd_t<128, false>(d, q, k, o, lse, sc, stream, rank_begin, rank_end);
-  if (d.head_dim == 64)
-    return step ? launch_fwd_t<64, true>(d, q, k, o, lse, sc, stream, rank_begin, rank_end)
-                : launch_fwd_t<64, false>(d, q, k, o, lse, sc, stream, rank_begin, rank_end);
-  return LOONG_ERR_UNSUPPORTED;
+  return bias ? launch_fwd_b<true>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
+              : launch_fwd_b<false>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr);
 }
 
 }  // namespace loong

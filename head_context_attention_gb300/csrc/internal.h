@@ -88,16 +88,42 @@ struct FwdWsLayout {
 };
 FwdWsLayout fwd_ws_layout(const loong_attn_desc& d);
 
+// The relative bias as the attention kernels read it (rel_bias.cu fills it):
+// place off + n stands for distance n = q - k, for every distance that any tile
+// reaches (masked and ragged rows included).
+struct BiasView {
+  const float* lut = nullptr;         // [hq][len], bias / softmax scale
+  const uint8_t* interval = nullptr;  // [len], ascending
+  int64_t len = 0;
+  int off = 0;
+  int intervals = 0;
+};
+
 // Kernel launchers (asynchronous on `stream`).
 // Query rows of ring ranks [rank_begin, rank_end) only (all of them: 0, cp).
 // The forward first writes V's fp16 copy into sc.v16.
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
-               float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin = 0, int rank_end = -1);
+               float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin = 0, int rank_end = -1,
+               const BiasView* bias = nullptr);
 // o_res: the forward's residual of O, or null (D from O alone).
 int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v,
                const void* o, const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv,
                float* dq_acc, float* dvec, float* dk_acc, float* dv_acc, cudaStream_t stream,
-               void* kv_recv = nullptr);
+               void* kv_recv = nullptr, const BiasView* bias = nullptr, float* dbias_part = nullptr);
+// The whole passes behind the entry points, on checked arguments, in a
+// workspace of loong_attn_workspace_size bytes.
+int run_attn_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
+                 void* o_res, void* ws, cudaStream_t stream, const BiasView* bias);
+int run_attn_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
+                 const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
+                 cudaStream_t stream, const BiasView* bias, float* dbias_part);
+// Blocks of a backward launch (key tiles of every kv head and sequence) and
+// compute warps of each: the rows of dbias_part.
+constexpr int kBwdComputeWarps = 16;
+inline int64_t bwd_blocks(const loong_attn_desc& d) {
+  const RingGeom g = ring_geom(d);
+  return d.batch * d.hkv * static_cast<int64_t>(g.nblocks) * g.ntile;
+}
 // max |V| into *amax (two launches: the maximum, then V * 2^-e as fp16 into v16).
 int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream);
 

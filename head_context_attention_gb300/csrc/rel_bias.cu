@@ -1,0 +1,277 @@
+// rel_bias.cu -- ring attention with a learned bias of the distance q - k, in
+// buckets: the entry points, the bias by distance that the attention kernels
+// read, and the sum of the bias gradient's parts.
+//
+//   logit_ij = scale q_i . k_j + table[bucket(i - j)][head]
+//   dtable[t][head] = sum over i, j with bucket(i - j) = t of dS_ij
+//
+// bucket() is piecewise constant in the distance.  It is expanded once per call
+// into the bias of every distance (in units of the unscaled score, so that a
+// score takes it with one add) and the distance's interval; the attention
+// kernels decide from the interval at a tile's two extreme distances whether
+// the whole tile shares one value.  The expansion is hq * S words against
+// hq * S^2 / 2 scores.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace loong {
+
+namespace {
+
+constexpr int kMaxIntervals = 256;
+constexpr int kMaxBuckets = 256;
+constexpr int kThreads = 256;
+// Below this a table value masks, as -inf does: the score's own part is lost in
+// it anyway, and divided by the smallest scale accepted it is still finite.
+constexpr float kMaskBelow = -1.2676506002282294e30f;  // -2^100
+constexpr float kMinScale = 5.9604645e-8f;             // 2^-24
+constexpr int64_t kMaxSeqlen = int64_t{1} << 29;       // places fit 32 bits
+constexpr int kSumSplits = 64;
+
+struct BucketMap {
+  int intervals;
+  int bounds[kMaxIntervals - 1];
+  uint8_t bucket[kMaxIntervals];
+};
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// One thread per distance: its interval by binary search, then the bias of
+// heads blockIdx.y, blockIdx.y + gridDim.y, ...; consecutive threads write
+// consecutive words.
+__global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ BucketMap m,
+                                                          const __nv_bfloat16* __restrict__ table, int hq, int64_t len,
+                                                          int off, float inv_scale, float* __restrict__ lut,
+                                                          uint8_t* __restrict__ interval) {
+  __shared__ int bounds[kMaxIntervals];
+  __shared__ uint8_t bucket[kMaxIntervals];
+  for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
+    bounds[i] = i + 1 < m.intervals ? m.bounds[i] : 0x7fffffff;
+    bucket[i] = m.bucket[i];
+  }
+  __syncthreads();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= len) return;
+  const int n = static_cast<int>(i) - off;
+  int lo = 0, hi = m.intervals - 1;  // the number of bounds <= n
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (bounds[mid] <= n)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  if (blockIdx.y == 0) interval[i] = static_cast<uint8_t>(lo);
+  const __nv_bfloat16* row = table + static_cast<int64_t>(bucket[lo]) * hq;
+  for (int h = blockIdx.y; h < hq; h += gridDim.y) {
+    const float v = __bfloat162float(row[h]);
+    lut[h * len + i] = v <= kMaskBelow ? -INFINITY : v * inv_scale;
+  }
+}
+
+// Sum of the backward's parts over warps, key tiles and sequences, in a fixed
+// order: block (kv head, split) adds its share of the (sequence, key tile)
+// pairs, 16 warps' numbers in 32 bits and those sums in 64.
+__global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const float* __restrict__ part, int64_t pairs, int nkt,
+                                                             int hkv, int width, double* __restrict__ sums) {
+  const int kvh = blockIdx.x;
+  const int64_t j0 = pairs * blockIdx.y / gridDim.y, j1 = pairs * (blockIdx.y + 1) / gridDim.y;
+  for (int e = threadIdx.x; e < width; e += kThreads) {
+    double acc = 0.0;
+    for (int64_t j = j0; j < j1; ++j) {
+      const int64_t b = j / nkt;
+      const float* p = part + ((b * hkv + kvh) * nkt + (j - b * nkt)) * kBwdComputeWarps * width + e;
+      float s[4] = {};
+#pragma unroll
+      for (int w = 0; w < kBwdComputeWarps; ++w) s[w & 3] += __ldg(p + static_cast<int64_t>(w) * width);
+      acc += static_cast<double>((s[0] + s[1]) + (s[2] + s[3]));
+    }
+    sums[(static_cast<int64_t>(blockIdx.y) * hkv + kvh) * width + e] = acc;
+  }
+}
+
+// One block per head: the splits' sums by interval, then the intervals of every bucket.
+__global__ void __launch_bounds__(kThreads) dbias_out_kernel(const __grid_constant__ BucketMap m,
+                                                             const double* __restrict__ sums, int splits, int hq,
+                                                             int buckets, __nv_bfloat16* __restrict__ dtable) {
+  __shared__ double by_interval[kMaxIntervals];
+  const int h = blockIdx.x;
+  for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
+    double s = 0.0;
+    for (int sp = 0; sp < splits; ++sp) s += sums[(static_cast<int64_t>(sp) * hq + h) * m.intervals + i];
+    by_interval[i] = s;
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < buckets; t += kThreads) {
+    double s = 0.0;
+    for (int i = 0; i < m.intervals; ++i)
+      if (m.bucket[i] == t) s += by_interval[i];
+    dtable[static_cast<int64_t>(t) * hq + h] = __float2bfloat16_rn(static_cast<float>(s));
+  }
+}
+
+int check_bias(const loong_attn_desc* d, const loong_rel_bias* b) {
+  int st = loong_attn_check(d);
+  if (st != LOONG_OK) return st;
+  if (!b) return LOONG_ERR_INVALID_ARG;
+  if (b->num_buckets < 1 || b->num_buckets > kMaxBuckets || b->num_bounds < 0 || b->num_bounds >= kMaxIntervals)
+    return LOONG_ERR_INVALID_ARG;
+  if (b->num_bounds > 0 && !b->bounds) return LOONG_ERR_INVALID_ARG;
+  for (int i = 1; i < b->num_bounds; ++i)
+    if (b->bounds[i] <= b->bounds[i - 1]) return LOONG_ERR_INVALID_ARG;
+  for (int i = 0; i <= b->num_bounds; ++i) {
+    const int t = b->bucket_of ? b->bucket_of[i] : i;
+    if (t < 0 || t >= b->num_buckets) return LOONG_ERR_INVALID_ARG;
+  }
+  if (d->seqlen > kMaxSeqlen) return LOONG_ERR_UNSUPPORTED;
+  if (d->softmax_scale > 0.f && d->softmax_scale < kMinScale) return LOONG_ERR_UNSUPPORTED;
+  return LOONG_OK;
+}
+
+BucketMap bucket_map(const loong_rel_bias& b) {
+  BucketMap m{};
+  m.intervals = b.num_bounds + 1;
+  for (int i = 0; i < b.num_bounds; ++i) m.bounds[i] = b.bounds[i];
+  for (int i = 0; i < m.intervals; ++i) m.bucket[i] = static_cast<uint8_t>(b.bucket_of ? b.bucket_of[i] : i);
+  return m;
+}
+
+// The workspace: the plain pass's first, then the bias by distance and, for the
+// backward, the gradient's parts and their sums.
+struct BiasWs {
+  size_t lut, interval, part, sums, total;
+  size_t part_bytes;
+  int off;
+  int64_t len;
+};
+
+BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
+  BiasWs w{};
+  // a tile's distances reach 127 past the first and the last token's
+  w.off = static_cast<int>(d.causal ? 128 : d.seqlen + 128);
+  w.len = w.off + d.seqlen + 128;
+  size_t at = up256(loong_attn_workspace_size(&d, pass));
+  w.lut = at;
+  at += up256(static_cast<size_t>(d.hq) * w.len * 4);
+  w.interval = at;
+  at += up256(static_cast<size_t>(w.len));
+  if (pass == 1) {
+    const size_t width = static_cast<size_t>(d.hq / d.hkv) * (b.num_bounds + 1);
+    w.part = at;
+    w.part_bytes = static_cast<size_t>(bwd_blocks(d)) * kBwdComputeWarps * width * 4;
+    at += up256(w.part_bytes);
+    w.sums = at;
+    at += up256(static_cast<size_t>(kSumSplits) * d.hkv * width * 8);
+  }
+  w.total = at;
+  return w;
+}
+
+int expand(const loong_attn_desc& d, const loong_rel_bias& b, const BucketMap& m, const BiasWs& w, void* ws,
+           BiasView* view, cudaStream_t stream) {
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  float* lut = reinterpret_cast<float*>(base + w.lut);
+  uint8_t* interval = base + w.interval;
+  const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.head_dim));
+  const int64_t nb = (w.len + kThreads - 1) / kThreads;
+  // short sequences spread the heads over blocks as well
+  const unsigned ny = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(d.hq, 608 / nb)));
+  expand_kernel<<<dim3(static_cast<unsigned>(nb), ny), kThreads, 0, stream>>>(
+      m, static_cast<const __nv_bfloat16*>(b.table), d.hq, w.len, w.off, 1.0f / scale, lut, interval);
+  view->lut = lut;
+  view->interval = interval;
+  view->len = w.len;
+  view->off = w.off;
+  view->intervals = m.intervals;
+  return check_launch();
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+}  // namespace loong
+
+using namespace loong;
+
+extern "C" {
+
+int loong_rel_bias_check(const loong_attn_desc* d, const loong_rel_bias* bias) { return check_bias(d, bias); }
+
+size_t loong_attn_bias_workspace_size(const loong_attn_desc* d, const loong_rel_bias* bias, int pass) {
+  if (check_bias(d, bias) != LOONG_OK || (pass != 0 && pass != 1)) return 0;
+  return bias_ws(*d, *bias, pass).total;
+}
+
+int loong_attn_bias_fwd(const loong_attn_desc* d, const loong_rel_bias* bias, const void* q, const void* k,
+                        const void* v, void* o, float* lse, void* o_res, void* ws, size_t ws_bytes,
+                        loong_stream_t stream_) {
+  NvtxRange range("loong_attn_bias_fwd");
+  int st = check_bias(d, bias);
+  if (st != LOONG_OK) return st;
+  const void* ptrs[] = {q, k, v, o, lse};
+  for (const void* p : ptrs)
+    if (!p || !aligned(p, 16)) return LOONG_ERR_INVALID_ARG;
+  if (!aligned(o_res, 16) || !bias->table || !aligned(bias->table, 2)) return LOONG_ERR_INVALID_ARG;
+  const BiasWs w = bias_ws(*d, *bias, 0);
+  if (!ws || ws_bytes < w.total || !aligned(ws, 16)) return LOONG_ERR_WORKSPACE;
+  if ((st = device_ready()) != LOONG_OK) return st;
+  for (const void* p : ptrs)
+    if (!on_device(p)) return LOONG_ERR_INVALID_ARG;
+  if (!on_device(ws) || !on_device(bias->table) || (o_res && !on_device(o_res))) return LOONG_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  BiasView view;
+  if ((st = expand(*d, *bias, bucket_map(*bias), w, ws, &view, stream)) != LOONG_OK) return st;
+  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, &view);
+}
+
+int loong_attn_bias_bwd(const loong_attn_desc* d, const loong_rel_bias* bias, const void* q, const void* k,
+                        const void* v, const void* o, const void* o_res, const float* lse, const void* dout, void* dq,
+                        void* dk, void* dv, void* dtable, void* ws, size_t ws_bytes, loong_stream_t stream_) {
+  NvtxRange range("loong_attn_bias_bwd");
+  int st = check_bias(d, bias);
+  if (st != LOONG_OK) return st;
+  const void* ptrs[] = {q, k, v, o, lse, dout, dq, dk, dv};
+  for (const void* p : ptrs)
+    if (!p || !aligned(p, 16)) return LOONG_ERR_INVALID_ARG;
+  const void* tables[] = {bias->table, dtable};
+  for (const void* p : tables)
+    if (!p || !aligned(p, 2)) return LOONG_ERR_INVALID_ARG;
+  if (!aligned(o_res, 16)) return LOONG_ERR_INVALID_ARG;
+  const BiasWs w = bias_ws(*d, *bias, 1);
+  if (!ws || ws_bytes < w.total || !aligned(ws, 16)) return LOONG_ERR_WORKSPACE;
+  if ((st = device_ready()) != LOONG_OK) return st;
+  for (const void* p : ptrs)
+    if (!on_device(p)) return LOONG_ERR_INVALID_ARG;
+  for (const void* p : tables)
+    if (!on_device(p)) return LOONG_ERR_INVALID_ARG;
+  if (!on_device(ws) || (o_res && !on_device(o_res))) return LOONG_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  float* part = reinterpret_cast<float*>(base + w.part);
+  double* sums = reinterpret_cast<double*>(base + w.sums);
+  const BucketMap m = bucket_map(*bias);
+  BiasView view;
+  if ((st = expand(*d, *bias, m, w, ws, &view, stream)) != LOONG_OK) return st;
+  cudaError_t e = cudaMemsetAsync(part, 0, w.part_bytes, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if ((st = run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, &view, part)) != LOONG_OK) return st;
+  const RingGeom g = ring_geom(*d);
+  const int nkt = g.nblocks * g.ntile;
+  const int64_t pairs = d->batch * nkt;
+  const int splits = static_cast<int>(std::min<int64_t>(kSumSplits, pairs));
+  const int width = d->hq / d->hkv * m.intervals;
+  dbias_sum_kernel<<<dim3(static_cast<unsigned>(d->hkv), static_cast<unsigned>(splits)), kThreads, 0, stream>>>(
+      part, pairs, nkt, d->hkv, width, sums);
+  if ((st = check_launch()) != LOONG_OK) return st;
+  dbias_out_kernel<<<static_cast<unsigned>(d->hq), kThreads, 0, stream>>>(m, sums, splits, d->hq, bias->num_buckets,
+                                                                          static_cast<__nv_bfloat16*>(dtable));
+  return check_launch();
+}
+
+}  // extern "C"

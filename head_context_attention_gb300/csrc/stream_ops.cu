@@ -456,7 +456,9 @@ __global__ void __launch_bounds__(256) bwd_rowstats_kernel(
       const int64_t pos = bh * stat_len + static_cast<int64_t>(blk_i) * blk_pad + (si - blk_i * blk);
       if (in_bounds(pos >= 0 && pos < (bh + 1) * stat_len, err)) {
         dstat[pos] = acc;
-        lse2[pos] = lse[bh * S + s] * kLog2e;
+        // a row that a bias of -inf left nothing: its P must come out 0
+        const float l = lse[bh * S + s];
+        lse2[pos] = l == -INFINITY ? INFINITY : l * kLog2e;
       }
     }
   }

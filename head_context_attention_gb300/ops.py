@@ -32,6 +32,7 @@ EXPORTS = ("loong_version", "loong_status_string", "loong_last_cuda_error", "loo
            "loong_attn_workspace_size", "loong_ring_schedule", "loong_attn_fwd", "loong_attn_fwd_ranks",
            "loong_attn_bwd",
            "loong_attn_bwd_noalloc", "loong_lse_merge", "loong_headctx_pack", "loong_headctx_pack_n",
+           "loong_rel_bias_check", "loong_attn_bias_workspace_size", "loong_attn_bias_fwd", "loong_attn_bias_bwd",
            "loong_qk_norm_rope_fwd", "loong_qk_norm_rope_bwd_workspace_size", "loong_qk_norm_rope_bwd",
            "loong_attn_2d_host_workspace_size", "loong_attn_2d_host", "loong_host_alloc", "loong_host_free",
            "loong_set_timing_events", "loong_get_device_status", "loong_selftest_wait_timeout")
@@ -45,6 +46,12 @@ class LoongAttnDesc(ctypes.Structure):
                 ("ring_inner", ctypes.c_int32), ("ring_outer", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("placement", ctypes.c_int32), ("mode", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float), ("layout", ctypes.c_int32)]
+
+
+class LoongRelBias(ctypes.Structure):
+    _fields_ = [("num_buckets", ctypes.c_int32), ("num_bounds", ctypes.c_int32),
+                ("bounds", ctypes.POINTER(ctypes.c_int32)), ("bucket_of", ctypes.POINTER(ctypes.c_int32)),
+                ("table", ctypes.c_void_p)]
 
 
 class LoongQkOpts(ctypes.Structure):
@@ -95,7 +102,12 @@ def lib():
                                          P, P, P]
         L.loong_headctx_pack_n.argtypes = [I32, I64, I32, I32, I64, ctypes.POINTER(ctypes.c_int32), I32,
                                            ctypes.c_int, ctypes.c_int, ctypes.POINTER(P), ctypes.POINTER(P), P]
-        QO = ctypes.POINTER(LoongQkOpts)
+        RB, QO = ctypes.POINTER(LoongRelBias), ctypes.POINTER(LoongQkOpts)
+        L.loong_rel_bias_check.argtypes = [D, RB]
+        L.loong_attn_bias_workspace_size.restype = SZ
+        L.loong_attn_bias_workspace_size.argtypes = [D, RB, ctypes.c_int]
+        L.loong_attn_bias_fwd.argtypes = [D, RB, P, P, P, P, P, P, P, SZ, P]
+        L.loong_attn_bias_bwd.argtypes = [D, RB, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         L.loong_qk_norm_rope_fwd.argtypes = [D, QO, P, P, P, P, P, P, P, P, P, P]
         L.loong_qk_norm_rope_bwd_workspace_size.restype = SZ
         L.loong_qk_norm_rope_bwd_workspace_size.argtypes = [D, QO]
@@ -199,6 +211,89 @@ def loong_headctx_pack_n(xs, outs, batch, cp, P, s_local, heads, d, direction, g
     ous = (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
     return _check("loong_headctx_pack_n", lib().loong_headctx_pack_n(
         n, batch, cp, P, s_local, hs, d, direction, gather, ins, ous, _stream(stream)))
+
+
+class RelBuckets:
+    """Buckets of the distance query - key: distance n lies in interval number
+    #{bounds <= n}, interval i belongs to bucket ``bucket_of[i]`` (None: bucket
+    i).  Keeps the host arrays that loong_rel_bias points at."""
+
+    def __init__(self, num_buckets, bounds, bucket_of=None):
+        bounds = [int(x) for x in bounds]
+        if any(not -2 ** 31 <= x < 2 ** 31 for x in bounds):
+            raise ValueError("bounds must fit 32 bits")
+        self.num_buckets, self.num_bounds = int(num_buckets), len(bounds)
+        self._bounds = (ctypes.c_int32 * max(1, len(bounds)))(*bounds)
+        self._bucket_of = None
+        if bucket_of is not None:
+            if len(bucket_of) != len(bounds) + 1:
+                raise ValueError("bucket_of needs one bucket for each of the len(bounds) + 1 intervals")
+            self._bucket_of = (ctypes.c_int32 * len(bucket_of))(*[int(x) for x in bucket_of])
+
+    @property
+    def bounds(self):
+        return list(self._bounds)[:self.num_bounds]
+
+    @property
+    def bucket_of(self):
+        return list(range(self.num_bounds + 1)) if self._bucket_of is None else list(self._bucket_of)
+
+    def struct(self, table=None):
+        p32 = ctypes.POINTER(ctypes.c_int32)
+        return LoongRelBias(self.num_buckets, self.num_bounds, ctypes.cast(self._bounds, p32),
+                            None if self._bucket_of is None else ctypes.cast(self._bucket_of, p32),
+                            None if table is None else table.data_ptr())
+
+
+def log_buckets(num_buckets, max_distance, causal=True):
+    """Buckets whose width grows with the distance: of a direction's n buckets
+    the first e = n // 2 hold the distances 0 .. e - 1 one by one, bucket e + t
+    starts at the first distance x with x / e >= (max_distance / e)^(t / (n - e)),
+    and the last one has every distance from its start on.  Formed in whole
+    numbers.  causal: all num_buckets for distances >= 0; else the first half
+    for those and the second half, by |distance|, for negative ones (its first
+    bucket stays empty).  Where two buckets would start at one distance the later
+    one has it."""
+    n = num_buckets if causal else num_buckets // 2
+    if num_buckets < 2 or (not causal and num_buckets % 2) or n < 2:
+        raise ValueError("need at least 2 buckets for each direction, and an even number of them when not causal")
+    e = n // 2
+    if max_distance <= e:
+        raise ValueError(f"max_distance must be above {e}, the distances with a bucket of their own")
+    first = {x: x for x in range(1, e + 1)}    # first distance -> bucket
+    x = e
+    for t in range(1, n - e):
+        while x ** (n - e) * e ** t < max_distance ** t * e ** (n - e):
+            # far below the bound: jump near it, then step
+            near = int(e * (max_distance / e) ** (t / (n - e))) - 2
+            x = max(x + 1, min(near, max_distance))
+        first[x] = e + t
+    starts = sorted(first)
+    bounds, of = list(starts), [0] + [first[s] for s in starts]
+    if not causal:
+        bounds = [1 - s for s in reversed(starts)] + bounds
+        of = [n + first[s] for s in reversed(starts)] + of
+    return RelBuckets(num_buckets, bounds, of)
+
+
+def loong_rel_bias_check(desc, bias):
+    return lib().loong_rel_bias_check(ctypes.byref(desc), ctypes.byref(bias))
+
+
+def loong_attn_bias_workspace_size(desc, bias, pass_):
+    return lib().loong_attn_bias_workspace_size(ctypes.byref(desc), ctypes.byref(bias), pass_)
+
+
+def loong_attn_bias_fwd(desc, bias, q, k, v, o, lse, o_res, ws, stream=None):
+    return _check("loong_attn_bias_fwd", lib().loong_attn_bias_fwd(
+        ctypes.byref(desc), ctypes.byref(bias), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(o_res), _ptr(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def loong_attn_bias_bwd(desc, bias, q, k, v, o, o_res, lse, dout, dq, dk, dv, dtable, ws, stream=None):
+    return _check("loong_attn_bias_bwd", lib().loong_attn_bias_bwd(
+        ctypes.byref(desc), ctypes.byref(bias), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse),
+        _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dtable), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def loong_qk_norm_rope_fwd(desc, opts, q, k, v, wq, wk, positions, q_out, k_out, v_out, stream=None):
@@ -368,6 +463,47 @@ def _on(device, stream):
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not {device}")
     return torch.cuda.device(device), torch.cuda.current_stream(device) if stream is None else stream
+
+
+def _bias_problem(w, table, buckets, mode, layout):
+    desc, bias = make_desc(w, mode, layout=layout), buckets.struct(table)
+    _check("loong_rel_bias_check", loong_rel_bias_check(desc, bias))
+    _contiguous("table", table, (buckets.num_buckets, w.hq), torch.bfloat16, table.device)
+    return desc, bias
+
+
+def attn_bias_fwd(w, q, k, v, table, buckets, mode=MODE_FUSED, stream=None, layout=LAYOUT_NATURAL, res=True):
+    """attn_fwd with a learned relative position bias: ``table`` bf16
+    [num_buckets, hq], ``buckets`` a RelBuckets (log_buckets makes the usual
+    ones).  Returns (o, lse, o_res); o_res is None when ``res`` is false."""
+    desc, bias = _bias_problem(w, table, buckets, mode, layout)
+    for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv)):
+        _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, table.device)
+    device, stream = _on(table.device, stream)
+    with device, torch.cuda.stream(stream):
+        o = torch.empty_like(q)
+        o_res = torch.empty_like(q) if res else None
+        lse = torch.empty((w.batch, w.hq, w.seqlen), dtype=torch.float32, device=q.device)
+        ws = torch.empty(loong_attn_bias_workspace_size(desc, bias, 0), dtype=torch.uint8, device=q.device)
+        loong_attn_bias_fwd(desc, bias, q, k, v, o, lse, o_res, ws, stream)
+    return o, lse, o_res
+
+
+def attn_bias_bwd(w, q, k, v, o, lse, do, table, buckets, o_res=None, mode=MODE_FUSED, stream=None,
+                  layout=LAYOUT_NATURAL):
+    """Gradient of attn_bias_fwd: (dq, dk, dv, dtable), dtable bf16 like the table."""
+    desc, bias = _bias_problem(w, table, buckets, mode, layout)
+    for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv), ("o", o, w.hq), ("do", do, w.hq),
+                    ("o_res", o_res, w.hq)):
+        if t is not None or n != "o_res":
+            _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, table.device)
+    _contiguous("lse", lse, (w.batch, w.hq, w.seqlen), torch.float32, table.device)
+    device, stream = _on(table.device, stream)
+    with device, torch.cuda.stream(stream):
+        dq, dk, dv, dtable = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(table)
+        ws = torch.empty(loong_attn_bias_workspace_size(desc, bias, 1), dtype=torch.uint8, device=q.device)
+        loong_attn_bias_bwd(desc, bias, q, k, v, o, o_res, lse, do, dq, dk, dv, dtable, ws, stream)
+    return dq, dk, dv, dtable
 
 
 class QkOpts:

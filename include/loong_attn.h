@@ -320,6 +320,76 @@ LOONG_API int loong_headctx_pack_n(int32_t n, int64_t batch, int32_t cp, int32_t
                                    const void* const* in, void* const* out, loong_stream_t stream);
 
 /*
+ * Ring attention with a learned relative position bias in buckets: the logit
+ * of query i and key j is softmax_scale * q_i.k_j + table[bucket(i - j)][head],
+ * with i, j natural token positions.  The paper's attention has no bias; a
+ * layer that learns its positions this way needs it inside the attention,
+ * whose scores never reach memory.
+ *   num_buckets  rows of the table, 1 .. 256.
+ *   num_bounds   0 .. 255; the distances -inf .. inf are cut into num_bounds + 1
+ *                intervals.
+ *   bounds       HOST array of num_bounds strictly increasing distances: n lies
+ *                in interval number #{bounds <= n}.  Causal descriptors only
+ *                meet n >= 0, others both signs.
+ *   bucket_of    HOST array of num_bounds + 1 buckets, one per interval
+ *                (several intervals may share one), or NULL: interval i is
+ *                bucket i.
+ *   table        DEVICE bf16 [num_buckets][hq], 2-byte aligned.  A value of
+ *                -2^100 or less (the type's lowest and -inf included) masks: its
+ *                keys get no weight.  A query that this leaves no key gets O = 0
+ *                and LSE = -inf, and adds nothing to any gradient.  Masked keys
+ *                are still read and multiplied.
+ * The two host arrays are read during the call only.
+ */
+typedef struct {
+  int32_t num_buckets, num_bounds;
+  const int32_t* bounds;
+  const int32_t* bucket_of;
+  const void* table;
+} loong_rel_bias;
+
+/*
+ * Check a descriptor and a bias without touching the GPU (the table pointer is
+ * not looked at): as loong_attn_check, and LOONG_ERR_INVALID_ARG for a bias
+ * out of the ranges above, LOONG_ERR_UNSUPPORTED for seqlen > 2^29 or a
+ * softmax_scale in (0, 2^-24).
+ */
+LOONG_API int loong_rel_bias_check(const loong_attn_desc* desc, const loong_rel_bias* bias);
+
+/*
+ * Device workspace, in bytes, of loong_attn_bias_fwd (pass 0) or
+ * loong_attn_bias_bwd (pass 1); 0 for invalid arguments.  Host-only.
+ * loong_attn_workspace_size's, then the bias of every distance (fp32,
+ * hq * (S + 256) values, hq * (2 S + 256) non-causal) and its interval (bytes),
+ * and for the backward the gradient's parts: 16 * (hq/hkv) * (num_bounds + 1)
+ * fp32 for every (sequence, kv head, 128-key tile), and 64 sums of them.
+ */
+LOONG_API size_t loong_attn_bias_workspace_size(const loong_attn_desc* desc, const loong_rel_bias* bias, int pass);
+
+/*
+ * loong_attn_fwd with the bias: same arguments, layouts, modes and accuracy.
+ * ws needs loong_attn_bias_workspace_size(desc, bias, 0) bytes.
+ */
+LOONG_API int loong_attn_bias_fwd(const loong_attn_desc* desc, const loong_rel_bias* bias, const void* q,
+                                  const void* k, const void* v, void* o, float* lse, void* o_res, void* ws,
+                                  size_t ws_bytes, loong_stream_t stream);
+
+/*
+ * loong_attn_bwd with the bias, and the gradient of the table:
+ *   dtable  bf16 [num_buckets][hq], written: the sum of dS (see loong_attn_bwd)
+ *           over every pair of the bucket, summed in fp32 and fp64 and rounded
+ *           once; 0 for a bucket no pair falls in.  Its order of summation is
+ *           fixed.  D carries the accuracy of o and o_res into it; without
+ *           o_res it is as exact as bf16 O.
+ * o, o_res and lse are loong_attn_bias_fwd's for the same bias.  ws needs
+ * loong_attn_bias_workspace_size(desc, bias, 1) bytes.
+ */
+LOONG_API int loong_attn_bias_bwd(const loong_attn_desc* desc, const loong_rel_bias* bias, const void* q,
+                                  const void* k, const void* v, const void* o, const void* o_res, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, void* dtable, void* ws,
+                                  size_t ws_bytes, loong_stream_t stream);
+
+/*
  * What loong_qk_norm_rope_fwd does to Q and K.
  *   q/k/v_stride, elements from one token to the next of the projections q, k, v
  *   dq/dk/dv_stride  and of their gradients, so that either can be slices of

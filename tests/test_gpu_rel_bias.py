@@ -1,0 +1,279 @@
+"""Ring attention with a bucketed relative bias, and its gradients, against the
+float64 oracle.
+
+Tolerances, per element, from what rounds on the way (half steps: bf16 2^-8 of
+the value, fp16 2^-11, fp32 2^-24):
+  * a logit x: products of bf16 are exact, their sum and the bias add take at
+    most d + 4 fp32 roundings of at most L = scale |q| |k|max + |bias|max:
+    dx = (d + 4) 2^-24 L; the exponential and its argument 2^-21 + 2^-23 L more:
+    every P is off by at most a factor 1 + e, e = 2 (dx + 2^-21 + 2^-23 L).
+  * O: P rounded to fp16, sums in fp32, O to bf16: 2^-8 |O| + (2^-11 + e + 2^-16) A,
+    A = P |V|; LSE: e + 2^-22 |LSE|.
+  * the backward's P and dS are rounded to bf16, D comes from O and its residual
+    (P to fp16: 2^-11 of A, then 2^-16): dS is off by at most
+    f = 2^-8 + 2^-11 + 2 e + 2^-14 of a = P (|dO| |V| + |dO| A), so dQ, dK, dV by f
+    times the same sums over absolute values, plus 2^-8 of themselves.
+  * dtable does not use the rounded dS: (2^-11 + 2 e + 2^-14) of the sum of a,
+    plus 2^-8 of itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+from head_context_attention_gb300 import inputs, ops
+from oracle import bias as obias
+from tests.helpers import to64
+
+pytestmark = pytest.mark.gpu
+
+LOG = "log"   # log_buckets(num, max_distance)
+# S, hq, hkv, d, hp, cp, inner, zigzag, batch, causal, buckets, table
+CASES = {
+    "one-token": (1, 2, 1, 64, 1, 1, 1, 0, 1, 1, (LOG, 8, 20), None),
+    "two-tokens": (2, 2, 2, 128, 1, 1, 1, 1, 3, 1, (LOG, 8, 20), None),
+    "three-keys": (3, 2, 1, 64, 1, 3, 3, 0, 1, 0, (LOG, 8, 20), None),
+    "under-a-tile": (100, 4, 2, 64, 1, 1, 1, 0, 1, 1, (LOG, 32, 128), None),
+    "tile-and-one": (129, 3, 1, 128, 1, 1, 1, 0, 1, 1, (LOG, 32, 128), None),
+    "gqa": (512, 4, 2, 64, 2, 4, 2, 1, 1, 1, (LOG, 32, 128), None),
+    "ragged-blocks": (600, 2, 1, 128, 1, 3, 3, 1, 1, 1, (LOG, 16, 300), None),
+    "not-causal": (398, 2, 2, 64, 1, 2, 2, 0, 2, 0, (LOG, 32, 128), None),
+    "not-causal-d128": (256, 3, 1, 128, 1, 2, 1, 1, 1, 0, (LOG, 16, 60), None),
+    "group-of-34": (150, 34, 1, 64, 1, 1, 1, 0, 1, 1, (LOG, 32, 128), None),
+    "far-boundaries": (900, 2, 1, 64, 1, 1, 1, 0, 1, 1, (4, [127, 128, 500]), None),
+    "tile-boundaries": (640, 2, 1, 128, 1, 1, 1, 0, 1, 1, (5, [128, 256, 384, 512]), None),
+    "shared-buckets": (300, 2, 1, 64, 1, 1, 1, 0, 1, 0, (3, [-200, -1, 0, 1, 200], [0, 1, 2, 2, 1, 0]), None),
+    "one-bucket": (400, 2, 1, 64, 1, 1, 1, 0, 1, 1, (1, []), None),
+    "beyond-all": (300, 2, 1, 64, 1, 1, 1, 0, 1, 1, (3, [-1000, 5000]), None),
+    "256-buckets": (520, 2, 2, 128, 1, 1, 1, 0, 1, 1, (256, list(range(1, 256))), None),
+    "window": (700, 2, 1, 64, 1, 1, 1, 0, 1, 1, (LOG, 32, 128), "window"),
+    "window-d128": (700, 2, 1, 128, 1, 1, 1, 0, 1, 1, (3, [150, 400]), "window"),
+    "empty-rows": (300, 2, 1, 64, 1, 1, 1, 0, 1, 1, (4, [20, 40, 200]), "no-near"),
+    "empty-rows-ring": (384, 2, 1, 128, 1, 3, 3, 1, 1, 1, (4, [20, 140, 200]), "no-near"),
+    "lowest": (300, 2, 1, 64, 1, 1, 1, 0, 1, 0, (4, [-20, 1, 130]), "lowest"),
+    "nothing": (140, 2, 1, 64, 1, 1, 1, 0, 1, 1, (1, []), "no-near"),
+    "large-bias": (400, 2, 1, 64, 1, 1, 1, 0, 1, 1, (LOG, 16, 300), "large"),
+}
+
+
+def _make(name, seed=0):
+    S, hq, hkv, d, hp, cp, inner, zz, B, causal, bk, how = CASES[name]
+    w = inputs.Workload(name, S, hq, hkv, d, hp, cp, inner, cp // inner, True, placement=zz, batch=B,
+                        causal=bool(causal))
+    if bk[0] == LOG:
+        buckets = ops.log_buckets(bk[1], bk[2], causal=bool(causal))
+    else:
+        buckets = ops.RelBuckets(*bk)
+    x = inputs.make_inputs(w, device="cuda", seed_offset=seed)
+    g = torch.Generator(device="cuda").manual_seed(100 + seed)
+    t = torch.randn((buckets.num_buckets, hq), generator=g, device="cuda")
+    if how == "large":
+        t *= 20
+    t = t.to(torch.bfloat16)
+    if how == "window":
+        t[-1] = -torch.inf
+    if how == "no-near":
+        t[0] = -torch.inf
+    if how == "lowest":
+        t[1, 0], t[2, 1] = torch.finfo(torch.bfloat16).min, -2.0 ** 100
+    return w, x, t, buckets
+
+
+def _pack(w, x):
+    return {n: ops.headctx_pack(t, w.cp, w.hp, 1 if w.placement else 2) for n, t in x.items()}
+
+
+def _unpack(w, t):
+    return ops.headctx_unpack(t, w.batch, w.cp, w.hp, 1 if w.placement else 2)
+
+
+def _run(w, x, t, buckets, mode=ops.MODE_FUSED, layout=ops.LAYOUT_NATURAL, res=True):
+    o, lse, o_res = ops.attn_bias_fwd(w, x["q"], x["k"], x["v"], t, buckets, mode=mode, layout=layout, res=res)
+    grads = ops.attn_bias_bwd(w, x["q"], x["k"], x["v"], o, lse, x["do"], t, buckets, o_res=o_res, mode=mode,
+                              layout=layout)
+    assert ops.loong_get_device_status() == ops.LOONG_OK
+    return (o, lse) + grads
+
+
+def _within(name, got, want, tol):
+    got = to64(got)
+    assert got.shape == want.shape, name
+    same_inf = np.isneginf(got) & np.isneginf(want)
+    assert np.all(np.isfinite(got) | same_inf), f"{name}: non-finite"
+    err = np.where(same_inf, 0, np.abs(np.where(same_inf, 0, got) - np.where(same_inf, 0, want)))
+    assert np.all(err <= tol), (f"{name}: {(err > tol).sum()} of {err.size} outside; worst "
+                                f"{np.max(err / np.maximum(tol, 1e-300)):.3g} of the tolerance")
+
+
+def _e(w, r):
+    """How far a probability may be off, relative (see the top)."""
+    L = r["logit"].max()
+    return 2 * ((w.head_dim + 4) * 2.0 ** -24 * L + 2.0 ** -21 + 2.0 ** -23 * L)
+
+
+def _check(w, x, t, buckets, out):
+    o, lse, dq, dk, dv, dt = out
+    scale = ops.default_scale(w.head_dim)
+    t64 = to64(t)
+    t64 = np.where(t64 <= -2.0 ** 100, -np.inf, t64)
+    want_dt, tol_dt = np.zeros(t64.shape), np.zeros(t64.shape)
+    for b in range(w.batch):
+        r = obias.forward_backward(to64(x["q"][b]), to64(x["k"][b]), to64(x["v"][b]), to64(x["do"][b]), t64,
+                                   buckets.bounds, buckets.bucket_of, scale, w.causal, terms=True)
+        e = _e(w, r)
+        _within("O", o[b], r["o"], 2.0 ** -8 * np.abs(r["o"]) + (2.0 ** -11 + e + 2.0 ** -16) * r["abs_o"])
+        some = np.isfinite(r["lse"])
+        _within("LSE", lse[b], r["lse"], np.where(some, e + 2.0 ** -22 * np.abs(np.where(some, r["lse"], 0)), 0))
+        f = 2.0 ** -8 + 2.0 ** -11 + 2 * e + 2.0 ** -14
+        for nm, got in (("dq", dq), ("dk", dk), ("dv", dv)):
+            _within(nm, got[b], r[nm], 2.0 ** -8 * np.abs(r[nm]) + f * r["abs_" + nm])
+        want_dt += r["dtable"]
+        tol_dt += (2.0 ** -11 + 2 * e + 2.0 ** -14) * r["abs_dtable"]
+    _within("dtable", dt, want_dt, tol_dt + 2.0 ** -8 * np.abs(want_dt))
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_matches_oracle(cuda_device, name):
+    w, x, t, buckets = _make(name)
+    out = _run(w, x, t, buckets)
+    _check(w, x, t, buckets, out)
+    # the table's gradient in the same bits again
+    assert torch.equal(_run(w, x, t, buckets)[5].view(torch.int16), out[5].view(torch.int16))
+
+
+@pytest.mark.parametrize("name", ["gqa", "ragged-blocks", "not-causal", "not-causal-d128", "empty-rows-ring", "window"])
+def test_stepwise_matches_oracle(cuda_device, name):
+    w, x, t, buckets = _make(name)
+    _check(w, x, t, buckets, _run(w, x, t, buckets, mode=ops.MODE_STEPWISE))
+
+
+@pytest.mark.parametrize("mode", [ops.MODE_FUSED, ops.MODE_STEPWISE, ops.MODE_STEPWISE_COPY, ops.MODE_STEPWISE_COPY_AB])
+@pytest.mark.parametrize("name", ["gqa", "empty-rows-ring"])
+def test_ranks_layout(cuda_device, name, mode):
+    w, x, t, buckets = _make(name)
+    o, lse, dq, dk, dv, dt = _run(w, _pack(w, x), t, buckets, mode=mode, layout=ops.LAYOUT_RANK_MAJOR)
+    _check(w, x, t, buckets, (_unpack(w, o), lse, _unpack(w, dq), _unpack(w, dk), _unpack(w, dv), dt))
+
+
+def test_without_the_residual(cuda_device):
+    """D from bf16 O: 2^-8 instead of 2^-11 of A more in dS, and in dtable."""
+    w, x, t, buckets = _make("gqa")
+    o, lse, dq, dk, dv, dt = _run(w, x, t, buckets, res=False)
+    r = obias.forward_backward(to64(x["q"][0]), to64(x["k"][0]), to64(x["v"][0]), to64(x["do"][0]), to64(t),
+                               buckets.bounds, buckets.bucket_of, ops.default_scale(w.head_dim), True, terms=True)
+    _within("dtable", dt, r["dtable"], 2.0 ** -8 * np.abs(r["dtable"]) + 2.0 ** -7 * r["abs_dtable"])
+    _within("dq", dq[0], r["dq"], 2.0 ** -8 * np.abs(r["dq"]) + 2.0 ** -6 * r["abs_dq"])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_zero_table_is_the_plain_attention(cuda_device, d):
+    """A table of zeros leaves every output of the plain pass bit for bit, but dQ
+    (whose adds have no fixed order: two runs of the plain pass differ as well)."""
+    w = inputs.small(640, 4, 2, d, cp=2)
+    x = inputs.make_inputs(w, device="cuda")
+    t, buckets = torch.zeros((32, 4), device="cuda", dtype=torch.bfloat16), ops.log_buckets(32, 300)
+    o, lse, o_res = ops.attn_fwd(w, x["q"], x["k"], x["v"])
+    dq, dk, dv = ops.attn_bwd(w, x["q"], x["k"], x["v"], o, lse, x["do"], o_res=o_res)
+    got = _run(w, x, t, buckets)
+    for a, b in ((o, got[0]), (lse, got[1]), (dk, got[3]), (dv, got[4])):
+        assert torch.equal(a, b)
+    assert (dq.float() - got[2].float()).abs().max() <= 2.0 ** -7 * dq.float().abs().max()
+
+
+def test_softmax_scale_and_long_walk(cuda_device):
+    """A scale of its own, through the descriptor, at a length whose walks pass
+    every interval: against the oracle on one head."""
+    w = inputs.small(1500, 1, 1, 64, placement=0)
+    x = inputs.make_inputs(w, device="cuda")
+    buckets = ops.log_buckets(16, 1000)
+    t = torch.randn((16, 1), device="cuda").to(torch.bfloat16)
+    desc, bias = ops.make_desc(w, scale=0.3), buckets.struct(t)
+    o, o_res, lse = torch.empty_like(x["q"]), torch.empty_like(x["q"]), torch.empty((1, 1, 1500), device="cuda")
+    grads = [torch.empty_like(x[n]) for n in ("q", "k", "v")] + [torch.empty_like(t)]
+    ws = [torch.empty(ops.loong_attn_bias_workspace_size(desc, bias, p), dtype=torch.uint8, device="cuda")
+          for p in (0, 1)]
+    ops.loong_attn_bias_fwd(desc, bias, x["q"], x["k"], x["v"], o, lse, o_res, ws[0])
+    ops.loong_attn_bias_bwd(desc, bias, x["q"], x["k"], x["v"], o, o_res, lse, x["do"], *grads, ws[1])
+    r = obias.forward_backward(to64(x["q"][0]), to64(x["k"][0]), to64(x["v"][0]), to64(x["do"][0]), to64(t),
+                               buckets.bounds, buckets.bucket_of, 0.3, True, terms=True)
+    e = _e(w, r)
+    _within("O", o[0], r["o"], 2.0 ** -8 * np.abs(r["o"]) + (2.0 ** -11 + e + 2.0 ** -16) * r["abs_o"])
+    f = 2.0 ** -11 + 2 * e + 2.0 ** -14
+    for nm, got in zip(("dq", "dk", "dv"), grads):
+        _within(nm, got[0], r[nm], 2.0 ** -8 * np.abs(r[nm]) + (2.0 ** -8 + f) * r["abs_" + nm])
+    _within("dtable", grads[3], r["dtable"], 2.0 ** -8 * np.abs(r["dtable"]) + f * r["abs_dtable"])
+
+
+def test_run_of_the_positional_operators(cuda_device):
+    """A layer's attention as it is used: fused projection -> norm, rotation and
+    the ranks' layout -> biased attention -> back to the projection's gradient,
+    eagerly, on another stream, and captured and replayed on new inputs."""
+    w = inputs.Workload("layer", 768, 4, 2, 64, 2, 3, 3, 1, True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x = rn(1, 768, 8 * 64).to(torch.bfloat16)
+    do = ops.headctx_pack(rn(1, 768, 4, 64).to(torch.bfloat16), w.cp, w.hp)
+    wq, wk, t = 1 + 0.1 * rn(64), 1 + 0.1 * rn(64), rn(32, 4).to(torch.bfloat16)
+    buckets, opts, lay = ops.log_buckets(32, 500), ops.make_qk_opts(64, base=500000.0), ops.LAYOUT_RANK_MAJOR
+    split = lambda a: [u.unflatten(2, (-1, 64)) for u in a.split([256, 128, 128], dim=2)]
+
+    def layer():
+        dx = torch.empty_like(x)
+        q, k, v = ops.qk_norm_rope(w, opts, *split(x), wq=wq, wk=wk, layout=lay)
+        o, lse, res = ops.attn_bias_fwd(w, q, k, v, t, buckets, layout=lay)
+        dq, dk, dv, dt = ops.attn_bias_bwd(w, q, k, v, o, lse, do, t, buckets, o_res=res, layout=lay)
+        sq, sk, _ = split(x)
+        _, _, _, dwq, dwk = ops.qk_norm_rope_bwd(w, opts, sq, sk, dq, dk, dv, wq=wq, wk=wk, layout=lay, into=split(dx))
+        return o, lse, dt, dwk, dx, dwq
+
+    def same(a, b):
+        assert all(torch.equal(u, v) for u, v in zip(a[:4], b[:4]))
+        for u, v in zip(a[4:], b[4:]):    # through dQ, whose fp32 adds have no fixed order before its bf16 rounding
+            assert (u.float() - v.float()).abs().max() <= 2.0 ** -6 * v.float().abs().max()
+    want = layer()
+    # against the same layer in float64 torch, by its own differentiation
+    from oracle import qk as oqk
+    x64, ws64, t64 = x.double().requires_grad_(), [wq.double().requires_grad_(), wk.double().requires_grad_()], \
+        t.double().requires_grad_()
+    m = torch.from_numpy(oqk.matrices(range(768), 64, 64, oqk.frequencies(64, 500000.0), False, 1.0)).cuda()
+    q, k, v = split(x64)
+    q, k = (torch.einsum("tab,nthb->ntha", m, u * (u.square().mean(-1, keepdim=True) + 1e-6).rsqrt() * wt)
+            for u, wt in ((q, ws64[0]), (k, ws64[1])))
+    n = torch.arange(768, device="cuda")[:, None] - torch.arange(768, device="cuda")
+    ids = torch.from_numpy(obias.buckets_of_distance(n.cpu().numpy(), buckets.bounds, buckets.bucket_of)).cuda()
+    logits = torch.einsum("nihd,njhd->nhij", q, k.repeat_interleave(2, 2)) / 8 + t64[ids].permute(2, 0, 1)
+    p = logits.masked_fill(n < 0, -torch.inf).softmax(-1)
+    o = torch.einsum("nhij,njhd->nihd", p, v.repeat_interleave(2, 2))
+    grads = torch.autograd.grad(o, [x64, t64] + ws64, _unpack(w, do).double())
+    # relative 2-norms: roundings to bf16 of Q, K, P, dS and the gradient (O: Q, K and O), of random sign, each at
+    # most 2^-8, and the first two through an exponent: a logit of |q| |k| / 8 <= 8 sqrt 2 shifts by 8 * 2^-8 /
+    # sqrt(64 / 2) or less in the mean square, under 2^-8 * sqrt 2
+    far = lambda a, b: ((a.double() - b).norm() / b.norm()).item()
+    assert far(_unpack(w, want[0]), o) < 5 ** 0.5 * 2.0 ** -8
+    for got, ref in zip((want[4], want[2], want[5], want[3]), grads):
+        assert far(got, ref) < 5 ** 0.5 * 2.0 ** -8
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = layer()
+    s.synchronize()
+    same(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = layer()
+    x.copy_(rn(*x.shape).to(torch.bfloat16))
+    t.copy_(rn(32, 4).to(torch.bfloat16))
+    graph.replay()
+    torch.cuda.synchronize()
+    held = [u.clone() for u in held]
+    same(held, layer())
+    assert not torch.equal(held[0], want[0])
+    assert ops.loong_get_device_status() == ops.LOONG_OK
+
+
+@pytest.mark.parametrize("name", ["gqa", "not-causal", "empty-rows-ring", "group-of-34"])
+def test_checked_build(cuda_device, monkeypatch, name):
+    """The build with device address checks finds nothing to report."""
+    monkeypatch.setattr(ops, "LIB_PATH", ops.CHECKED_LIB_PATH)
+    monkeypatch.setattr(ops, "_lib", None)
+    w, x, t, buckets = _make(name)
+    _check(w, x, t, buckets, _run(w, x, t, buckets))
