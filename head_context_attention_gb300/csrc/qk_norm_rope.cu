@@ -14,8 +14,10 @@
 // x and dy and writes dx.  A warp owns one token at a time (or, when tokens are
 // few, some of a token's heads): its lanes form the token's angles once, D / 8
 // lanes hold one head (8 elements each, one 16-byte vector), so a warp
-// instruction moves 512 consecutive bytes of a token, and kUnroll heads' loads
-// are in flight per lane before the first is used.
+// instruction moves 512 consecutive bytes of a token.  Every lane copies its
+// own vectors into shared memory asynchronously, several batches of heads (and
+// the next token's) ahead of their use, and reads back only what it copied
+// itself, so the warps need no barrier.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -74,17 +76,60 @@ struct Lane {
   __device__ Lane() : sub((threadIdx.x & 31) / LPH), li((threadIdx.x & 31) % LPH) {}
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 bf16 as four pairs of fp32, for the paired fp32 instructions.
+struct Vec8 {
+  float2 v[4];
+};
+
+__device__ __forceinline__ Vec8 unpack8(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  Vec8 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return f;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const Vec8& f) {
+  return make_uint4(pack_bf16(f.v[0].x, f.v[0].y), pack_bf16(f.v[1].x, f.v[1].y), pack_bf16(f.v[2].x, f.v[2].y),
+                    pack_bf16(f.v[3].x, f.v[3].y));
+}
+
+__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ Vec8 mul(const Vec8& a, const Vec8& b) {
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+  return r;
+}
+
+__device__ __forceinline__ Vec8 mul(const Vec8& a, float b) {
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], dup(b));
+  return r;
+}
+
+// a b + c
+__device__ __forceinline__ Vec8 fma8(const Vec8& a, const Vec8& b, const Vec8& c) {
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+
+__device__ __forceinline__ Vec8 fma8(const Vec8& a, float b, const Vec8& c) {
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], dup(b), c.v[i]);
+  return r;
+}
+
+__device__ __forceinline__ float dot(const Vec8& a, const Vec8& b) {
+  float2 s = __fmul2_rn(a.v[0], b.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
+  return s.x + s.y;
 }
 
 template <int LPH>
@@ -99,14 +144,25 @@ __device__ __forceinline__ uint4 shfl4(const uint4& v, int src) {
                     __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src));
 }
 
-// The rotation of this lane's 8 elements at one token.  Half-split pairs
-// (i, i + rot_dim / 2): out_i = own_i c_i + partner_i s_i, with the partner's 8
-// elements in lane `partner` and the sign of the sine folded into s.
-// Interleaved pairs (2i, 2i + 1) lie inside the lane: c, s of pair j in c[j], s[j].
-// A lane past rot_dim has c = 1, s = 0.
+// The other half of every pair: lane `partner`'s 8 elements (half-split pairs)
+// or this lane's own with each pair swapped (interleaved pairs).
+template <bool INTER>
+__device__ __forceinline__ uint4 partners(const uint4& x, int partner) {
+  if constexpr (INTER)
+    return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032), __byte_perm(x.z, 0, 0x1032),
+                      __byte_perm(x.w, 0, 0x1032));
+  else
+    return shfl4(x, partner);
+}
+
+// The rotation of this lane's 8 elements at one token: out = own c + other s
+// with `other` the other half of each element's pair and the sign of the sine
+// folded into s; its transpose is own c - other s.  Half-split pairs
+// (i, i + rot_dim / 2) have their other half in lane `partner`, interleaved
+// ones (2i, 2i + 1) in this lane.  Past rot_dim c = 1, s = 0.
 template <int D, bool INTER>
 struct Rotation {
-  float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
+  Vec8 c, s;
   int partner;
 
   // Lane l holds frequencies l and l + 32 (f0, f1); every lane calls.
@@ -124,36 +180,43 @@ struct Rotation {
       sv *= rot_scale;
     };
     sincos_turns(f0, c0, s0);
-    if (half > 32) sincos_turns(f1, c1, s1);  // uniform
-    const int e = ln.li * 8;                  // this lane's first element
+    const bool wide = D == 128 && half > 32;  // uniform
+    if (wide) sincos_turns(f1, c1, s1);
+    const int e = ln.li * 8;  // this lane's first element
     const bool rotated = e < rot_dim;
+    const bool hi = e >= half;
     partner = lane;
-    if constexpr (INTER) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = e / 2 + j;
-        const float ca = __shfl_sync(0xffffffffu, c0, i & 31), cb = __shfl_sync(0xffffffffu, c1, i & 31);
-        const float sa = __shfl_sync(0xffffffffu, s0, i & 31), sb = __shfl_sync(0xffffffffu, s1, i & 31);
-        c[j] = rotated ? (i < 32 ? ca : cb) : 1.f;
-        s[j] = rotated ? (i < 32 ? sa : sb) : 0.f;
+    if (!INTER && rotated) partner = hi ? lane - half / 8 : lane + half / 8;
+    // frequency i lies in lane i mod 32, in the second register from 32 on
+    auto pick = [&](int i, float& cv, float& sv) {
+      cv = __shfl_sync(0xffffffffu, c0, i & 31);
+      sv = __shfl_sync(0xffffffffu, s0, i & 31);
+      if (wide) {
+        const float cb = __shfl_sync(0xffffffffu, c1, i & 31), sb = __shfl_sync(0xffffffffu, s1, i & 31);
+        cv = i & 32 ? cb : cv;
+        sv = i & 32 ? sb : sv;
       }
-    } else {
-      const bool hi = e >= half;
-      if (rotated) partner = hi ? lane - half / 8 : lane + half / 8;
+      cv = rotated ? cv : 1.f;
+      sv = rotated ? sv : 0.f;
+    };
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = (hi ? e - half : e) + j;
-        const float ca = __shfl_sync(0xffffffffu, c0, i & 31), cb = __shfl_sync(0xffffffffu, c1, i & 31);
-        const float sa = __shfl_sync(0xffffffffu, s0, i & 31), sb = __shfl_sync(0xffffffffu, s1, i & 31);
-        const float sj = i < 32 ? sa : sb;
-        c[j] = rotated ? (i < 32 ? ca : cb) : 1.f;
-        s[j] = rotated ? (hi ? sj : -sj) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (INTER) {
+        float cv, sv;
+        pick(e / 2 + j, cv, sv);
+        c.v[j] = make_float2(cv, cv);
+        s.v[j] = make_float2(-sv, sv);
+      } else {
+        const int i = (hi ? e - half : e) + 2 * j;
+        pick(i, c.v[j].x, s.v[j].x);
+        pick(i + 1, c.v[j].y, s.v[j].y);
+        if (!hi) s.v[j] = make_float2(-s.v[j].x, -s.v[j].y);
       }
     }
   }
 };
 
-// Token of a warp's work item and where its rows lie on both sides.
+// Token of a warp's work item and where its rows lie on the attention side.
 struct TokenPlace {
   int tok;
   int64_t rank_row;  // (b cp + c) P
@@ -174,232 +237,332 @@ struct TokenPlace {
     rank_row = (static_cast<int64_t>(b) * a.cp + c) * a.P;
     pos = a.positions ? __ldg(a.positions + tok) : a.pos_begin + s;
   }
-  // element offset of head h on the attention side
+};
+
+// This lane's vector on the attention side, walked head by head: `at` is its
+// element offset for head h = p hpr + hr, moved on by whole slots (HPW heads),
+// over a head rank's end into the next one's plane.
+struct AttnCursor {
+  int64_t at, jump;
+  int hr, hpr;
   template <int D>
-  __device__ __forceinline__ int64_t attn(const QkArgs& a, const HeadTensor& t, int h) const {
-    const int p = a.P == 1 ? 0 : h / t.hpr;
-    return (rank_row + p) * t.plane + (u * t.hpr + (h - p * t.hpr)) * D;
+  __device__ __forceinline__ void set(const TokenPlace& tp, const HeadTensor& t, int h, int li) {
+    hpr = t.hpr;
+    const int p = h / hpr;
+    hr = h - p * hpr;
+    at = (tp.rank_row + p) * t.plane + (tp.u * hpr + hr) * D + li * 8;
+    jump = t.plane - static_cast<int64_t>(hpr) * D;
   }
   template <int D>
-  __device__ __forceinline__ int64_t proj(int64_t stride, int h) const {
-    return tok * stride + static_cast<int64_t>(h) * D;
+  __device__ __forceinline__ void next() {
+    constexpr int HPW = Lane<D>::HPW;
+    at += HPW * D;
+    hr += HPW;
+    while (hr >= hpr) {  // natural layout: past the last head only
+      hr -= hpr;
+      at += jump;
+    }
   }
 };
 
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
 // w + w_offset of 8 elements from e
-__device__ __forceinline__ void load_w(const float* w, float w_offset, int e, float (&f)[8]) {
-  if (!w) {
+__device__ __forceinline__ Vec8 load_w(const float* w, float w_offset, int e) {
+  Vec8 f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
-    return;
+  for (int i = 0; i < 4; i += 2) {
+    if (!w) {
+      f.v[i] = f.v[i + 1] = dup(1.f);
+      continue;
+    }
+    const float4 v = __ldg(reinterpret_cast<const float4*>(w + e + 2 * i));
+    f.v[i] = make_float2(v.x + w_offset, v.y + w_offset);
+    f.v[i + 1] = make_float2(v.z + w_offset, v.w + w_offset);
   }
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(w + e + i));
-    f[i] = v.x + w_offset;
-    f[i + 1] = v.y + w_offset;
-    f[i + 2] = v.z + w_offset;
-    f[i + 3] = v.w + w_offset;
-  }
+  return f;
 }
 
-constexpr int kUnroll = 4;
+// 16 bytes from global to shared memory, asynchronously; `live` false writes
+// zeros and reads nothing.
+__device__ __forceinline__ void copy16(void* dst, const __nv_bfloat16* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most N of this thread's newest copy groups are under way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The batches of a warp's work, in order: items it, it + nwarps, ..., an item
+// being a token and a range of its slots (Q's, then K's, then V's; a slot is
+// the heads of one warp instruction), cut into batches of up to U slots of one
+// tensor.  Two of these run over the same batches: one starts their copies, the
+// other, some batches behind, uses them.
+template <int U>
+struct BatchWalk {
+  uint32_t it, items, nwarps;
+  int slots, tok, lo, hi;   // the item
+  int ti, first;            // the tensor and the item's first slot of the next one
+  int sl, s1;               // the batch: slots [sl, min(sl + U, s1)) of the tensor
+  bool new_item, new_tensor;
+  __device__ __forceinline__ void start(const QkArgs& a) {
+    slots = a.t[0].slots + a.t[1].slots + a.t[2].slots;
+    items = static_cast<uint32_t>(a.tokens) * a.parts;
+    nwarps = gridDim.x * kWarps;
+    it = blockIdx.x * kWarps + (threadIdx.x >> 5) - nwarps;
+    ti = 2;
+    settle(a);
+  }
+  __device__ __forceinline__ bool done() const { return it >= items; }
+  __device__ __forceinline__ void settle(const QkArgs& a) {
+    new_item = false;
+    new_tensor = true;
+    do {
+      if (++ti == 3) {
+        it += nwarps;
+        if (it >= items) return;
+        new_item = true;
+        ti = first = 0;
+        if (a.parts == 1) {
+          tok = static_cast<int>(it);
+          lo = 0;
+          hi = slots;
+        } else {
+          tok = static_cast<int>(it / a.parts);
+          const int part = static_cast<int>(it - static_cast<uint32_t>(tok) * a.parts);
+          lo = slots * part / a.parts;
+          hi = slots * (part + 1) / a.parts;
+        }
+      }
+      const int n = a.t[ti].slots;
+      sl = max(lo, first) - first;
+      s1 = min(hi, first + n) - first;
+      first += n;
+    } while (sl >= s1);
+  }
+  __device__ __forceinline__ void next(const QkArgs& a) {
+    sl += U;
+    new_item = new_tensor = false;
+    if (sl >= s1) settle(a);
+  }
+};
+
+// Slots per batch and batches per warp in shared memory: loads of DEPTH - 1
+// batches are in flight while one is used.
+constexpr int kFwdBatch = 4, kFwdDepth = 5, kFwdBlocks = 2;
+constexpr int kBwdBatch = 2, kBwdDepth = 5, kBwdBlocks = 2;
+constexpr int kFwdSmem = kWarps * kFwdDepth * kFwdBatch * 512;
+constexpr int kBwdSmem = kWarps * kBwdDepth * kBwdBatch * 2 * 512;
 
 template <int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) qk_fwd_kernel(const __grid_constant__ QkArgs a) {
   using L = Lane<D>;
+  constexpr int U = kFwdBatch, DEPTH = kFwdDepth;
+  extern __shared__ uint4 ring_smem[];
   const L ln;
   const int lane = threadIdx.x & 31;
+  uint4* ring = ring_smem + (threadIdx.x >> 5) * (DEPTH * U * 32) + lane;  // this lane's vectors, 32 apart
   const int half = a.rot_dim / 2;
   const uint64_t f0 = lane < half ? a.freq[lane] : 0, f1 = lane + 32 < half ? a.freq[lane + 32] : 0;
-  const int slots = a.t[0].slots + a.t[1].slots + a.t[2].slots;
-  const int64_t items = static_cast<int64_t>(a.tokens) * a.parts;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += nwarps) {
-    const int tok = static_cast<int>(it / a.parts);
-    const int part = static_cast<int>(it - static_cast<int64_t>(tok) * a.parts);
-    const int lo = static_cast<int>(static_cast<int64_t>(slots) * part / a.parts);
-    const int hi = static_cast<int>(static_cast<int64_t>(slots) * (part + 1) / a.parts);
-    TokenPlace tp;
-    tp.set(a, tok);
-    Rotation<D, INTER> rot;
-    rot.form(ln, a.rot_dim, f0, f1, tp.pos, a.rot_scale);
-    int first = 0;  // the tensor's first slot
-#pragma unroll 1
-    for (int ti = 0; ti < 3; ++ti) {
-      const HeadTensor& t = a.t[ti];
-      const int s0 = max(lo, first) - first, s1 = min(hi, first + t.slots) - first;
-      first += t.slots;
-      if (s0 >= s1) continue;
-      float w[8], wp[8];
-      if (NORM && ti < 2) {
-        load_w(t.w, a.w_offset, ln.li * 8, w);
-        if (!INTER) load_w(t.w, a.w_offset, (rot.partner % L::LPH) * 8, wp);
+
+  BatchWalk<U> ahead;
+  const __nv_bfloat16* src = nullptr;
+  int ahead_h = 0;
+  auto issue = [&](int stage) {
+    if (!ahead.done()) {
+      const HeadTensor& t = a.t[ahead.ti];
+      if (ahead.new_tensor) {
+        ahead_h = ahead.sl * L::HPW + ln.sub;
+        src = t.x + ahead.tok * t.x_stride + ahead_h * D + ln.li * 8;
       }
-      for (int sl = s0; sl < s1; sl += kUnroll) {
-        uint4 x[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          const int h = (sl + k) * L::HPW + ln.sub;
-          x[k] = make_uint4(0, 0, 0, 0);
-          if (sl + k < s1 && h < t.heads) x[k] = load16(t.x + tp.proj<D>(t.x_stride, h) + ln.li * 8);
-        }
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          if (sl + k >= s1) break;  // uniform
-          const int h = (sl + k) * L::HPW + ln.sub;
-          uint4 y = x[k];
-          if (ti < 2) {
-            float f[8];
-            unpack8(x[k], f);
-            float r = 1.f;
-            if (NORM) {
-              float ss = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-              r = rsqrtf(head_sum<L::LPH>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] *= r * w[i];
-            }
-            if constexpr (INTER) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float u = f[2 * j], v = f[2 * j + 1];
-                f[2 * j] = u * rot.c[j] - v * rot.s[j];
-                f[2 * j + 1] = v * rot.c[j] + u * rot.s[j];
-              }
-            } else {
-              float g[8];
-              unpack8(shfl4(x[k], rot.partner), g);  // the partner's raw elements: the head's r is shared
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float gp = NORM ? g[i] * (r * wp[i]) : g[i];
-                f[i] = fmaf(f[i], rot.c[i], gp * rot.s[i]);
-              }
-            }
-            y = pack8(f);
-          }
-          if (h < t.heads) {
-            const int64_t o = tp.attn<D>(a, t, h) + ln.li * 8;
-            if (in_bounds(o >= 0 && o + 8 <= a.out_elems[ti], a.err)) *reinterpret_cast<uint4*>(t.out + o) = y;
-          }
-        }
-      }
+      for (int k = 0; k < U; ++k)
+        copy16(ring + (stage * U + k) * 32, src + k * L::HPW * D,
+               ahead.sl + k < ahead.s1 && ahead_h + k * L::HPW < t.heads);
+      src += U * L::HPW * D;
+      ahead_h += U * L::HPW;
+      ahead.next(a);
     }
+    copy_commit();
+  };
+  ahead.start(a);
+  BatchWalk<U> w = ahead;
+  for (int i = 0; i < DEPTH - 1; ++i) issue(i);
+
+  TokenPlace tp;
+  Rotation<D, INTER> rot;
+  Vec8 wc, ws;
+  AttnCursor out;
+  int h = 0;
+  for (int stage = 0; !w.done(); w.next(a)) {
+    issue(stage == 0 ? DEPTH - 1 : stage - 1);
+    const HeadTensor& t = a.t[w.ti];
+    if (w.new_item) {
+      tp.set(a, w.tok);
+      rot.form(ln, a.rot_dim, f0, f1, tp.pos, a.rot_scale);
+    }
+    if (w.new_tensor) {
+      // y = r (x (w c) + x_other (w_other s)): the weights go into this token's cosines and sines
+      wc = rot.c;
+      ws = rot.s;
+      if (NORM && w.ti < 2) {
+        const Vec8 wt = load_w(t.w, a.w_offset, ln.li * 8);
+        wc = mul(wt, wc);
+        if constexpr (INTER) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ws.v[i] = __fmul2_rn(make_float2(wt.v[i].y, wt.v[i].x), ws.v[i]);
+        } else {
+          ws = mul(load_w(t.w, a.w_offset, (rot.partner % L::LPH) * 8), ws);
+        }
+      }
+      h = w.sl * L::HPW + ln.sub;
+      out.set<D>(tp, t, h, ln.li);
+    }
+    copy_wait<DEPTH - 1>();
+    uint4 x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) x[k] = ring[(stage * U + k) * 32];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (w.sl + k >= w.s1) break;  // uniform
+      uint4 y = x[k];
+      if (w.ti < 2) {
+        const Vec8 f = unpack8(x[k]);
+        Vec8 g = unpack8(partners<INTER>(x[k], rot.partner));
+        g = fma8(g, ws, mul(f, wc));
+        if (NORM) g = mul(g, rsqrtf(head_sum<L::LPH>(dot(f, f)) * (1.f / D) + a.eps));
+        y = pack8(g);
+      }
+      if (h < t.heads && in_bounds(out.at >= 0 && out.at + 8 <= a.out_elems[w.ti], a.err))
+        *reinterpret_cast<uint4*>(t.out + out.at) = y;
+      h += L::HPW;
+      out.next<D>();
+    }
+    stage = stage == DEPTH - 1 ? 0 : stage + 1;
   }
 }
 
-constexpr int kBwdUnroll = 2;
-
 template <int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
   using L = Lane<D>;
+  constexpr int U = kBwdBatch, DEPTH = kBwdDepth;
+  extern __shared__ uint4 ring_smem[];
   const L ln;
+  const int lane = threadIdx.x & 31;
+  // per stage: U vectors of dy, then U of x
+  uint4* ring = ring_smem + (threadIdx.x >> 5) * (DEPTH * U * 2 * 32) + lane;
   // The weight gradients of this warp: per lane, 8 elements of Q's and of K's,
   // summed in registers over one token's heads and then here over its tokens
   // (two short chains instead of one long one).
   __shared__ float4 dw_sh[NORM ? 2 : 1][NORM ? 2 : 1][NORM ? kThreads : 1];
   if (NORM)
     for (int i = 0; i < 4; ++i) dw_sh[i >> 1][i & 1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int lane = threadIdx.x & 31;
   const int half = a.rot_dim / 2;
   const uint64_t f0 = lane < half ? a.freq[lane] : 0, f1 = lane + 32 < half ? a.freq[lane + 32] : 0;
-  const int slots = a.t[0].slots + a.t[1].slots + a.t[2].slots;
-  const int64_t items = static_cast<int64_t>(a.tokens) * a.parts;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += nwarps) {
-    const int tok = static_cast<int>(it / a.parts);
-    const int part = static_cast<int>(it - static_cast<int64_t>(tok) * a.parts);
-    const int lo = static_cast<int>(static_cast<int64_t>(slots) * part / a.parts);
-    const int hi = static_cast<int>(static_cast<int64_t>(slots) * (part + 1) / a.parts);
-    TokenPlace tp;
-    tp.set(a, tok);
-    Rotation<D, INTER> rot;
-    rot.form(ln, a.rot_dim, f0, f1, tp.pos, a.rot_scale);
-    int first = 0;
-#pragma unroll 1
-    for (int ti = 0; ti < 3; ++ti) {
-      const HeadTensor& t = a.t[ti];
-      const int s0 = max(lo, first) - first, s1 = min(hi, first + t.slots) - first;
-      first += t.slots;
-      if (s0 >= s1) continue;
-      const bool normed = NORM && ti < 2;
-      float w[8], dw[8] = {};
-      if (normed) load_w(t.w, a.w_offset, ln.li * 8, w);
-      for (int sl = s0; sl < s1; sl += kBwdUnroll) {
-        uint4 x[kBwdUnroll], dy[kBwdUnroll];
-#pragma unroll
-        for (int k = 0; k < kBwdUnroll; ++k) {
-          const int h = (sl + k) * L::HPW + ln.sub;
-          x[k] = dy[k] = make_uint4(0, 0, 0, 0);
-          if (sl + k < s1 && h < t.heads) {
-            if (normed) x[k] = load16(t.x + tp.proj<D>(t.x_stride, h) + ln.li * 8);
-            const int64_t o = tp.attn<D>(a, t, h) + ln.li * 8;
-            if (in_bounds(o >= 0 && o + 8 <= a.out_elems[ti], a.err)) dy[k] = load16(t.dy + o);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kBwdUnroll; ++k) {
-          if (sl + k >= s1) break;  // uniform
-          const int h = (sl + k) * L::HPW + ln.sub;
-          uint4 y = dy[k];
-          if (ti < 2) {
-            float g[8];
-            unpack8(dy[k], g);
-            if constexpr (INTER) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float u = g[2 * j], v = g[2 * j + 1];
-                g[2 * j] = u * rot.c[j] + v * rot.s[j];
-                g[2 * j + 1] = v * rot.c[j] - u * rot.s[j];
-              }
-            } else {
-              float p[8];
-              unpack8(shfl4(dy[k], rot.partner), p);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) g[i] = fmaf(g[i], rot.c[i], -p[i] * rot.s[i]);
-            }
-            if (NORM) {
-              float f[8];
-              unpack8(x[k], f);
-              float ss = 0.f, dot = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                ss = fmaf(f[i], f[i], ss);
-                dot = fmaf(g[i] * w[i], f[i], dot);
-              }
-              ss = head_sum<L::LPH>(ss);
-              dot = head_sum<L::LPH>(dot);
-              const float r = rsqrtf(ss * (1.f / D) + a.eps);
-              const float m = dot * r * (1.f / D);  // mean(h x r)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float xr = f[i] * r;
-                dw[i] = fmaf(g[i], xr, dw[i]);
-                g[i] = r * fmaf(-xr, m, g[i] * w[i]);
-              }
-            }
-            y = pack8(g);
-          }
-          if (h < t.heads) *reinterpret_cast<uint4*>(t.out + tp.proj<D>(t.dx_stride, h) + ln.li * 8) = y;
-        }
+
+  BatchWalk<U> ahead;
+  TokenPlace ahead_tp;
+  const __nv_bfloat16* src = nullptr;
+  AttnCursor in;
+  int ahead_h = 0;
+  auto issue = [&](int stage) {
+    if (!ahead.done()) {
+      const HeadTensor& t = a.t[ahead.ti];
+      if (ahead.new_item) ahead_tp.set(a, ahead.tok);
+      if (ahead.new_tensor) {
+        ahead_h = ahead.sl * L::HPW + ln.sub;
+        src = t.x + ahead.tok * t.x_stride + ahead_h * D + ln.li * 8;
+        in.set<D>(ahead_tp, t, ahead_h, ln.li);
       }
-      if (normed) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float4 v = dw_sh[ti][i][threadIdx.x];
-          v.x += dw[4 * i];
-          v.y += dw[4 * i + 1];
-          v.z += dw[4 * i + 2];
-          v.w += dw[4 * i + 3];
-          dw_sh[ti][i][threadIdx.x] = v;
-        }
+      for (int k = 0; k < U; ++k) {
+        const bool live = ahead.sl + k < ahead.s1 && ahead_h < t.heads;
+        const bool ok = live && in_bounds(in.at >= 0 && in.at + 8 <= a.out_elems[ahead.ti], a.err);
+        copy16(ring + (stage * 2 * U + k) * 32, t.dy + (ok ? in.at : 0), ok);
+        if (NORM && ahead.ti < 2) copy16(ring + ((stage * 2 + 1) * U + k) * 32, src + k * L::HPW * D, live);
+        ahead_h += L::HPW;
+        in.next<D>();
       }
+      src += U * L::HPW * D;
+      ahead.next(a);
     }
+    copy_commit();
+  };
+  ahead.start(a);
+  BatchWalk<U> w = ahead;
+  for (int i = 0; i < DEPTH - 1; ++i) issue(i);
+
+  Rotation<D, INTER> rot;
+  Vec8 wt, dw{};
+  __nv_bfloat16* dst = nullptr;
+  int h = 0, dw_ti = 0;
+  auto bank_dw = [&]() {  // the sums of a token's heads into the warp's sums
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float4 v = dw_sh[dw_ti][i][threadIdx.x];
+      v.x += dw.v[2 * i].x;
+      v.y += dw.v[2 * i].y;
+      v.z += dw.v[2 * i + 1].x;
+      v.w += dw.v[2 * i + 1].y;
+      dw_sh[dw_ti][i][threadIdx.x] = v;
+    }
+    dw = Vec8{};
+  };
+  for (int stage = 0; !w.done(); w.next(a)) {
+    issue(stage == 0 ? DEPTH - 1 : stage - 1);
+    const HeadTensor& t = a.t[w.ti];
+    const bool normed = NORM && w.ti < 2;
+    if (w.new_item) {
+      rot.form(ln, a.rot_dim, f0, f1, a.positions ? __ldg(a.positions + w.tok) : a.pos_begin + w.tok % a.S,
+               a.rot_scale);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rot.s.v[i] = make_float2(-rot.s.v[i].x, -rot.s.v[i].y);  // the transpose
+    }
+    if (w.new_tensor) {
+      if (normed) {
+        bank_dw();
+        dw_ti = w.ti;
+        wt = load_w(t.w, a.w_offset, ln.li * 8);
+      }
+      h = w.sl * L::HPW + ln.sub;
+      dst = t.out + w.tok * t.dx_stride + h * D + ln.li * 8;
+    }
+    copy_wait<DEPTH - 1>();
+    uint4 dy[U], x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      dy[k] = ring[(stage * 2 * U + k) * 32];
+      if (normed) x[k] = ring[((stage * 2 + 1) * U + k) * 32];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (w.sl + k >= w.s1) break;  // uniform
+      uint4 y = dy[k];
+      if (w.ti < 2) {
+        Vec8 g = mul(unpack8(dy[k]), rot.c);
+        g = fma8(unpack8(partners<INTER>(dy[k], rot.partner)), rot.s, g);
+        if (NORM) {
+          const Vec8 f = unpack8(x[k]);
+          const Vec8 gx = mul(g, f);
+          const float ss = head_sum<L::LPH>(dot(f, f)), gwx = head_sum<L::LPH>(dot(gx, wt));
+          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+          dw = fma8(gx, r, dw);
+          // dx = r (g w - x r mean(g w x r))
+          g = mul(fma8(f, -r * (r * gwx * (1.f / D)), mul(g, wt)), r);
+        }
+        y = pack8(g);
+      }
+      if (h < t.heads) *reinterpret_cast<uint4*>(dst) = y;
+      h += L::HPW;
+      dst += L::HPW * D;
+    }
+    stage = stage == DEPTH - 1 ? 0 : stage + 1;
   }
   if (NORM && a.dw_part) {
+    bank_dw();
     __syncthreads();
     // element e of a head lies in lanes li = e / 8 of every head slot of every warp
     for (int j = threadIdx.x; j < 2 * D; j += kThreads) {
@@ -517,24 +680,25 @@ unsigned plan_grid(QkArgs& a, int blocks_per_sm, int max_blocks) {
   return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cap, (items + kWarps - 1) / kWarps)));
 }
 
-template <int D>
-void launch_fwd_kernel(const QkArgs& a, bool inter, bool norm, unsigned grid, cudaStream_t s) {
-  if (inter)
-    norm ? qk_fwd_kernel<D, true, true><<<grid, kThreads, 0, s>>>(a)
-         : qk_fwd_kernel<D, true, false><<<grid, kThreads, 0, s>>>(a);
-  else
-    norm ? qk_fwd_kernel<D, false, true><<<grid, kThreads, 0, s>>>(a)
-         : qk_fwd_kernel<D, false, false><<<grid, kThreads, 0, s>>>(a);
+using QkKernel = void (*)(QkArgs);
+
+int launch(QkKernel kern, int smem, unsigned grid, const QkArgs& a, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e);
+  kern<<<grid, kThreads, smem, s>>>(a);
+  return check_launch();
 }
 
 template <int D>
-void launch_bwd_kernel(const QkArgs& a, bool inter, bool norm, unsigned grid, cudaStream_t s) {
-  if (inter)
-    norm ? qk_bwd_kernel<D, true, true><<<grid, kThreads, 0, s>>>(a)
-         : qk_bwd_kernel<D, true, false><<<grid, kThreads, 0, s>>>(a);
-  else
-    norm ? qk_bwd_kernel<D, false, true><<<grid, kThreads, 0, s>>>(a)
-         : qk_bwd_kernel<D, false, false><<<grid, kThreads, 0, s>>>(a);
+QkKernel fwd_kernel(bool inter, bool norm) {
+  if (inter) return norm ? qk_fwd_kernel<D, true, true> : qk_fwd_kernel<D, true, false>;
+  return norm ? qk_fwd_kernel<D, false, true> : qk_fwd_kernel<D, false, false>;
+}
+
+template <int D>
+QkKernel bwd_kernel(bool inter, bool norm) {
+  if (inter) return norm ? qk_bwd_kernel<D, true, true> : qk_bwd_kernel<D, true, false>;
+  return norm ? qk_bwd_kernel<D, false, true> : qk_bwd_kernel<D, false, false>;
 }
 
 }  // namespace
@@ -572,13 +736,10 @@ int loong_qk_norm_rope_fwd(const loong_attn_desc* d, const loong_qk_opts* opts, 
     a.t[i].out = static_cast<__nv_bfloat16*>(out[i]);
     a.t[i].w = w[i];
   }
-  const unsigned grid = plan_grid(a, 6, 1 << 20);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  if (d->head_dim == 128)
-    launch_fwd_kernel<128>(a, opts->interleaved, opts->norm, grid, s);
-  else
-    launch_fwd_kernel<64>(a, opts->interleaved, opts->norm, grid, s);
-  return check_launch();
+  const unsigned grid = plan_grid(a, kFwdBlocks, 1 << 20);
+  return launch(d->head_dim == 128 ? fwd_kernel<128>(opts->interleaved, opts->norm)
+                                   : fwd_kernel<64>(opts->interleaved, opts->norm),
+                kFwdSmem, grid, a, reinterpret_cast<cudaStream_t>(stream_));
 }
 
 size_t loong_qk_norm_rope_bwd_workspace_size(const loong_attn_desc* d, const loong_qk_opts* opts) {
@@ -624,13 +785,12 @@ int loong_qk_norm_rope_bwd(const loong_attn_desc* d, const loong_qk_opts* opts, 
     a.t[i].w = w[i];
   }
   a.dw_part = want_dw ? static_cast<float*>(ws) : nullptr;
-  const unsigned grid = plan_grid(a, 4, kBwdMaxBlocks);
+  const unsigned grid = plan_grid(a, kBwdBlocks, kBwdMaxBlocks);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  if (d->head_dim == 128)
-    launch_bwd_kernel<128>(a, opts->interleaved, opts->norm, grid, s);
-  else
-    launch_bwd_kernel<64>(a, opts->interleaved, opts->norm, grid, s);
-  if ((st = check_launch()) != LOONG_OK || !want_dw) return st;
+  st = launch(d->head_dim == 128 ? bwd_kernel<128>(opts->interleaved, opts->norm)
+                                 : bwd_kernel<64>(opts->interleaved, opts->norm),
+              kBwdSmem, grid, a, s);
+  if (st != LOONG_OK || !want_dw) return st;
   dw_sum_kernel<<<(2 * d->head_dim + kWarps - 1) / kWarps, kThreads, 0, s>>>(a.dw_part, static_cast<int>(grid),
                                                                              d->head_dim, dwq, dwk);
   return check_launch();
