@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -53,6 +54,7 @@ struct QkArgs {
   HeadTensor t[3];
   int tokens, S;           // batch * S and S
   int P, cp, zigzag, blk;  // natural: P = cp = 1, blk = S
+  FastDiv by_S, by_blk;
   int64_t s_rank;
   const int64_t* positions;  // [B, S] or null
   int64_t pos_begin;
@@ -164,78 +166,87 @@ template <int D, bool INTER>
 struct Rotation {
   Vec8 c, s;
   int partner;
+  int at;          // first frequency of this lane's elements
+  float sign;      // of the sine
+  uint64_t f0, f1;  // frequencies lane and lane + 32
 
-  // Lane l holds frequencies l and l + 32 (f0, f1); every lane calls.
-  __device__ __forceinline__ void form(const Lane<D>& ln, int rot_dim, uint64_t f0, uint64_t f1, int64_t pos,
-                                       float rot_scale) {
+  __device__ __forceinline__ void init(const QkArgs& a, const Lane<D>& ln) {
     const int lane = threadIdx.x & 31;
-    const int half = rot_dim / 2;
-    float c0, s0, c1 = 1.f, s1 = 0.f;
-    auto sincos_turns = [&](uint64_t f, float& cv, float& sv) {
+    const int half = a.rot_dim / 2;
+    f0 = lane < half ? a.freq[lane] : 0;
+    f1 = D == 128 && lane + 32 < half ? a.freq[lane + 32] : 0;
+    const int e = ln.li * 8;  // this lane's first element
+    const bool hi = e >= half;
+    partner = lane;
+    at = -1;
+    if (e < a.rot_dim) {
+      if (!INTER) partner = hi ? lane - half / 8 : lane + half / 8;
+      at = INTER ? e / 2 : hi ? e - half : e;
+    }
+    sign = hi ? 1.f : -1.f;
+  }
+  // Every lane calls: the warp forms each angle once, in its own `table` (cosines
+  // of 64 frequencies, then sines).
+  __device__ __forceinline__ void form(float* table, bool wide, int64_t pos, float rot_scale) {
+    const int lane = threadIdx.x & 31;
+    auto put = [&](int i, uint64_t f) {
       const uint64_t turns = static_cast<uint64_t>(pos) * f;
       // the top 32 bits as a signed fraction of a turn; 2^-31 gives half turns
       const float x = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f;
+      float sv, cv;
       sincospif(x, &sv, &cv);
-      cv *= rot_scale;
-      sv *= rot_scale;
+      table[i] = cv * rot_scale;
+      table[64 + i] = sv * rot_scale;
     };
-    sincos_turns(f0, c0, s0);
-    const bool wide = D == 128 && half > 32;  // uniform
-    if (wide) sincos_turns(f1, c1, s1);
-    const int e = ln.li * 8;  // this lane's first element
-    const bool rotated = e < rot_dim;
-    const bool hi = e >= half;
-    partner = lane;
-    if (!INTER && rotated) partner = hi ? lane - half / 8 : lane + half / 8;
-    // frequency i lies in lane i mod 32, in the second register from 32 on
-    auto pick = [&](int i, float& cv, float& sv) {
-      cv = __shfl_sync(0xffffffffu, c0, i & 31);
-      sv = __shfl_sync(0xffffffffu, s0, i & 31);
-      if (wide) {
-        const float cb = __shfl_sync(0xffffffffu, c1, i & 31), sb = __shfl_sync(0xffffffffu, s1, i & 31);
-        cv = i & 32 ? cb : cv;
-        sv = i & 32 ? sb : sv;
-      }
-      cv = rotated ? cv : 1.f;
-      sv = rotated ? sv : 0.f;
-    };
+    __syncwarp();  // the previous token's table has been read
+    put(lane, f0);
+    if (D == 128 && wide) put(lane + 32, f1);  // uniform
+    __syncwarp();
+    if (at < 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (INTER) {
-        float cv, sv;
-        pick(e / 2 + j, cv, sv);
-        c.v[j] = make_float2(cv, cv);
-        s.v[j] = make_float2(-sv, sv);
-      } else {
-        const int i = (hi ? e - half : e) + 2 * j;
-        pick(i, c.v[j].x, s.v[j].x);
-        pick(i + 1, c.v[j].y, s.v[j].y);
-        if (!hi) s.v[j] = make_float2(-s.v[j].x, -s.v[j].y);
+      for (int j = 0; j < 4; ++j) {
+        c.v[j] = dup(1.f);
+        s.v[j] = dup(0.f);
+      }
+    } else if constexpr (INTER) {
+      const float4 cv = *reinterpret_cast<const float4*>(table + at);
+      const float4 sv = *reinterpret_cast<const float4*>(table + 64 + at);
+      c.v[0] = dup(cv.x);
+      c.v[1] = dup(cv.y);
+      c.v[2] = dup(cv.z);
+      c.v[3] = dup(cv.w);
+      s.v[0] = make_float2(-sv.x, sv.x);
+      s.v[1] = make_float2(-sv.y, sv.y);
+      s.v[2] = make_float2(-sv.z, sv.z);
+      s.v[3] = make_float2(-sv.w, sv.w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float4 cv = *reinterpret_cast<const float4*>(table + at + 2 * j);
+        const float4 sv = *reinterpret_cast<const float4*>(table + 64 + at + 2 * j);
+        c.v[j] = make_float2(cv.x, cv.y);
+        c.v[j + 1] = make_float2(cv.z, cv.w);
+        s.v[j] = __fmul2_rn(make_float2(sv.x, sv.y), dup(sign));
+        s.v[j + 1] = __fmul2_rn(make_float2(sv.z, sv.w), dup(sign));
       }
     }
   }
 };
 
-// Token of a warp's work item and where its rows lie on the attention side.
+// Where a token's rows lie on the attention side: its row (b cp + c) P of
+// planes, and its position within the ring rank.
 struct TokenPlace {
-  int tok;
-  int64_t rank_row;  // (b cp + c) P
-  int64_t u;         // position within the ring rank
-  int64_t pos;
-  __device__ __forceinline__ void set(const QkArgs& a, int tok_) {
-    tok = tok_;
-    const int b = tok / a.S;
-    const int s = tok - b * a.S;
-    const int k = s / a.blk;
+  int64_t rank_row, u;
+  int s;  // position in the sequence
+  __device__ __forceinline__ void set(const QkArgs& a, int tok) {
+    const int b = static_cast<int>(fdiv(tok, a.by_S));
+    s = tok - b * a.S;
+    const int k = static_cast<int>(fdiv(s, a.by_blk));
     const int off = s - k * a.blk;
-    int c = k;
-    u = off;
-    if (a.zigzag && k >= a.cp) {
-      c = 2 * a.cp - 1 - k;
-      u = a.blk + off;
-    }
-    rank_row = (static_cast<int64_t>(b) * a.cp + c) * a.P;
-    pos = a.positions ? __ldg(a.positions + tok) : a.pos_begin + s;
+    const bool second = a.zigzag && k >= a.cp;
+    const int c = second ? 2 * a.cp - 1 - k : k;
+    u = second ? a.blk + off : off;
+    rank_row = static_cast<int64_t>(b * a.cp + c) * a.P;
   }
 };
 
@@ -248,20 +259,22 @@ struct AttnCursor {
   template <int D>
   __device__ __forceinline__ void set(const TokenPlace& tp, const HeadTensor& t, int h, int li) {
     hpr = t.hpr;
-    const int p = h / hpr;
-    hr = h - p * hpr;
-    at = (tp.rank_row + p) * t.plane + (tp.u * hpr + hr) * D + li * 8;
+    hr = h;
     jump = t.plane - static_cast<int64_t>(hpr) * D;
+    at = tp.rank_row * t.plane + (tp.u * hpr + h) * D + li * 8;
+    wrap();
   }
-  template <int D>
-  __device__ __forceinline__ void next() {
-    constexpr int HPW = Lane<D>::HPW;
-    at += HPW * D;
-    hr += HPW;
+  __device__ __forceinline__ void wrap() {
     while (hr >= hpr) {  // natural layout: past the last head only
       hr -= hpr;
       at += jump;
     }
+  }
+  template <int D>
+  __device__ __forceinline__ void next() {
+    at += Lane<D>::HPW * D;
+    hr += Lane<D>::HPW;
+    wrap();
   }
 };
 
@@ -296,273 +309,298 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The batches of a warp's work, in order: items it, it + nwarps, ..., an item
-// being a token and a range of its slots (Q's, then K's, then V's; a slot is
-// the heads of one warp instruction), cut into batches of up to U slots of one
-// tensor.  Two of these run over the same batches: one starts their copies, the
-// other, some batches behind, uses them.
-template <int U>
+// A warp's items are tokens (or ranges of a token's slots: Q's, then K's, then
+// V's; a slot is the heads of one warp instruction) it, it + nwarps, ..., each
+// cut into batches of up to U slots of one tensor.  This walks them ahead of
+// their use, to start their copies.
+template <int D, int U>
 struct BatchWalk {
-  uint32_t it, items, nwarps;
-  int slots, tok, lo, hi;   // the item
-  int ti, first;            // the tensor and the item's first slot of the next one
-  int sl, s1;               // the batch: slots [sl, min(sl + U, s1)) of the tensor
+  uint32_t it;
+  int tok, lo, hi;  // the item
+  int ti, first;    // the tensor, and the item's first slot of the next one
+  int h, h1;        // this lane's head of the batch's first slot, and the tensor part's end
   bool new_item, new_tensor;
-  __device__ __forceinline__ void start(const QkArgs& a) {
-    slots = a.t[0].slots + a.t[1].slots + a.t[2].slots;
-    items = static_cast<uint32_t>(a.tokens) * a.parts;
-    nwarps = gridDim.x * kWarps;
-    it = blockIdx.x * kWarps + (threadIdx.x >> 5) - nwarps;
-    ti = 2;
-    settle(a);
-  }
-  __device__ __forceinline__ bool done() const { return it >= items; }
-  __device__ __forceinline__ void settle(const QkArgs& a) {
+  __device__ __forceinline__ bool settle(const QkArgs& a, const Lane<D>& ln, uint32_t items, uint32_t nwarps) {
     new_item = false;
     new_tensor = true;
+    int s0, s1;
     do {
       if (++ti == 3) {
         it += nwarps;
-        if (it >= items) return;
+        if (it >= items) {
+          h = h1 = 0;
+          ti = 2;
+          return false;
+        }
         new_item = true;
         ti = first = 0;
-        if (a.parts == 1) {
-          tok = static_cast<int>(it);
-          lo = 0;
-          hi = slots;
-        } else {
-          tok = static_cast<int>(it / a.parts);
-          const int part = static_cast<int>(it - static_cast<uint32_t>(tok) * a.parts);
-          lo = slots * part / a.parts;
-          hi = slots * (part + 1) / a.parts;
-        }
+        item_of(a, it, tok, lo, hi);
       }
       const int n = a.t[ti].slots;
-      sl = max(lo, first) - first;
-      s1 = min(hi, first + n) - first;
+      s0 = max(lo - first, 0);
+      s1 = min(hi - first, n);
       first += n;
-    } while (sl >= s1);
+    } while (s0 >= s1);
+    h = s0 * Lane<D>::HPW + ln.sub;
+    h1 = min(s1 * Lane<D>::HPW, a.t[ti].heads);
+    left = s1 - s0;
+    return true;
   }
-  __device__ __forceinline__ void next(const QkArgs& a) {
-    sl += U;
-    new_item = new_tensor = false;
-    if (sl >= s1) settle(a);
+  int left;  // slots from the batch's first to the tensor part's end
+  static __device__ __forceinline__ void item_of(const QkArgs& a, uint32_t it, int& tok, int& lo, int& hi) {
+    const int slots = a.t[0].slots + a.t[1].slots + a.t[2].slots;
+    if (a.parts == 1) {
+      tok = static_cast<int>(it);
+      lo = 0;
+      hi = slots;
+    } else {
+      tok = static_cast<int>(it / a.parts);
+      const int part = static_cast<int>(it - static_cast<uint32_t>(tok) * a.parts);
+      lo = slots * part / a.parts;
+      hi = slots * (part + 1) / a.parts;
+    }
   }
 };
 
-// Slots per batch and batches per warp in shared memory: loads of DEPTH - 1
-// batches are in flight while one is used.
-constexpr int kFwdBatch = 4, kFwdDepth = 5, kFwdBlocks = 2;
-constexpr int kBwdBatch = 2, kBwdDepth = 5, kBwdBlocks = 2;
-constexpr int kFwdSmem = kWarps * kFwdDepth * kFwdBatch * 512;
-constexpr int kBwdSmem = kWarps * kBwdDepth * kBwdBatch * 2 * 512;
+// Slots per batch and batches per warp in shared memory: the loads of DEPTH - 1
+// batches are in flight while one is used.  Measured at 32 + 8 heads of 128
+// (ranks' layout), forward at 32K and backward at 128K tokens: forward 4 x 6
+// 131 us (6.1 TB/s), 4 x 3 133, 2 x 6 with three blocks per SM 142 (its 80
+// registers spill); backward 2 x 3 710 us (6.4 TB/s), 2 x 4 713, 4 x 3 1015,
+// 2 x 3 with three blocks 1840.
+constexpr int kFwdBatch = 4, kFwdDepth = 6, kFwdBlocks = 2;
+constexpr int kBwdBatch = 2, kBwdDepth = 3, kBwdBlocks = 2;
+constexpr int kTableBytes = kWarps * 128 * 4;  // a warp's cosines and sines
+constexpr int kFwdSmem = kTableBytes + kWarps * kFwdDepth * kFwdBatch * 512;
+constexpr int kBwdSmem = kTableBytes + kWarps * kBwdDepth * kBwdBatch * 2 * 512;
 
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks) qk_fwd_kernel(const __grid_constant__ QkArgs a) {
   using L = Lane<D>;
-  constexpr int U = kFwdBatch, DEPTH = kFwdDepth;
-  extern __shared__ uint4 ring_smem[];
+  constexpr int U = kFwdBatch, DEPTH = kFwdDepth, HPW = L::HPW;
+  extern __shared__ uint4 smem[];
   const L ln;
-  const int lane = threadIdx.x & 31;
-  uint4* ring = ring_smem + (threadIdx.x >> 5) * (DEPTH * U * 32) + lane;  // this lane's vectors, 32 apart
-  const int half = a.rot_dim / 2;
-  const uint64_t f0 = lane < half ? a.freq[lane] : 0, f1 = lane + 32 < half ? a.freq[lane + 32] : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* table = reinterpret_cast<float*>(smem) + warp * 128;
+  // this lane's vectors, 32 apart
+  uint4* ring = smem + kTableBytes / 16 + warp * (DEPTH * U * 32) + lane;
+  const uint32_t items = static_cast<uint32_t>(a.tokens) * a.parts, nwarps = gridDim.x * kWarps;
+  const bool wide = a.rot_dim > 64;
 
-  BatchWalk<U> ahead;
+  BatchWalk<D, U> ahead;
   const __nv_bfloat16* src = nullptr;
-  int ahead_h = 0;
+  bool more = true;
   auto issue = [&](int stage) {
-    if (!ahead.done()) {
-      const HeadTensor& t = a.t[ahead.ti];
-      if (ahead.new_tensor) {
-        ahead_h = ahead.sl * L::HPW + ln.sub;
-        src = t.x + ahead.tok * t.x_stride + ahead_h * D + ln.li * 8;
-      }
+    if (more) {
+      if (ahead.left <= 0) more = ahead.settle(a, ln, items, nwarps);
+      if (more) {
+        if (ahead.new_tensor) src = a.t[ahead.ti].x + ahead.tok * a.t[ahead.ti].x_stride + ahead.h * D + ln.li * 8;
+        ahead.new_tensor = false;
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        copy16(ring + (stage * U + k) * 32, src + k * L::HPW * D,
-               ahead.sl + k < ahead.s1 && ahead_h + k * L::HPW < t.heads);
-      src += U * L::HPW * D;
-      ahead_h += U * L::HPW;
-      ahead.next(a);
+        for (int k = 0; k < U; ++k)
+          copy16(ring + (stage * U + k) * 32, src + k * HPW * D, ahead.h + k * HPW < ahead.h1);
+        src += U * HPW * D;
+        ahead.h += U * HPW;
+        ahead.left -= U;
+      }
     }
     copy_commit();
   };
-  ahead.start(a);
-  BatchWalk<U> w = ahead;
+  const uint32_t it0 = blockIdx.x * kWarps + warp;
+  ahead.it = it0 - nwarps;
+  ahead.ti = 2;
+  ahead.left = 0;
+#pragma unroll 1
   for (int i = 0; i < DEPTH - 1; ++i) issue(i);
 
-  TokenPlace tp;
   Rotation<D, INTER> rot;
-  Vec8 wc, ws;
-  AttnCursor out;
-  int h = 0;
-  for (int stage = 0; !w.done(); w.next(a)) {
-    issue(stage == 0 ? DEPTH - 1 : stage - 1);
-    const HeadTensor& t = a.t[w.ti];
-    if (w.new_item) {
-      tp.set(a, w.tok);
-      rot.form(ln, a.rot_dim, f0, f1, tp.pos, a.rot_scale);
-    }
-    if (w.new_tensor) {
+  rot.init(a, ln);
+  int stage = 0;
+  for (uint32_t it = it0; it < items; it += nwarps) {
+    int tok, lo, hi, first = 0;
+    BatchWalk<D, U>::item_of(a, it, tok, lo, hi);
+    TokenPlace tp;
+    tp.set(a, tok);
+    rot.form(table, wide, a.positions ? __ldg(a.positions + tok) : a.pos_begin + tp.s, a.rot_scale);
+#pragma unroll 1
+    for (int ti = 0; ti < 3; ++ti) {
+      const HeadTensor& t = a.t[ti];
+      const int s0 = max(lo - first, 0), s1 = min(hi - first, t.slots);
+      first += t.slots;
+      if (s0 >= s1) continue;
       // y = r (x (w c) + x_other (w_other s)): the weights go into this token's cosines and sines
-      wc = rot.c;
-      ws = rot.s;
-      if (NORM && w.ti < 2) {
-        const Vec8 wt = load_w(t.w, a.w_offset, ln.li * 8);
-        wc = mul(wt, wc);
+      Vec8 wc = rot.c, ws = rot.s;
+      if (NORM && ti < 2) {
+        const Vec8 w = load_w(t.w, a.w_offset, ln.li * 8);
+        wc = mul(w, wc);
         if constexpr (INTER) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ws.v[i] = __fmul2_rn(make_float2(wt.v[i].y, wt.v[i].x), ws.v[i]);
+          for (int i = 0; i < 4; ++i) ws.v[i] = __fmul2_rn(make_float2(w.v[i].y, w.v[i].x), ws.v[i]);
         } else {
           ws = mul(load_w(t.w, a.w_offset, (rot.partner % L::LPH) * 8), ws);
         }
       }
-      h = w.sl * L::HPW + ln.sub;
+      int h = s0 * HPW + ln.sub;
+      const int h1 = min(s1 * HPW, t.heads);
+      AttnCursor out;
       out.set<D>(tp, t, h, ln.li);
-    }
-    copy_wait<DEPTH - 1>();
-    uint4 x[U];
+      for (int sl = s0; sl < s1; sl += U) {
+        issue(stage == 0 ? DEPTH - 1 : stage - 1);
+        copy_wait<DEPTH - 1>();
+        uint4 x[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) x[k] = ring[(stage * U + k) * 32];
+        for (int k = 0; k < U; ++k) x[k] = ring[(stage * U + k) * 32];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (w.sl + k >= w.s1) break;  // uniform
-      uint4 y = x[k];
-      if (w.ti < 2) {
-        const Vec8 f = unpack8(x[k]);
-        Vec8 g = unpack8(partners<INTER>(x[k], rot.partner));
-        g = fma8(g, ws, mul(f, wc));
-        if (NORM) g = mul(g, rsqrtf(head_sum<L::LPH>(dot(f, f)) * (1.f / D) + a.eps));
-        y = pack8(g);
+        for (int k = 0; k < U; ++k) {
+          if (sl + k >= s1) break;  // uniform
+          uint4 y = x[k];
+          if (ti < 2) {
+            const Vec8 f = unpack8(x[k]);
+            Vec8 g = unpack8(partners<INTER>(x[k], rot.partner));
+            g = fma8(g, ws, mul(f, wc));
+            if (NORM) g = mul(g, rsqrtf(head_sum<L::LPH>(dot(f, f)) * (1.f / D) + a.eps));
+            y = pack8(g);
+          }
+          if (h < h1 && in_bounds(out.at >= 0 && out.at + 8 <= a.out_elems[ti], a.err))
+            *reinterpret_cast<uint4*>(t.out + out.at) = y;
+          h += HPW;
+          out.next<D>();
+        }
+        stage = stage == DEPTH - 1 ? 0 : stage + 1;
       }
-      if (h < t.heads && in_bounds(out.at >= 0 && out.at + 8 <= a.out_elems[w.ti], a.err))
-        *reinterpret_cast<uint4*>(t.out + out.at) = y;
-      h += L::HPW;
-      out.next<D>();
     }
-    stage = stage == DEPTH - 1 ? 0 : stage + 1;
   }
 }
 
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
   using L = Lane<D>;
-  constexpr int U = kBwdBatch, DEPTH = kBwdDepth;
-  extern __shared__ uint4 ring_smem[];
+  constexpr int U = kBwdBatch, DEPTH = kBwdDepth, HPW = L::HPW;
+  extern __shared__ uint4 smem[];
   const L ln;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* table = reinterpret_cast<float*>(smem) + warp * 128;
   // per stage: U vectors of dy, then U of x
-  uint4* ring = ring_smem + (threadIdx.x >> 5) * (DEPTH * U * 2 * 32) + lane;
+  uint4* ring = smem + kTableBytes / 16 + warp * (DEPTH * U * 2 * 32) + lane;
   // The weight gradients of this warp: per lane, 8 elements of Q's and of K's,
   // summed in registers over one token's heads and then here over its tokens
   // (two short chains instead of one long one).
   __shared__ float4 dw_sh[NORM ? 2 : 1][NORM ? 2 : 1][NORM ? kThreads : 1];
   if (NORM)
     for (int i = 0; i < 4; ++i) dw_sh[i >> 1][i & 1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int half = a.rot_dim / 2;
-  const uint64_t f0 = lane < half ? a.freq[lane] : 0, f1 = lane + 32 < half ? a.freq[lane + 32] : 0;
+  const uint32_t items = static_cast<uint32_t>(a.tokens) * a.parts, nwarps = gridDim.x * kWarps;
+  const bool wide = a.rot_dim > 64;
 
-  BatchWalk<U> ahead;
+  BatchWalk<D, U> ahead;
   TokenPlace ahead_tp;
   const __nv_bfloat16* src = nullptr;
   AttnCursor in;
-  int ahead_h = 0;
+  bool more = true;
   auto issue = [&](int stage) {
-    if (!ahead.done()) {
-      const HeadTensor& t = a.t[ahead.ti];
-      if (ahead.new_item) ahead_tp.set(a, ahead.tok);
-      if (ahead.new_tensor) {
-        ahead_h = ahead.sl * L::HPW + ln.sub;
-        src = t.x + ahead.tok * t.x_stride + ahead_h * D + ln.li * 8;
-        in.set<D>(ahead_tp, t, ahead_h, ln.li);
-      }
+    if (more) {
+      if (ahead.left <= 0) more = ahead.settle(a, ln, items, nwarps);
+      if (more) {
+        const HeadTensor& t = a.t[ahead.ti];
+        if (ahead.new_item) ahead_tp.set(a, ahead.tok);
+        if (ahead.new_tensor) {
+          src = t.x + ahead.tok * t.x_stride + ahead.h * D + ln.li * 8;
+          in.set<D>(ahead_tp, t, ahead.h, ln.li);
+        }
+        ahead.new_item = ahead.new_tensor = false;
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const bool live = ahead.sl + k < ahead.s1 && ahead_h < t.heads;
-        const bool ok = live && in_bounds(in.at >= 0 && in.at + 8 <= a.out_elems[ahead.ti], a.err);
-        copy16(ring + (stage * 2 * U + k) * 32, t.dy + (ok ? in.at : 0), ok);
-        if (NORM && ahead.ti < 2) copy16(ring + ((stage * 2 + 1) * U + k) * 32, src + k * L::HPW * D, live);
-        ahead_h += L::HPW;
-        in.next<D>();
+        for (int k = 0; k < U; ++k) {
+          const bool live = ahead.h < ahead.h1;
+          const bool ok = live && in_bounds(in.at >= 0 && in.at + 8 <= a.out_elems[ahead.ti], a.err);
+          copy16(ring + (stage * 2 * U + k) * 32, t.dy + in.at, ok);
+          if (NORM && ahead.ti < 2) copy16(ring + ((stage * 2 + 1) * U + k) * 32, src + k * HPW * D, live);
+          ahead.h += HPW;
+          in.next<D>();
+        }
+        src += U * HPW * D;
+        ahead.left -= U;
       }
-      src += U * L::HPW * D;
-      ahead.next(a);
     }
     copy_commit();
   };
-  ahead.start(a);
-  BatchWalk<U> w = ahead;
+  const uint32_t it0 = blockIdx.x * kWarps + warp;
+  ahead.it = it0 - nwarps;
+  ahead.ti = 2;
+  ahead.left = 0;
+#pragma unroll 1
   for (int i = 0; i < DEPTH - 1; ++i) issue(i);
 
   Rotation<D, INTER> rot;
-  Vec8 wt, dw{};
-  __nv_bfloat16* dst = nullptr;
-  int h = 0, dw_ti = 0;
-  auto bank_dw = [&]() {  // the sums of a token's heads into the warp's sums
+  rot.init(a, ln);
+  rot.sign = -rot.sign;  // the transpose
+  int stage = 0;
+  for (uint32_t it = it0; it < items; it += nwarps) {
+    int tok, lo, hi, first = 0;
+    BatchWalk<D, U>::item_of(a, it, tok, lo, hi);
+    const int s = tok - static_cast<int>(fdiv(tok, a.by_S)) * a.S;
+    rot.form(table, wide, a.positions ? __ldg(a.positions + tok) : a.pos_begin + s, a.rot_scale);
+    if constexpr (INTER) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float4 v = dw_sh[dw_ti][i][threadIdx.x];
-      v.x += dw.v[2 * i].x;
-      v.y += dw.v[2 * i].y;
-      v.z += dw.v[2 * i + 1].x;
-      v.w += dw.v[2 * i + 1].y;
-      dw_sh[dw_ti][i][threadIdx.x] = v;
+      for (int i = 0; i < 4; ++i) rot.s.v[i] = make_float2(-rot.s.v[i].x, -rot.s.v[i].y);
     }
-    dw = Vec8{};
-  };
-  for (int stage = 0; !w.done(); w.next(a)) {
-    issue(stage == 0 ? DEPTH - 1 : stage - 1);
-    const HeadTensor& t = a.t[w.ti];
-    const bool normed = NORM && w.ti < 2;
-    if (w.new_item) {
-      rot.form(ln, a.rot_dim, f0, f1, a.positions ? __ldg(a.positions + w.tok) : a.pos_begin + w.tok % a.S,
-               a.rot_scale);
+#pragma unroll 1
+    for (int ti = 0; ti < 3; ++ti) {
+      const HeadTensor& t = a.t[ti];
+      const int s0 = max(lo - first, 0), s1 = min(hi - first, t.slots);
+      first += t.slots;
+      if (s0 >= s1) continue;
+      const bool normed = NORM && ti < 2;
+      Vec8 w, dw{};
+      if (normed) w = load_w(t.w, a.w_offset, ln.li * 8);
+      int h = s0 * HPW + ln.sub;
+      const int h1 = min(s1 * HPW, t.heads);
+      __nv_bfloat16* dst = t.out + tok * t.dx_stride + h * D + ln.li * 8;
+      for (int sl = s0; sl < s1; sl += U) {
+        issue(stage == 0 ? DEPTH - 1 : stage - 1);
+        copy_wait<DEPTH - 1>();
+        uint4 dy[U], x[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rot.s.v[i] = make_float2(-rot.s.v[i].x, -rot.s.v[i].y);  // the transpose
-    }
-    if (w.new_tensor) {
-      if (normed) {
-        bank_dw();
-        dw_ti = w.ti;
-        wt = load_w(t.w, a.w_offset, ln.li * 8);
-      }
-      h = w.sl * L::HPW + ln.sub;
-      dst = t.out + w.tok * t.dx_stride + h * D + ln.li * 8;
-    }
-    copy_wait<DEPTH - 1>();
-    uint4 dy[U], x[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      dy[k] = ring[(stage * 2 * U + k) * 32];
-      if (normed) x[k] = ring[((stage * 2 + 1) * U + k) * 32];
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (w.sl + k >= w.s1) break;  // uniform
-      uint4 y = dy[k];
-      if (w.ti < 2) {
-        Vec8 g = mul(unpack8(dy[k]), rot.c);
-        g = fma8(unpack8(partners<INTER>(dy[k], rot.partner)), rot.s, g);
-        if (NORM) {
-          const Vec8 f = unpack8(x[k]);
-          const Vec8 gx = mul(g, f);
-          const float ss = head_sum<L::LPH>(dot(f, f)), gwx = head_sum<L::LPH>(dot(gx, wt));
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          dw = fma8(gx, r, dw);
-          // dx = r (g w - x r mean(g w x r))
-          g = mul(fma8(f, -r * (r * gwx * (1.f / D)), mul(g, wt)), r);
+        for (int k = 0; k < U; ++k) {
+          dy[k] = ring[(stage * 2 * U + k) * 32];
+          if (normed) x[k] = ring[((stage * 2 + 1) * U + k) * 32];
         }
-        y = pack8(g);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          if (sl + k >= s1) break;  // uniform
+          uint4 y = dy[k];
+          if (ti < 2) {
+            Vec8 g = mul(unpack8(dy[k]), rot.c);
+            g = fma8(unpack8(partners<INTER>(dy[k], rot.partner)), rot.s, g);
+            if (NORM) {
+              const Vec8 f = unpack8(x[k]);
+              const Vec8 gx = mul(g, f);
+              const float ss = head_sum<L::LPH>(dot(f, f)), gwx = head_sum<L::LPH>(dot(gx, w));
+              const float r = rsqrtf(ss * (1.f / D) + a.eps);
+              dw = fma8(gx, r, dw);
+              // dx = r (g w - x r mean(g w x r))
+              g = mul(fma8(f, -r * (r * gwx * (1.f / D)), mul(g, w)), r);
+            }
+            y = pack8(g);
+          }
+          if (h < h1) *reinterpret_cast<uint4*>(dst) = y;
+          h += HPW;
+          dst += HPW * D;
+        }
+        stage = stage == DEPTH - 1 ? 0 : stage + 1;
       }
-      if (h < t.heads) *reinterpret_cast<uint4*>(dst) = y;
-      h += L::HPW;
-      dst += L::HPW * D;
+      if (normed) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float4 v = dw_sh[ti][i][threadIdx.x];
+          v.x += dw.v[2 * i].x;
+          v.y += dw.v[2 * i].y;
+          v.z += dw.v[2 * i + 1].x;
+          v.w += dw.v[2 * i + 1].y;
+          dw_sh[ti][i][threadIdx.x] = v;
+        }
+      }
     }
-    stage = stage == DEPTH - 1 ? 0 : stage + 1;
   }
   if (NORM && a.dw_part) {
-    bank_dw();
     __syncthreads();
     // element e of a head lies in lanes li = e / 8 of every head slot of every warp
     for (int j = threadIdx.x; j < 2 * D; j += kThreads) {
@@ -636,6 +674,8 @@ void fill_args(QkArgs& a, const loong_attn_desc& d, const loong_qk_opts& o, cons
   a.zigzag = rm && g.zigzag;
   a.blk = rm ? g.blk : a.S;
   a.s_rank = d.seqlen / a.cp;
+  a.by_S = make_fastdiv(static_cast<uint32_t>(a.S));
+  a.by_blk = make_fastdiv(static_cast<uint32_t>(a.blk));
   a.positions = positions;
   a.pos_begin = o.pos_begin;
   a.eps = o.eps;

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -113,27 +114,6 @@ __global__ void bf16_to_f16_scaled_kernel(const uint4* __restrict__ in, uint4* _
       y[u] = pack_f16(__uint_as_float(w[u] << 16) * f, __uint_as_float(w[u] & 0xFFFF0000u) * f);
     out[i] = make_uint4(y[0], y[1], y[2], y[3]);
   }
-}
-
-// Unsigned division by a divisor fixed for the launch, n < 2^31: the
-// multiply-and-shift method of Granlund and Montgomery ("Division by Invariant
-// Integers using Multiplication", 1994), with l = ceil(log2 d) and
-// m = floor(2^32 (2^l - d) / d) + 1, so that n / d = (umulhi(m, n) + n) >> l.
-struct FastDiv {
-  uint32_t d, m, l;
-};
-
-FastDiv make_fastdiv(uint32_t d) {
-  FastDiv f;
-  f.d = d;
-  f.l = 0;
-  while ((1ull << f.l) < d) ++f.l;
-  f.m = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.l) - d)) / d + 1);
-  return f;
-}
-
-__device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
-  return (__umulhi(f.m, n) + n) >> f.l;
 }
 
 // One lane segment per row: L = min(32, 2^ceil(log2 vpr)) lanes, 32 / L rows
