@@ -56,9 +56,9 @@ struct BwdCfg {
   static constexpr int STAT_BYTES = 2 * kTile * 4;  // LSE*log2e and D of one query tile
   // Tiles first (1024-byte aligned, checked at run time), then the row
   // statistics stages, the barriers, the TMEM base address and the abort
-  // flag, then two iteration descriptors per stage (the second for the bias).
+  // flag, then per stage an iteration descriptor and the bias's pieces.
   static constexpr int SMEM_BYTES =
-      (2 + 2 * NS) * TILE_BYTES + DS_BYTES + NS * STAT_BYTES + NBARS * 8 + 16 + 2 * NS * 16;
+      (2 + 2 * NS) * TILE_BYTES + DS_BYTES + NS * STAT_BYTES + NBARS * 8 + 16 + NS * 144;
   // Compute groups of four warps, each covering all 128 TMEM lanes: group g
   // owns query columns [GW g, GW (g+1)) of S^T / dP^T and head-dim columns
   // [GD g, GD (g+1)) of dQ.  Four groups (four compute warps per scheduler)
@@ -107,7 +107,7 @@ struct BwdArgs {
   int t_begin, t_end;
   float scale, scale_log2;
   // Row statistics, [B*Hq][stat_len] each, block b's rows at b*blk_pad:
-  const float* lse2;   // LSE * log2(e)
+  const float* lse2;   // LSE * log2(e); with a bias its negative
   const float* dstat;  // D = rowsum(dO * O)
   int blk_pad, stat_len;
   float* dq_acc;      // fp32, the layout of Q
@@ -122,15 +122,24 @@ struct BwdArgs {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// BIAS: the scores carry the bias of their distance (see attn_fwd.cu) and the
-// kernel sums dS by interval of distances, the gradient of the bias.  A tile
+// BIAS: the scores carry the bias of their distance and the kernel sums dS by
+// interval of distances, the gradient of the bias, both per piece of 32 keys by
+// 32 queries, a compute warp's share of a tile (see attn_fwd.cu).  A piece
 // inside one interval adds its constant to the exponent's offset and its dS sum
-// to one number: a warp sums its part by shuffles and lane g keeps the running
-// sum of the group's head g, written out when the interval changes.  In a tile
-// that a boundary crosses, dS is summed along the diagonals (the sum for a
-// distance moves one lane up with every column) and the diagonals' sums are
-// added up by interval.  Every warp adds to numbers of its own, so the sums do
-// not depend on the order in which blocks run.
+// to one number: the warp sums it by shuffles and lane g keeps the running
+// sum of the group's head g, written out when the interval changes.  In a piece
+// that one boundary crosses, a score and its dS go to one of two constants and
+// sums by the column at which its row passes the boundary.  With more
+// boundaries, dS is summed along the diagonals (the sum for a distance moves
+// one lane up with every column) and the diagonals' sums are added up by
+// interval.  Every warp adds to numbers of its own, so the sums do not depend on
+// the order in which blocks run.
+struct BwdPiece {
+  float lo, hi;  // the bias of the first and the last place
+  int code;      // PieceCode; entry 7: the head in its group
+  int place;     // entry 7: the place of distance q0 - k0
+};
+
 template <int D, bool STEP, bool BIAS>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     ring_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -176,9 +185,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // q_full arrival, so everyone who waited for the stage's data sees it; the
   // compute and reducer warps then need no walk of their own.
   int4* sInfo = reinterpret_cast<int4*>(bars + C::NBARS + 2);
-  // BIAS, per stage: the constant bias in log2 units, the tile's interval (-1: a
-  // boundary crosses it), the place of distance q0 - k0, the head in its group.
-  int4* sBias = sInfo + C::NS;
+  // BIAS, per stage: piece diagonal i < 7 (queries 32 (i - 3) ahead of the keys);
+  // entry 7: the tile's place and head.
+  BwdPiece* sBias = reinterpret_cast<BwdPiece*>(sInfo + C::NS);
+  static_assert(!BIAS || (C::GW == 32 && C::GCH == 1), "a compute warp covers one 32 x 32 piece");
 
   // ---- work item: (batch, kv head, key tile); early (heavy) key tiles first
   const RingGeom& g = a.ring;
@@ -264,7 +274,26 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         tma_load_3d_p(leader, sV + at * C::ATOM_BYTES, &tmV, kv_full, at * 64, kvc, kr);
       }
       int issued = 0;
-      for (int i = 0; i < n; ++i, walk.advance()) {
+      // lanes 0-6: a piece diagonal of the tile the walk stands at, lane 7: its place
+      BwdPiece piece;
+      auto look_up = [&]() {
+        if constexpr (BIAS) {
+          const int i0 = a.bias.off + walk.q0() - k0;
+          if (lane < 7) {
+            const int at = i0 + 32 * (lane - 3);
+            // independent loads, waited for in the next trip
+            piece.code = a.bias.piece[at];
+            const float* l = a.bias.lut + (kvh * a.G + walk.head) * a.bias.len + at;
+            piece.lo = l[-31];
+            piece.hi = l[31];
+          } else {
+            piece.code = walk.head;
+            piece.place = i0;
+          }
+        }
+      };
+      look_up();
+      for (int i = 0; i < n; ++i) {
         const int s = i % C::NS;
         const int u = i / C::NS;
         // coordinates first, off the wait's critical path
@@ -276,17 +305,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // checked build: a reduction never starts outside the accumulator (skipped if it would)
         const bool red_ok =
             in_bounds(qrow64 >= 0 && qrow64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
-        int4 tb;
-        if constexpr (BIAS) {
-          const int i0 = a.bias.off + walk.q0() - k0;
-          const int lo = a.bias.interval[i0 - (kTile - 1)], hi = a.bias.interval[i0 + (kTile - 1)];
-          const float c = lo == hi ? a.bias.lut[head * a.bias.len + i0] * a.scale_log2 : 0.f;
-          tb = make_int4(__float_as_int(c), lo == hi ? lo : -1, i0, walk.head);
-        }
         if (i >= C::NS && !warp_wait(&q_empty[s], (u - 1) & 1, abort_flag, a.err)) break;
-        if (leader) {
-          sInfo[s] = make_int4(qrow, hc, walk.qlen(), (walk.diag() ? 1 : 0) | (red_ok ? 2 : 0));
-          if constexpr (BIAS) sBias[s] = tb;
+        if (leader) sInfo[s] = make_int4(qrow, hc, walk.qlen(), (walk.diag() ? 1 : 0) | (red_ok ? 2 : 0));
+        if constexpr (BIAS) {
+          if (lane < 8) sBias[s * 8 + lane] = piece;
+          __syncwarp();
         }
         mbar_expect_tx_p(leader, &q_full[s], 2 * C::TILE_BYTES + C::STAT_BYTES);
         for (int at = 0; at < C::ATOMS; ++at) {
@@ -305,6 +328,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         bulk_load_p(leader, sStat + s * (2 * kTile), a.lse2 + srow, kTile * 4, &q_full[s]);
         bulk_load_p(leader, sStat + s * (2 * kTile) + kTile, a.dstat + srow, kTile * 4, &q_full[s]);
         ++issued;
+        walk.advance();
+        if (BIAS && i + 1 < n) look_up();  // used in the next trip
       }
       mbar_drain(kv_full, 0, a.err);
       for (int s = 0; s < C::NS; ++s) {
@@ -479,6 +504,19 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       // row statistics of this tile, staged by the producer with Q and dO
       const float* lse_row = sStat + (i % C::NS) * (2 * kTile);
       const float* d_row = lse_row + kTile;
+      // BIAS: this warp's piece; the stage's descriptor comes with Q(i)
+      float tile_b = 0.f;
+      int kind = kPieceConst;
+      const BwdPiece* piece = nullptr;
+      if constexpr (BIAS) {
+        if (!warp_wait(&q_full[i % C::NS], (i / C::NS) & 1)) {
+          ok = false;
+          break;
+        }
+        piece = sBias + (i % C::NS) * 8 + grp - quarter + 3;
+        kind = PieceCode::kind(piece->code);
+        if (kind == kPieceConst) tile_b = piece->lo * a.scale_log2;
+      }
       // ---- P^T = exp2(S^T * scale * log2e - LSE * log2e), two 32-query chunks
       if (!warp_wait(s_full, i & 1)) {
         ok = false;
@@ -489,9 +527,6 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       const int4 info = sInfo[i % C::NS];
       const int qlen = info.z;
       const bool dg = info.w & 1;
-      int4 tb = make_int4(0, 0, 0, 0);
-      if constexpr (BIAS) tb = sBias[i % C::NS];
-      const float tile_b = __int_as_float(tb.x);
       float pv[C::GCH][32];
       {
         uint32_t sv[C::GCH][32];
@@ -503,17 +538,37 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) pv[ch][e] = __uint_as_float(sv[ch][e]);
       }
+      // kPieceStep: the columns (queries) past the boundary for this row
+      auto past_step = [&]() {
+        const int t = lane - PieceCode::step(piece->code);
+        return t > 31 ? 0u : 0xffffffffu << max(t, 0);
+      };
       if constexpr (BIAS) {
-        if (tb.y < 0) {
-          const float* lp = a.bias.lut + static_cast<int64_t>(kvh * a.G + tb.w) * a.bias.len + tb.z - row + grp * C::GW;
+        if (kind == kPieceStep) {
+          const float lo = piece->lo, hi = piece->hi;
+          const uint32_t past = past_step();
 #pragma unroll
-          for (int ch = 0; ch < C::GCH; ++ch)
+          for (int e = 0; e < 32; ++e) pv[0][e] += past >> e & 1 ? hi : lo;
+        } else if (kind == kPieceMixed) {
+          const BwdPiece& place = sBias[(i % C::NS) * 8 + 7];
+          const float* lp = a.bias.lut + static_cast<int64_t>(kvh * a.G + place.code) * a.bias.len + place.place +
+                            32 * (grp - quarter) - lane;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) pv[ch][e] += __ldg(lp + ch * 32 + e);
+          for (int e = 0; e < 32; ++e) pv[0][e] += __ldg(lp + e);
         }
       }
-      // the exponent's offset of a query: the tile's bias minus its LSE
-      auto ofs = [&](float lse2) { return BIAS ? tile_b - lse2 : -lse2; };
+      // P^T before masking: with a bias in pairs, the statistics hold -LSE
+      auto form_p = [&](float s0, float s1, float l0, float l1, float& p0, float& p1) {
+        if constexpr (BIAS) {
+          const float2 x = __ffma2_rn(make_float2(s0, s1), make_float2(a.scale_log2, a.scale_log2),
+                                      __fadd2_rn(make_float2(l0, l1), make_float2(tile_b, tile_b)));
+          p0 = fast_exp2(x.x);
+          p1 = fast_exp2(x.y);
+        } else {
+          p0 = fast_exp2(fmaf(s0, a.scale_log2, -l0));
+          p1 = fast_exp2(fmaf(s1, a.scale_log2, -l1));
+        }
+      };
       // Query columns c with lo <= c < hi are live for this key row (causal
       // diagonal, ragged query tile, key row past the block).  Interior tiles
       // have every column live and skip the per-element mask.
@@ -529,10 +584,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           for (int e = 0; e < 32; e += 4) {
             // the same query indices in every lane: broadcast shared-memory reads
             const float4 l4 = *reinterpret_cast<const float4*>(lse_row + cbase + e);
-            pv[ch][e] = fast_exp2(fmaf(pv[ch][e], a.scale_log2, ofs(l4.x)));
-            pv[ch][e + 1] = fast_exp2(fmaf(pv[ch][e + 1], a.scale_log2, ofs(l4.y)));
-            pv[ch][e + 2] = fast_exp2(fmaf(pv[ch][e + 2], a.scale_log2, ofs(l4.z)));
-            pv[ch][e + 3] = fast_exp2(fmaf(pv[ch][e + 3], a.scale_log2, ofs(l4.w)));
+            form_p(pv[ch][e], pv[ch][e + 1], l4.x, l4.y, pv[ch][e], pv[ch][e + 1]);
+            form_p(pv[ch][e + 2], pv[ch][e + 3], l4.z, l4.w, pv[ch][e + 2], pv[ch][e + 3]);
           }
         } else {
 #pragma unroll
@@ -540,11 +593,13 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             const float4 l4 = *reinterpret_cast<const float4*>(lse_row + cbase + e);
             const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 4; u += 2) {
               const int c = cbase + e + u;
               // masked columns may hold statistics of other rows or padding: select
-              const float x = fast_exp2(fmaf(pv[ch][e + u], a.scale_log2, ofs(lv[u])));
+              float x, y;
+              form_p(pv[ch][e + u], pv[ch][e + u + 1], lv[u], lv[u + 1], x, y);
               pv[ch][e + u] = (c >= lo && c < hi) ? x : 0.f;
+              pv[ch][e + u + 1] = (c + 1 >= lo && c + 1 < hi) ? y : 0.f;
             }
           }
         }
@@ -570,6 +625,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         break;
       }
       tc_fence_after();
+      float2 ds_sum[2] = {};  // BIAS: this row's sum of dS
       uint32_t dpv2[C::GCH][32];
 #pragma unroll
       for (int ch = 0; ch < C::GCH; ++ch) tmem_ld32(tbase + t_lane + C::R1 + grp * C::GW + ch * 32, dpv2[ch]);
@@ -591,6 +647,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             // masked columns: p is 0 and D may be another row's or padding
             ds[u] = unmasked ? x : (p != 0.f ? x : 0.f);
             if constexpr (BIAS) pv[ch][e + u] = ds[u];  // kept for the bias gradient
+          }
+          if constexpr (BIAS) {
+            ds_sum[0] = __fadd2_rn(ds_sum[0], make_float2(ds[0], ds[1]));
+            ds_sum[1] = __fadd2_rn(ds_sum[1], make_float2(ds[2], ds[3]));
           }
           dsk[e / 2] = pack_bf16(ds[0], ds[1]);
           dsk[e / 2 + 1] = pack_bf16(ds[2], ds[3]);
@@ -617,51 +677,60 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
 
       // ---- the bias gradient's sums of dS, while dQ is computed
       if constexpr (BIAS) {
-        if (tb.y >= 0) {
-          if (tb.y != sum_ivl || (tb.w >> 5) != sum_block) {
+        const BwdPiece& place = sBias[(i % C::NS) * 8 + 7];
+        const int head = place.code, ivl = PieceCode::interval(piece->code);
+        auto warp_sum = [](float x) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          return x;
+        };
+        if (kind == kPieceConst) {
+          if (ivl != sum_ivl || (head >> 5) != sum_block) {
             flush_sum();
-            sum_ivl = tb.y;
-            sum_block = tb.w >> 5;
+            sum_ivl = ivl;
+            sum_block = head >> 5;
           }
-          float s4[4] = {};
+          const float s = warp_sum((ds_sum[0].x + ds_sum[0].y) + (ds_sum[1].x + ds_sum[1].y));
+          if (lane == (head & 31)) run_sum += s;
+        } else if (kind == kPieceStep) {
+          const uint32_t past = past_step();
+          float s2[2] = {}, p2[2] = {};
 #pragma unroll
-          for (int ch = 0; ch < C::GCH; ++ch)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s4[e & 3] += pv[ch][e];
-          float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == (tb.w & 31)) run_sum += s;
+          for (int e = 0; e < 32; ++e) {
+            if (past >> e & 1)
+              p2[e & 1] += pv[0][e];
+            else
+              s2[e & 1] += pv[0][e];
+          }
+          const float before = warp_sum(s2[0] + s2[1]), after = warp_sum(p2[0] + p2[1]);
+          if (lane < 2) atomicAdd(part + head * a.bias.intervals + ivl + lane, lane ? after : before);
         } else {
-          float* ph = part + tb.w * a.bias.intervals;
+          float* ph = part + head * a.bias.intervals;
+          // lane l, column c: distance at place base + c - l
+          const uint8_t* at = a.bias.interval + place.place + 32 * (grp - quarter);
+          float acc = 0.f, fin = 0.f;
 #pragma unroll
-          for (int ch = 0; ch < C::GCH; ++ch) {
-            // lane l, column c: distance at place base + c - l
-            const uint8_t* at = a.bias.interval + tb.z + grp * C::GW + ch * 32 - quarter * 32;
-            float acc = 0.f, fin = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              acc += pv[ch][c];
-              const float done = __shfl_sync(0xffffffffu, acc, 31);  // distance base + c - 31
-              if (lane == c) fin = done;
-              acc = __shfl_up_sync(0xffffffffu, acc, 1);
-              if (lane == 0) acc = 0.f;
-            }
-            // now lane l holds the sums of distances base + l - 31 (fin) and,
-            // l > 0, base + 32 - l (acc); intervals are runs of lanes
-            auto add_runs = [&](float v, int id) {
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const float v2 = __shfl_down_sync(0xffffffffu, v, o);
-                const int id2 = __shfl_down_sync(0xffffffffu, id, o);
-                if (lane + o < 32 && id2 == id) v += v2;
-              }
-              const int before = __shfl_up_sync(0xffffffffu, id, 1);
-              if (lane == 0 || before != id) atomicAdd(ph + id, v);
-            };
-            add_runs(fin, at[lane - 31]);
-            add_runs(acc, at[32 - (lane > 0 ? lane : 1)]);
+          for (int c = 0; c < 32; ++c) {
+            acc += pv[0][c];
+            const float done = __shfl_sync(0xffffffffu, acc, 31);  // distance base + c - 31
+            if (lane == c) fin = done;
+            acc = __shfl_up_sync(0xffffffffu, acc, 1);
+            if (lane == 0) acc = 0.f;
           }
+          // now lane l holds the sums of distances base + l - 31 (fin) and,
+          // l > 0, base + 32 - l (acc); intervals are runs of lanes
+          auto add_runs = [&](float v, int id) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const float v2 = __shfl_down_sync(0xffffffffu, v, o);
+              const int id2 = __shfl_down_sync(0xffffffffu, id, o);
+              if (lane + o < 32 && id2 == id) v += v2;
+            }
+            const int before = __shfl_up_sync(0xffffffffu, id, 1);
+            if (lane == 0 || before != id) atomicAdd(ph + id, v);
+          };
+          add_runs(fin, at[lane - 31]);
+          add_runs(acc, at[32 - (lane > 0 ? lane : 1)]);
         }
       }
 
@@ -934,7 +1003,7 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
   if ((e = cudaMemsetAsync(dk_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess ||
       (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess)
     return cuda_fail(e);
-  if ((st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream)) != LOONG_OK) return st;
+  if ((st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream, bias != nullptr)) != LOONG_OK) return st;
   st = bias ? launch_bwd_b<true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,
                                  dbias_part)
             : launch_bwd_b<false>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, nullptr,

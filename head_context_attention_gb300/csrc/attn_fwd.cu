@@ -73,6 +73,10 @@ struct FwdCfg {
   static_assert(NINFO >= NS + 2, "a tile's entry is read before it is rewritten");
   static constexpr int SMEM_BYTES = (NQ + 2 * NS) * TILE_BYTES + NBARS * 8 + 1024;
   static constexpr int THREADS = 320;
+  // Bias: a third whole warpgroup (two of its warps idle), whose registers go to
+  // the softmax warps: 256 * 216 + 128 * 72 = 384 * 168, what the block starts with.
+  static constexpr int BIAS_THREADS = 384, BIAS_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
+  static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= BIAS_THREADS * BIAS_REGS, "register split");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int buf) { return static_cast<uint32_t>(buf) * 128u; }
   __host__ __device__ static constexpr uint32_t O_COL(int h) { return NSB * 128u + static_cast<uint32_t>(h) * D; }
@@ -107,24 +111,40 @@ constexpr float kPBias = 7.0f;
 constexpr float kSumBound = 32768.0f;
 static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bound = 2^(bias + threshold)");
 
-// BIAS adds bias(q - k) of the query's head to every scaled score.  Most tiles
-// lie inside one interval of distances: their bias is a constant that goes into
-// the exponent's offset and the tile maximum, at no cost per score.  In a tile
-// that an interval boundary crosses, each score gets its own value from the
-// bias by distance (in units of the unscaled score), where neighbouring rows
-// read neighbouring words.  A bias of -inf masks like a causal mask; a row that
-// it leaves nothing gets O = 0 and LSE = -inf.
+// BIAS adds bias(q - k) of the query's head to every scaled score.  Every tile
+// has a constant (the bias at its middle), which goes into the exponent's offset
+// and the tile maximum, at no work per score; a tile inside one interval of
+// distances needs no more.  In a tile that interval boundaries cross, the scores
+// get the difference to that constant in tensor memory before the softmax reads
+// them, per piece of 32 rows (a softmax warp's) by 32 keys, whose distances span
+// 63 values: a piece inside one interval takes one difference (none where it is
+// 0); in a piece that a single boundary crosses, a score takes one of two by the
+// column at which its row passes the boundary; with more boundaries each score
+// takes its own from the bias by distance, where neighbouring rows read
+// neighbouring words.  (Adding them in registers, with a row's 128 scores live,
+// spilled and slowed every tile by 10 %.)  Differences stand in units of the
+// unscaled score.  The producer looks the tile and its seven kinds of piece up
+// (pieces on one diagonal are alike) a tile ahead.  A bias of -inf masks like a
+// causal mask; a row that it leaves nothing gets O = 0 and LSE = -inf.
+struct FwdPiece {
+  float lo[2], hi[2];  // head slots 0 and 1: the difference before and, kPieceStep, from the boundary on
+  int kind;            // PieceKind
+  int step;            // kPieceStep: row r of the piece has passed the boundary up to column r + step
+  int pad[2];
+};
+
 template <int D, bool STEP, bool BIAS>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::THREADS, 1)
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
   using C = FwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  // BIAS, per tile: the constant bias of head slots 0 and 1 in log2 units, and
-  // whether the tile is crossed by an interval boundary
-  __shared__ float4 tile_bias[BIAS ? C::NINFO : 1];
+  // BIAS, per tile: piece diagonal i < 7 (rows 32 (i - 3) ahead of the keys), and
+  // as entry 7 the tile as a whole, its constant in `hi` and, in log2 units, `lo`
+  __shared__ FwdPiece piece_bias[BIAS ? C::NINFO : 1][8];
+  __shared__ uint64_t bias_full[BIAS ? C::NINFO : 1];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -192,6 +212,8 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(&p_full[sb], 4);
     }
     for (int h = 0; h < 2; ++h) mbar_init(&pv_done[h], 1);
+    if constexpr (BIAS)
+      for (int e = 0; e < C::NINFO; ++e) mbar_init(&bias_full[e], 1);
     mbar_init(o_final, 1);
     mbar_init(drain, 1);
     abort_sh = 0;
@@ -210,23 +232,49 @@ __global__ void __launch_bounds__(320, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = tmem_base_sh;
+  if constexpr (BIAS) {
+    if (warp >= 8) regs_dec<C::OTHER_REGS>();
+  }
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      mbar_expect_tx(q_full, C::NQ * C::TILE_BYTES);
-      for (int h = 0; h < C::NQ; ++h) {
-        int hc;
-        const int64_t qr64 = a.lay.view_row(b, q0, h ? head1 : head0, a.hq, hc);
-        // checked build: the tile starts inside the tensor (TMA fills rows past its end with zeros)
-        in_bounds(qr64 >= 0 && qr64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
-        const int qr = static_cast<int>(qr64);
-        for (int at = 0; at < C::ATOMS; ++at)
-          tma_load_3d(sQ + h * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, q_full, at * 64, hc, qr);
+    if (BIAS || lane == 0) {  // lane 0 issues; with a bias the other lanes look pieces up
+      const bool leader = lane == 0;
+      auto all = [&](bool x) { return BIAS ? __all_sync(0xffffffffu, x) != 0 : x; };
+      if (leader) {
+        mbar_expect_tx(q_full, C::NQ * C::TILE_BYTES);
+        for (int h = 0; h < C::NQ; ++h) {
+          int hc;
+          const int64_t qr64 = a.lay.view_row(b, q0, h ? head1 : head0, a.hq, hc);
+          // checked build: the tile starts inside the tensor (TMA fills rows past its end with zeros)
+          in_bounds(qr64 >= 0 && qr64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
+          const int qr = static_cast<int>(qr64);
+          for (int at = 0; at < C::ATOMS; ++at)
+            tma_load_3d(sQ + h * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, q_full, at * 64, hc, qr);
+        }
       }
       int jk = 0, jv = 0;
       const int c_q = block_owner(g, bq);  // the query tile's ring rank
-      for (int j = 0; j < n; ++j, walk.advance()) {
+      // lanes 0-6: a piece diagonal of the tile the walk stands at, lane 7: the tile
+      FwdPiece piece;
+      int code = 0;
+      auto look_up = [&]() {
+        if constexpr (BIAS) {
+          if (lane < 8) {
+            const int64_t i0 = a.bias.off + q0 - walk.k0() + (lane < 7 ? 32 * (lane - 3) : 0);  // the middle distance
+            // independent loads, waited for in the next trip
+            code = (lane < 7 ? a.bias.piece : a.bias.tile)[i0];
+            const float* l0 = a.bias.lut + head0 * a.bias.len + i0;
+            const float* l1 = a.bias.lut + head1 * a.bias.len + i0;
+            piece.lo[0] = l0[-31];
+            piece.lo[1] = l1[-31];
+            piece.hi[0] = l0[31];
+            piece.hi[1] = l1[31];
+          }
+        }
+      };
+      look_up();
+      for (int j = 0; j < n; ++j) {
         const int s = j % C::NS;
         const int u = j / C::NS;
         int kvc;
@@ -234,35 +282,47 @@ __global__ void __launch_bounds__(320, 1)
                                        : a.lay.view_row(b, walk.k0(), kvh, a.hkv, kvc);
         in_bounds(k064 >= 0 && k064 < a.lay.view_rows(a.batch) && kvc >= 0 && kvc < a.lay.view_heads(a.hkv), a.err);
         const int k0 = static_cast<int>(k064);
-        float4 tb;
-        if constexpr (BIAS) {
-          const int64_t i0 = a.bias.off + q0 - walk.k0();  // place of distance q0 - k0
-          const bool mixed = a.bias.interval[i0 - (kTile - 1)] != a.bias.interval[i0 + (kTile - 1)];
-          tb.x = mixed ? 0.f : a.bias.lut[head0 * a.bias.len + i0] * a.scale_log2;
-          tb.y = mixed ? 0.f : a.bias.lut[head1 * a.bias.len + i0] * a.scale_log2;
-          tb.z = mixed ? 1.f : 0.f;
-          tb.w = 0.f;
+        walk.advance();  // to tile j + 1, if there is one
+        if (j >= C::NS && !all(mbar_wait(&k_empty[s], (u - 1) & 1, abort_flag, a.err))) break;
+        if (leader) {
+          mbar_expect_tx(&k_full[s], C::TILE_BYTES);
+          for (int at = 0; at < C::ATOMS; ++at)
+            tma_load_3d(sK + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmK, &k_full[s], at * 64, kvc, k0);
         }
-        if (j >= C::NS && !mbar_wait(&k_empty[s], (u - 1) & 1, abort_flag, a.err)) break;
-        // written before the tile's arrival, so whoever waited for its scores sees it
-        if constexpr (BIAS) tile_bias[j % C::NINFO] = tb;
-        mbar_expect_tx(&k_full[s], C::TILE_BYTES);
-        for (int at = 0; at < C::ATOMS; ++at)
-          tma_load_3d(sK + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmK, &k_full[s], at * 64, kvc, k0);
         ++jk;
-        if (j >= C::NS && !mbar_wait(&v_empty[s], (u - 1) & 1, abort_flag, a.err)) break;
-        mbar_expect_tx(&v_full[s], C::TILE_BYTES);
-        for (int at = 0; at < C::ATOMS; ++at)
-          tma_load_3d(sV + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmV, &v_full[s], at * 64, kvc, k0);
+        if constexpr (BIAS) {
+          piece.kind = PieceCode::kind(code);
+          piece.step = PieceCode::step(code);
+          const bool crossed = __shfl_sync(0xffffffffu, piece.kind, 7) != kPieceConst;
+#pragma unroll
+          for (int hs = 0; hs < 2; ++hs) {
+            float mid = __shfl_sync(0xffffffffu, piece.lo[hs], 7);
+            if (crossed && !isfinite(mid)) mid = 0.f;  // differences to it have to mean something
+            piece.lo[hs] = lane == 7 ? mid * a.scale_log2 : piece.lo[hs] - mid;
+            piece.hi[hs] = lane == 7 ? mid : piece.hi[hs] - mid;
+          }
+          if (lane < 8) piece_bias[j % C::NINFO][lane] = piece;
+          __syncwarp();
+          if (leader) mbar_arrive(&bias_full[j % C::NINFO]);
+          if (j + 1 < n) look_up();
+        }
+        if (j >= C::NS && !all(mbar_wait(&v_empty[s], (u - 1) & 1, abort_flag, a.err))) break;
+        if (leader) {
+          mbar_expect_tx(&v_full[s], C::TILE_BYTES);
+          for (int at = 0; at < C::ATOMS; ++at)
+            tma_load_3d(sV + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmV, &v_full[s], at * 64, kvc, k0);
+        }
         ++jv;
       }
       // Let every copy this thread issued land before the CTA can exit.
-      mbar_drain(q_full, 0, a.err);
-      for (int s = 0; s < C::NS; ++s) {
-        const int nk = jk > s ? (jk - 1 - s) / C::NS + 1 : 0;
-        const int nv = jv > s ? (jv - 1 - s) / C::NS + 1 : 0;
-        if (nk) mbar_drain(&k_full[s], (nk - 1) & 1, a.err);
-        if (nv) mbar_drain(&v_full[s], (nv - 1) & 1, a.err);
+      if (leader) {
+        mbar_drain(q_full, 0, a.err);
+        for (int s = 0; s < C::NS; ++s) {
+          const int nk = jk > s ? (jk - 1 - s) / C::NS + 1 : 0;
+          const int nv = jv > s ? (jv - 1 - s) / C::NS + 1 : 0;
+          if (nk) mbar_drain(&k_full[s], (nk - 1) & 1, a.err);
+          if (nv) mbar_drain(&v_full[s], (nv - 1) & 1, a.err);
+        }
       }
     }
   } else if (warp == 9) {
@@ -335,7 +395,8 @@ __global__ void __launch_bounds__(320, 1)
       mma_commit_w(drain);
       mbar_drain(drain, 0, a.err);
     }
-  } else {
+  } else if (!BIAS || warp < 8) {
+    if constexpr (BIAS) regs_inc<C::SOFTMAX_REGS>();
     // ------------------------------------------------------------ softmax
     const int h = warp >> 2;
     const int quarter = warp & 3;
@@ -343,9 +404,6 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tO = tbase + t_lane + C::O_COL(h);
     const float sl2 = a.scale_log2;
-    // BIAS: the bias of this row's query at distance off from the row
-    const float* lut_row =
-        BIAS ? a.bias.lut + static_cast<int64_t>(h ? head1 : head0) * a.bias.len + a.bias.off + q0 + row : nullptr;
     float m_run = -INFINITY;
     float l_run = 0.f;
     bool ok = true;
@@ -353,36 +411,74 @@ __global__ void __launch_bounds__(320, 1)
       // Lanes leave together so the .sync.aligned TMEM accesses never diverge.
       const int J = 2 * j + h;  // this tile's MMA job and its score buffer
       const uint32_t tS = tbase + t_lane + C::S_COL(J % C::NSB);
+      // BIAS: the tile's constant (log2 units), whether a boundary crosses it, and
+      // which of this warp's pieces then add something
+      const int e = j % C::NINFO;
+      float tile_b = 0.f;
+      bool crossed = false;
+      unsigned needs = 0;
+      if constexpr (BIAS) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bias_full[e], (j / C::NINFO) & 1, abort_flag, a.err))) {
+          ok = false;
+          break;
+        }
+        tile_b = piece_bias[e][7].lo[h];
+        crossed = piece_bias[e][7].kind != kPieceConst;
+        if (crossed) {
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb) {
+            const FwdPiece& pb = piece_bias[e][quarter - cb + 3];
+            needs |= pb.kind != kPieceConst || pb.lo[h] != 0.f ? 1u << cb : 0u;
+          }
+        }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[J % C::NSB], (J / C::NSB) & 1, abort_flag, a.err))) {
         ok = false;
         break;
       }
       tc_fence_after();
+      if (BIAS && crossed) {
+        const float* lp = a.bias.lut + static_cast<int64_t>(h ? head1 : head0) * a.bias.len + a.bias.off + q0 + row -
+                          walk.k0();
+#pragma unroll 1
+        for (int cb = 0; cb < 4; ++cb) {
+          if (!(needs >> cb & 1)) continue;
+          uint32_t x[32];
+          tmem_ld32(tS + cb * 32, x);
+          const FwdPiece& pb = piece_bias[e][quarter - cb + 3];
+          const float lo = pb.lo[h], hi = pb.hi[h];
+          float2 add[16];
+          if (pb.kind == kPieceMixed) {  // the kinds are uniform over the warp
+            const float mid = piece_bias[e][7].hi[h];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              add[i] = make_float2(__ldg(lp - (cb * 32 + 2 * i)) - mid, __ldg(lp - (cb * 32 + 2 * i + 1)) - mid);
+          } else {
+            const int t = lane + pb.step;  // columns up to t are past the boundary
+            const uint32_t past = pb.kind == kPieceConst || t < 0 ? 0u : 0xffffffffu >> (31 - min(t, 31));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              add[i] = make_float2(past >> (2 * i) & 1 ? hi : lo, past >> (2 * i + 1) & 1 ? hi : lo);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = __fadd2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), add[i]);
+            x[2 * i] = __float_as_uint(y.x);
+            x[2 * i + 1] = __float_as_uint(y.y);
+          }
+          tmem_st32(tS + cb * 32, x);
+        }
+        tmem_wait_st();
+      }
       uint32_t sr[4][32];
       const int klen = walk.klen();
       const bool dg = walk.diag();
-      float tile_b = 0.f;  // the tile's constant bias (log2 units)
-      bool mixed = false;
-      if constexpr (BIAS) {
-        const float4 tb = tile_bias[j % C::NINFO];
-        tile_b = h ? tb.y : tb.x;
-        mixed = tb.z != 0.f;
-      }
       // the tile's scores, masked columns at -inf (read again by the full path)
       auto load_s = [&]() {
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) tmem_ld32(tS + cb * 32, sr[cb]);
         tmem_wait_ld();
-        if constexpr (BIAS) {
-          if (mixed) {
-            const float* lp = lut_row - walk.k0();
-#pragma unroll
-            for (int cb = 0; cb < 4; ++cb)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                sr[cb][i] = __float_as_uint(__uint_as_float(sr[cb][i]) + __ldg(lp - (cb * 32 + i)));
-          }
-        }
         if (dg || klen < kTile) {
           const int lim = dg ? min(row, klen - 1) : klen - 1;
 #pragma unroll
@@ -625,6 +721,13 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   auto kern = ring_fwd_kernel<D, STEP, BIAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
+  constexpr int threads = BIAS ? C::BIAS_THREADS : C::THREADS;
+  if constexpr (BIAS) {
+    // the register split draws on what the block starts with: less would wait for ever
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return cuda_fail(e);
+    if (at.numRegs < C::BIAS_REGS) return LOONG_ERR_UNSUPPORTED;
+  }
   const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring) *
                        a.ring.ntile * a.npairs;
   if (grid <= 0 || grid > 0x7fffffff) return LOONG_ERR_INVALID_ARG;
@@ -632,7 +735,7 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
     a.t_begin = 0;
     a.t_end = d.cp;
     record_start(stream);
-    kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
+    kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
     record_stop(stream);
     return check_launch();
   }
@@ -653,7 +756,7 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
       a.t_begin = t;
       a.t_end = t + 1;
       a.kv_held = buf >= 0;
-      kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(mq, buf >= 0 ? mkr[buf] : mk,
+      kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, buf >= 0 ? mkr[buf] : mk,
                                                                                buf >= 0 ? mvr[buf] : mv, a);
       return check_launch();
     });
@@ -665,7 +768,7 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
     NvtxRange step("fwd ring step %d", t);
     a.t_begin = t;
     a.t_end = t + 1;
-    kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
+    kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
     if ((st = check_launch()) != LOONG_OK) return st;
   }
   record_stop(stream);

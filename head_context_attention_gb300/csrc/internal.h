@@ -94,9 +94,26 @@ FwdWsLayout fwd_ws_layout(const loong_attn_desc& d);
 struct BiasView {
   const float* lut = nullptr;         // [hq][len], bias / softmax scale
   const uint8_t* interval = nullptr;  // [len], ascending
+  const int* piece = nullptr;         // [len], PieceCode of the places up to 31 away
+  const int* tile = nullptr;          // [len], of those up to 127 away
   int64_t len = 0;
   int off = 0;
   int intervals = 0;
+};
+
+// What a run of places [at - reach, at + reach] looks like, in one word.
+enum PieceKind : int {
+  kPieceConst = 0,  // one interval
+  kPieceStep = 1,   // two
+  kPieceMixed = 2,  // more
+};
+struct PieceCode {
+  static __host__ __device__ int make(int kind, int first_interval, int step) {
+    return kind | first_interval << 2 | (step + 128) << 10;
+  }
+  static __host__ __device__ int kind(int c) { return c & 3; }
+  static __host__ __device__ int interval(int c) { return c >> 2 & 255; }  // of the first place
+  static __host__ __device__ int step(int c) { return (c >> 10) - 128; }   // kPieceStep: at - the second's first place
 };
 
 // Kernel launchers (asynchronous on `stream`).
@@ -147,8 +164,8 @@ inline int stat_block_pad(int blk) { return (blk + 3) & ~3; }
 inline int64_t stat_row_len(const RingGeom& g) {
   return static_cast<int64_t>(g.nblocks) * stat_block_pad(g.blk) + kTile;
 }
-// With o_res, D = rowsum(dO * (O + O_res)).
+// With o_res, D = rowsum(dO * (O + O_res)).  negate: the LSE part as -LSE*log2(e).
 int launch_bwd_rowstats(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout,
-                        const float* lse, float* stats, cudaStream_t stream);
+                        const float* lse, float* stats, cudaStream_t stream, bool negate = false);
 
 }  // namespace loong

@@ -346,6 +346,19 @@ __host__ __device__ constexpr int v16_shift(uint32_t amax_bits) {
   return e < -100 ? -100 : (e > 114 ? 114 : e);
 }
 
+// ------------------------------------------------------------- registers
+// The executing warpgroup's registers per thread, from now on (every warp of
+// the warpgroup calls; an increase waits for registers other warpgroups of the
+// block have given up).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- math
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;

@@ -41,13 +41,12 @@ struct BucketMap {
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// One thread per distance: its interval by binary search, then the bias of
-// heads blockIdx.y, blockIdx.y + gridDim.y, ...; consecutive threads write
-// consecutive words.
+// One thread per distance: its interval and its pieces' by binary search, then
+// the bias of heads blockIdx.y, blockIdx.y + gridDim.y, ...; consecutive threads
+// write consecutive words.
 __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ BucketMap m,
-                                                          const __nv_bfloat16* __restrict__ table, int hq, int64_t len,
-                                                          int off, float inv_scale, float* __restrict__ lut,
-                                                          uint8_t* __restrict__ interval) {
+                                                          const __nv_bfloat16* __restrict__ table, int hq,
+                                                          float inv_scale, BiasView out) {
   __shared__ int bounds[kMaxIntervals];
   __shared__ uint8_t bucket[kMaxIntervals];
   for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
@@ -56,21 +55,35 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
   }
   __syncthreads();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= len) return;
-  const int n = static_cast<int>(i) - off;
-  int lo = 0, hi = m.intervals - 1;  // the number of bounds <= n
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (bounds[mid] <= n)
-      lo = mid + 1;
-    else
-      hi = mid;
+  if (i >= out.len) return;
+  const int n = static_cast<int>(i) - out.off;
+  auto interval_of = [&](int d) {  // the number of bounds <= d
+    int lo = 0, hi = m.intervals - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (bounds[mid] <= d)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
+  const int at = interval_of(n);
+  if (blockIdx.y == 0) {
+    const_cast<uint8_t*>(out.interval)[i] = static_cast<uint8_t>(at);
+    auto code = [&](int reach) {
+      const int lo = interval_of(n - reach), hi = interval_of(n + reach);
+      const int kind = min(hi - lo, static_cast<int>(kPieceMixed));
+      return PieceCode::make(kind, lo, kind == kPieceStep ? n - bounds[lo] : 0);
+    };
+    const_cast<int*>(out.piece)[i] = code(31);
+    const_cast<int*>(out.tile)[i] = code(127);
   }
-  if (blockIdx.y == 0) interval[i] = static_cast<uint8_t>(lo);
-  const __nv_bfloat16* row = table + static_cast<int64_t>(bucket[lo]) * hq;
+  const __nv_bfloat16* row = table + static_cast<int64_t>(bucket[at]) * hq;
+  float* lut = const_cast<float*>(out.lut);
   for (int h = blockIdx.y; h < hq; h += gridDim.y) {
     const float v = __bfloat162float(row[h]);
-    lut[h * len + i] = v <= kMaskBelow ? -INFINITY : v * inv_scale;
+    lut[h * out.len + i] = v <= kMaskBelow ? -INFINITY : v * inv_scale;
   }
 }
 
@@ -144,7 +157,7 @@ BucketMap bucket_map(const loong_rel_bias& b) {
 // The workspace: the plain pass's first, then the bias by distance and, for the
 // backward, the gradient's parts and their sums.
 struct BiasWs {
-  size_t lut, interval, part, sums, total;
+  size_t lut, interval, piece, tile, part, sums, total;
   size_t part_bytes;
   int off;
   int64_t len;
@@ -160,6 +173,10 @@ BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
   at += up256(static_cast<size_t>(d.hq) * w.len * 4);
   w.interval = at;
   at += up256(static_cast<size_t>(w.len));
+  w.piece = at;
+  at += up256(static_cast<size_t>(w.len) * 4);
+  w.tile = at;
+  at += up256(static_cast<size_t>(w.len) * 4);
   if (pass == 1) {
     const size_t width = static_cast<size_t>(d.hq / d.hkv) * (b.num_bounds + 1);
     w.part = at;
@@ -175,19 +192,19 @@ BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
 int expand(const loong_attn_desc& d, const loong_rel_bias& b, const BucketMap& m, const BiasWs& w, void* ws,
            BiasView* view, cudaStream_t stream) {
   uint8_t* base = static_cast<uint8_t*>(ws);
-  float* lut = reinterpret_cast<float*>(base + w.lut);
-  uint8_t* interval = base + w.interval;
+  view->lut = reinterpret_cast<float*>(base + w.lut);
+  view->interval = base + w.interval;
+  view->piece = reinterpret_cast<int*>(base + w.piece);
+  view->tile = reinterpret_cast<int*>(base + w.tile);
+  view->len = w.len;
+  view->off = w.off;
+  view->intervals = m.intervals;
   const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.head_dim));
   const int64_t nb = (w.len + kThreads - 1) / kThreads;
   // short sequences spread the heads over blocks as well
   const unsigned ny = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(d.hq, 608 / nb)));
   expand_kernel<<<dim3(static_cast<unsigned>(nb), ny), kThreads, 0, stream>>>(
-      m, static_cast<const __nv_bfloat16*>(b.table), d.hq, w.len, w.off, 1.0f / scale, lut, interval);
-  view->lut = lut;
-  view->interval = interval;
-  view->len = w.len;
-  view->off = w.off;
-  view->intervals = m.intervals;
+      m, static_cast<const __nv_bfloat16*>(b.table), d.hq, 1.0f / scale, *view);
   return check_launch();
 }
 

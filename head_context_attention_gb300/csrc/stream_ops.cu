@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(256) bwd_rowstats_kernel(
     const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ o_res,
     const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse, float* __restrict__ lse2,
     float* __restrict__ dstat, int64_t rows, int S, int hq, int blk, int blk_pad, int64_t stat_len, Layout lay,
-    unsigned* err) {
+    float sign, unsigned* err) {
   constexpr int TPR = D / 8;         // threads per row
   constexpr int RPB = 256 / TPR;     // rows (tokens) per block and pass
   const int h = blockIdx.y;
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(256) bwd_rowstats_kernel(
         dstat[pos] = acc;
         // a row that a bias of -inf left nothing: its P must come out 0
         const float l = lse[bh * S + s];
-        lse2[pos] = l == -INFINITY ? INFINITY : l * kLog2e;
+        lse2[pos] = l == -INFINITY ? sign * INFINITY : l * (sign * kLog2e);
       }
     }
   }
@@ -556,7 +556,7 @@ int launch_headctx_pack(int n, int64_t batch, int cp, int P, int64_t s_local, co
 }
 
 int launch_bwd_rowstats(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout,
-                        const float* lse, float* stats, cudaStream_t stream) {
+                        const float* lse, float* stats, cudaStream_t stream, bool negate) {
   const RingGeom g = ring_geom(d);
   const int64_t rows = d.batch * d.seqlen * d.hq;
   const int64_t stat_len = stat_row_len(g);
@@ -578,10 +578,10 @@ int launch_bwd_rowstats(const loong_attn_desc& d, const void* o, const void* o_r
                   static_cast<unsigned>(d.hq), static_cast<unsigned>(d.batch));
   if (d.head_dim == 128)
     bwd_rowstats_kernel<128><<<grid, 256, 0, stream>>>(po, pr, pd, lse, lse2, dstat, rows, d.seqlen, d.hq, g.blk,
-                                                       bp, stat_len, layout_of(d), err);
+                                                       bp, stat_len, layout_of(d), negate ? -1.f : 1.f, err);
   else if (d.head_dim == 64)
     bwd_rowstats_kernel<64><<<grid, 256, 0, stream>>>(po, pr, pd, lse, lse2, dstat, rows, d.seqlen, d.hq, g.blk,
-                                                      bp, stat_len, layout_of(d), err);
+                                                      bp, stat_len, layout_of(d), negate ? -1.f : 1.f, err);
   else
     return LOONG_ERR_UNSUPPORTED;
   return check_launch();
