@@ -1000,8 +1000,12 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
   int st;
   cudaError_t e = cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  if ((e = cudaMemsetAsync(dk_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess ||
-      (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess)
+  // FUSED walks of at most kFlush (tile, head) pairs never touch the dK, dV accumulators
+  const RingGeom g = ring_geom(d);
+  const int64_t longest = static_cast<int64_t>(d.hq / d.hkv) * g.nblocks * g.ntile;
+  if ((step || longest > kFlush) &&
+      ((e = cudaMemsetAsync(dk_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess ||
+       (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess))
     return cuda_fail(e);
   if ((st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream, bias != nullptr)) != LOONG_OK) return st;
   st = bias ? launch_bwd_b<true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,

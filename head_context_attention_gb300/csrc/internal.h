@@ -118,7 +118,7 @@ struct PieceCode {
 
 // Kernel launchers (asynchronous on `stream`).
 // Query rows of ring ranks [rank_begin, rank_end) only (all of them: 0, cp).
-// The forward first writes V's fp16 copy into sc.v16.
+// The forward first writes V's fp16 copy into sc.v16 (with a bias, *sc.v_amax is 0 already).
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
                float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin = 0, int rank_end = -1,
                const BiasView* bias = nullptr);
@@ -142,7 +142,8 @@ inline int64_t bwd_blocks(const loong_attn_desc& d) {
   return d.batch * d.hkv * static_cast<int64_t>(g.nblocks) * g.ntile;
 }
 // max |V| into *amax (two launches: the maximum, then V * 2^-e as fp16 into v16).
-int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream);
+// cleared: *amax is 0 already.
+int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream, bool cleared = false);
 
 int launch_fill_f32(float* p, int64_t n, float value, cudaStream_t stream);
 // One CTA whose bounded mbarrier wait has nothing to wait for (selftest.cu).

@@ -43,10 +43,16 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // One thread per distance: its interval and its pieces' by binary search, then
 // the bias of heads blockIdx.y, blockIdx.y + gridDim.y, ...; consecutive threads
-// write consecutive words.
+// write consecutive words.  The same launch clears the words that the pass adds
+// into: max |V| (forward), the gradient's parts and tickets (backward).
 __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ BucketMap m,
                                                           const __nv_bfloat16* __restrict__ table, int hq,
-                                                          float inv_scale, BiasView out) {
+                                                          float inv_scale, BiasView out,
+                                                          uint4* __restrict__ zero, int64_t zero_vecs) {
+  const int64_t nthreads = static_cast<int64_t>(gridDim.x) * gridDim.y * kThreads;
+  for (int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x; z < zero_vecs;
+       z += nthreads)
+    zero[z] = make_uint4(0, 0, 0, 0);
   __shared__ int bounds[kMaxIntervals];
   __shared__ uint8_t bucket[kMaxIntervals];
   for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
@@ -89,10 +95,18 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
 
 // Sum of the backward's parts over warps, key tiles and sequences, in a fixed
 // order: block (kv head, split) adds its share of the (sequence, key tile)
-// pairs, 16 warps' numbers in 32 bits and those sums in 64.
-__global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const float* __restrict__ part, int64_t pairs, int nkt,
-                                                             int hkv, int width, double* __restrict__ sums) {
+// pairs, 16 warps' numbers in 32 bits and those sums in 64; the last block of a
+// kv head to finish (tickets, cleared by expand_kernel) adds the splits' sums and
+// then the intervals of every bucket.
+__global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const __grid_constant__ BucketMap m,
+                                                             const float* __restrict__ part, int64_t pairs, int nkt,
+                                                             int hkv, int group, double* __restrict__ sums,
+                                                             unsigned* __restrict__ ticket, int buckets,
+                                                             __nv_bfloat16* __restrict__ dtable) {
+  __shared__ bool last;
+  __shared__ double by_interval[kMaxIntervals];
   const int kvh = blockIdx.x;
+  const int width = group * m.intervals;
   const int64_t j0 = pairs * blockIdx.y / gridDim.y, j1 = pairs * (blockIdx.y + 1) / gridDim.y;
   for (int e = threadIdx.x; e < width; e += kThreads) {
     double acc = 0.0;
@@ -106,25 +120,27 @@ __global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const float* __rest
     }
     sums[(static_cast<int64_t>(blockIdx.y) * hkv + kvh) * width + e] = acc;
   }
-}
-
-// One block per head: the splits' sums by interval, then the intervals of every bucket.
-__global__ void __launch_bounds__(kThreads) dbias_out_kernel(const __grid_constant__ BucketMap m,
-                                                             const double* __restrict__ sums, int splits, int hq,
-                                                             int buckets, __nv_bfloat16* __restrict__ dtable) {
-  __shared__ double by_interval[kMaxIntervals];
-  const int h = blockIdx.x;
-  for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
-    double s = 0.0;
-    for (int sp = 0; sp < splits; ++sp) s += sums[(static_cast<int64_t>(sp) * hq + h) * m.intervals + i];
-    by_interval[i] = s;
-  }
+  __threadfence();
   __syncthreads();
-  for (int t = threadIdx.x; t < buckets; t += kThreads) {
-    double s = 0.0;
-    for (int i = 0; i < m.intervals; ++i)
-      if (m.bucket[i] == t) s += by_interval[i];
-    dtable[static_cast<int64_t>(t) * hq + h] = __float2bfloat16_rn(static_cast<float>(s));
+  if (threadIdx.x == 0) last = atomicAdd(ticket + kvh, 1u) == gridDim.y - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int g = 0; g < group; ++g) {
+    __syncthreads();  // the previous head's sums have been read
+    for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
+      const double* src = sums + static_cast<int64_t>(kvh) * width + g * m.intervals + i;
+      double s = 0.0;
+      for (unsigned sp = 0; sp < gridDim.y; ++sp) s += __ldcg(src + static_cast<int64_t>(sp) * hkv * width);
+      by_interval[i] = s;
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < buckets; t += kThreads) {
+      double s = 0.0;
+      for (int i = 0; i < m.intervals; ++i)
+        if (m.bucket[i] == t) s += by_interval[i];
+      dtable[(static_cast<int64_t>(t) * hkv + kvh) * group + g] = __float2bfloat16_rn(static_cast<float>(s));
+    }
   }
 }
 
@@ -157,8 +173,8 @@ BucketMap bucket_map(const loong_rel_bias& b) {
 // The workspace: the plain pass's first, then the bias by distance and, for the
 // backward, the gradient's parts and their sums.
 struct BiasWs {
-  size_t lut, interval, piece, tile, part, sums, total;
-  size_t part_bytes;
+  size_t lut, interval, piece, tile, zero, part, ticket, sums, total;
+  size_t zero_bytes;  // from `zero` on: the forward's max |V|; the backward's parts and tickets
   int off;
   int64_t len;
 };
@@ -177,11 +193,16 @@ BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
   at += up256(static_cast<size_t>(w.len) * 4);
   w.tile = at;
   at += up256(static_cast<size_t>(w.len) * 4);
-  if (pass == 1) {
+  if (pass == 0) {
+    w.zero = fwd_ws_layout(d).amax;
+    w.zero_bytes = 16;
+  } else {
     const size_t width = static_cast<size_t>(d.hq / d.hkv) * (b.num_bounds + 1);
-    w.part = at;
-    w.part_bytes = static_cast<size_t>(bwd_blocks(d)) * kBwdComputeWarps * width * 4;
-    at += up256(w.part_bytes);
+    w.zero = w.part = at;
+    at += up256(static_cast<size_t>(bwd_blocks(d)) * kBwdComputeWarps * width * 4);
+    w.ticket = at;
+    at += up256(static_cast<size_t>(d.hkv) * 4);
+    w.zero_bytes = at - w.zero;
     w.sums = at;
     at += up256(static_cast<size_t>(kSumSplits) * d.hkv * width * 8);
   }
@@ -204,7 +225,8 @@ int expand(const loong_attn_desc& d, const loong_rel_bias& b, const BucketMap& m
   // short sequences spread the heads over blocks as well
   const unsigned ny = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(d.hq, 608 / nb)));
   expand_kernel<<<dim3(static_cast<unsigned>(nb), ny), kThreads, 0, stream>>>(
-      m, static_cast<const __nv_bfloat16*>(b.table), d.hq, 1.0f / scale, *view);
+      m, static_cast<const __nv_bfloat16*>(b.table), d.hq, 1.0f / scale, *view,
+      reinterpret_cast<uint4*>(base + w.zero), static_cast<int64_t>(w.zero_bytes / 16));
   return check_launch();
 }
 
@@ -244,7 +266,7 @@ int loong_attn_bias_fwd(const loong_attn_desc* d, const loong_rel_bias* bias, co
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   BiasView view;
   if ((st = expand(*d, *bias, bucket_map(*bias), w, ws, &view, stream)) != LOONG_OK) return st;
-  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, &view);
+  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, &view);  // max |V| is cleared
 }
 
 int loong_attn_bias_bwd(const loong_attn_desc* d, const loong_rel_bias* bias, const void* q, const void* k,
@@ -275,19 +297,14 @@ int loong_attn_bias_bwd(const loong_attn_desc* d, const loong_rel_bias* bias, co
   const BucketMap m = bucket_map(*bias);
   BiasView view;
   if ((st = expand(*d, *bias, m, w, ws, &view, stream)) != LOONG_OK) return st;
-  cudaError_t e = cudaMemsetAsync(part, 0, w.part_bytes, stream);
-  if (e != cudaSuccess) return cuda_fail(e);
   if ((st = run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, &view, part)) != LOONG_OK) return st;
   const RingGeom g = ring_geom(*d);
   const int nkt = g.nblocks * g.ntile;
   const int64_t pairs = d->batch * nkt;
   const int splits = static_cast<int>(std::min<int64_t>(kSumSplits, pairs));
-  const int width = d->hq / d->hkv * m.intervals;
   dbias_sum_kernel<<<dim3(static_cast<unsigned>(d->hkv), static_cast<unsigned>(splits)), kThreads, 0, stream>>>(
-      part, pairs, nkt, d->hkv, width, sums);
-  if ((st = check_launch()) != LOONG_OK) return st;
-  dbias_out_kernel<<<static_cast<unsigned>(d->hq), kThreads, 0, stream>>>(m, sums, splits, d->hq, bias->num_buckets,
-                                                                          static_cast<__nv_bfloat16*>(dtable));
+      m, part, pairs, nkt, d->hkv, d->hq / d->hkv, sums, reinterpret_cast<unsigned*>(base + w.ticket),
+      bias->num_buckets, static_cast<__nv_bfloat16*>(dtable));
   return check_launch();
 }
 

@@ -459,10 +459,12 @@ int launch_f32_to_bf16(const float* in, void* out, int64_t n, cudaStream_t strea
   return check_launch();
 }
 
-int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream) {
+int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream, bool cleared) {
   if (n <= 0 || n % 8) return LOONG_ERR_INVALID_ARG;
-  cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(unsigned), stream);
-  if (e != cudaSuccess) return cuda_fail(e);
+  if (!cleared) {
+    const cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(unsigned), stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   const int64_t nvec = n / 8;
   absmax_bf16_kernel<<<grid_for(nvec, 256, 8), 256, 0, stream>>>(static_cast<const uint4*>(v), nvec, amax);
   int st = check_launch();

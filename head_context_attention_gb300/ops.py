@@ -6,11 +6,15 @@ step of the computation runs in the library's kernels.  The library is loaded
 on first use; a missing library raises ``RuntimeError`` (there is no other
 implementation to fall back to).
 """
+import contextlib
 import ctypes
+import functools
 import math
 import os
 
 import torch
+
+from .inputs import Workload
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libloong_attn.so")
@@ -229,6 +233,9 @@ class RelBuckets:
             if len(bucket_of) != len(bounds) + 1:
                 raise ValueError("bucket_of needs one bucket for each of the len(bounds) + 1 intervals")
             self._bucket_of = (ctypes.c_int32 * len(bucket_of))(*[int(x) for x in bucket_of])
+        p32 = ctypes.POINTER(ctypes.c_int32)
+        self._struct = LoongRelBias(self.num_buckets, self.num_bounds, ctypes.cast(self._bounds, p32),
+                                    None if self._bucket_of is None else ctypes.cast(self._bucket_of, p32), None)
 
     @property
     def bounds(self):
@@ -239,10 +246,11 @@ class RelBuckets:
         return list(range(self.num_bounds + 1)) if self._bucket_of is None else list(self._bucket_of)
 
     def struct(self, table=None):
-        p32 = ctypes.POINTER(ctypes.c_int32)
-        return LoongRelBias(self.num_buckets, self.num_bounds, ctypes.cast(self._bounds, p32),
-                            None if self._bucket_of is None else ctypes.cast(self._bucket_of, p32),
-                            None if table is None else table.data_ptr())
+        b = LoongRelBias.from_buffer_copy(self._struct)
+        b.keep = self    # it points at this object's arrays
+        if table is not None:
+            b.table = table.data_ptr()
+        return b
 
 
 def log_buckets(num_buckets, max_distance, causal=True):
@@ -458,15 +466,36 @@ def _attn_shape(w, heads, layout):
     return (w.batch, w.seqlen, heads, w.head_dim)
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(device, stream):
-    """The calls below run on the tensors' device, on its current stream unless one is given."""
+    """The calls below run on the tensors' device, on its current stream unless
+    one is given: (what to enter, the stream).  Nothing to enter where both are
+    current already."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not {device}")
-    return torch.cuda.device(device), torch.cuda.current_stream(device) if stream is None else stream
+    if stream is None and device.index == torch.cuda.current_device():
+        return _NOTHING, torch.cuda.current_stream()
+    where = contextlib.ExitStack()
+    where.enter_context(torch.cuda.device(device))
+    stream = torch.cuda.current_stream(device) if stream is None else stream
+    where.enter_context(torch.cuda.stream(stream))
+    return where, stream
+
+
+@functools.lru_cache(maxsize=256)
+def _desc_kept(w, mode, layout):
+    return make_desc(w, mode, layout=layout)
+
+
+def _desc_of(w, mode, layout):
+    """make_desc for reading only: kept for a Workload, which cannot change."""
+    return _desc_kept(w, mode, layout) if type(w) is Workload else make_desc(w, mode, layout=layout)
 
 
 def _bias_problem(w, table, buckets, mode, layout):
-    desc, bias = make_desc(w, mode, layout=layout), buckets.struct(table)
+    desc, bias = _desc_of(w, mode, layout), buckets.struct(table)
     _check("loong_rel_bias_check", loong_rel_bias_check(desc, bias))
     _contiguous("table", table, (buckets.num_buckets, w.hq), torch.bfloat16, table.device)
     return desc, bias
@@ -479,8 +508,8 @@ def attn_bias_fwd(w, q, k, v, table, buckets, mode=MODE_FUSED, stream=None, layo
     desc, bias = _bias_problem(w, table, buckets, mode, layout)
     for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv)):
         _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, table.device)
-    device, stream = _on(table.device, stream)
-    with device, torch.cuda.stream(stream):
+    where, stream = _on(table.device, stream)
+    with where:
         o = torch.empty_like(q)
         o_res = torch.empty_like(q) if res else None
         lse = torch.empty((w.batch, w.hq, w.seqlen), dtype=torch.float32, device=q.device)
@@ -498,8 +527,8 @@ def attn_bias_bwd(w, q, k, v, o, lse, do, table, buckets, o_res=None, mode=MODE_
         if t is not None or n != "o_res":
             _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, table.device)
     _contiguous("lse", lse, (w.batch, w.hq, w.seqlen), torch.float32, table.device)
-    device, stream = _on(table.device, stream)
-    with device, torch.cuda.stream(stream):
+    where, stream = _on(table.device, stream)
+    with where:
         dq, dk, dv, dtable = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(table)
         ws = torch.empty(loong_attn_bias_workspace_size(desc, bias, 1), dtype=torch.uint8, device=q.device)
         loong_attn_bias_bwd(desc, bias, q, k, v, o, o_res, lse, do, dq, dk, dv, dtable, ws, stream)
@@ -514,19 +543,35 @@ class QkOpts:
                  interleaved=False, rot_scale=1.0):
         self.rot_dim = head_dim if rot_dim is None else int(rot_dim)
         self.norm = bool(norm)
-        self._inv = None
+        self._inv = self._formed = None
+        n = max(0, self.rot_dim // 2)
         if inv_freq is not None:
             inv = [float(x) for x in inv_freq]
-            if len(inv) != self.rot_dim // 2:
-                raise ValueError(f"inv_freq needs {self.rot_dim // 2} values")
-            self._inv = (ctypes.c_double * max(1, len(inv)))(*inv)
+            if len(inv) != n:
+                raise ValueError(f"inv_freq needs {n} values")
+            self._inv = self._formed = (ctypes.c_double * max(1, n))(*inv)
+        elif 0 < base < math.inf:  # what the library would form from the base, once
+            self._formed = (ctypes.c_double * max(1, n))(*[float(base) ** (-2.0 * i / self.rot_dim) for i in range(n)])
+        self._structs = {}
         self._fixed = (float(base), float(eps), float(w_offset), float(rot_scale), 1 if norm else 0, self.rot_dim,
                        1 if interleaved else 0)
 
-    def struct(self, x_strides=(0, 0, 0), dx_strides=(0, 0, 0), pos_begin=0):
+    def struct(self, x_strides=(0, 0, 0), dx_strides=(0, 0, 0), pos_begin=0, formed=False):
+        """loong_qk_opts; formed: with the frequencies of ``base`` spelled out."""
         base, eps, w_offset, rot_scale, norm, rot_dim, inter = self._fixed
-        inv = None if self._inv is None else ctypes.cast(self._inv, ctypes.POINTER(ctypes.c_double))
+        inv = self._formed if formed else self._inv
+        inv = None if inv is None else ctypes.cast(inv, ctypes.POINTER(ctypes.c_double))
         return LoongQkOpts(*x_strides, *dx_strides, pos_begin, base, inv, eps, w_offset, rot_scale, norm, rot_dim, inter)
+
+    def _struct_of(self, x_strides, dx_strides=(0, 0, 0), pos_begin=0):
+        """struct(...), kept: a program calls with a few strides, and one pos_begin or a counting one."""
+        key = (*x_strides, *dx_strides, pos_begin)
+        o = self._structs.get(key)
+        if o is None:
+            if len(self._structs) >= 64:
+                self._structs.clear()
+            o = self._structs[key] = self.struct(x_strides, dx_strides, pos_begin, formed=True)
+        return o
 
 
 def make_qk_opts(head_dim, **kw):
@@ -564,12 +609,12 @@ def qk_norm_rope(w, opts, q, k, v=None, wq=None, wk=None, positions=None, pos_be
     attention's layout, in one pass: projections [B, S, heads, d] (views of one
     fused projection, or contiguous) -> (q, k, v) as attn_fwd takes them.  ``v``
     is only brought into the layout; None leaves it out."""
-    desc = make_desc(w, layout=layout)
+    desc = _desc_of(w, MODE_FUSED, layout)
     _check("loong_attn_check", loong_attn_check(desc))
     _qk_weights(w, wq, wk, positions, q.device)
-    o = opts.struct(_token_strides(("q", "k", "v"), (q, k, v), w, q.device), pos_begin=pos_begin)
-    device, stream = _on(q.device, stream)
-    with device, torch.cuda.stream(stream):
+    o = opts._struct_of(_token_strides(("q", "k", "v"), (q, k, v), w, q.device), pos_begin=pos_begin)
+    where, stream = _on(q.device, stream)
+    with where:
         out = [None if t is None else torch.empty(_attn_shape(w, h, layout), dtype=torch.bfloat16, device=q.device)
                for t, h in ((q, w.hq), (k, w.hkv), (v, w.hkv))]
         loong_qk_norm_rope_fwd(desc, o, q, k, v, wq, wk, positions, *out, stream)
@@ -583,7 +628,7 @@ def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions
     there is none).  ``into``: the three projection gradients to write, e.g.
     views of one fused gradient (the third None without dv); else they are made
     contiguous."""
-    desc = make_desc(w, layout=layout)
+    desc = _desc_of(w, MODE_FUSED, layout)
     _check("loong_attn_check", loong_attn_check(desc))
     _qk_weights(w, wq, wk, positions, q.device)
     for n, t, h in (("dq", dq, w.hq), ("dk", dk, w.hkv), ("dv", dv, w.hkv)):
@@ -591,13 +636,13 @@ def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions
             _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, q.device)
     if into is not None and (into[2] is None) != (dv is None):
         raise ValueError("into[2] belongs to dv: give both or neither")
-    device, stream = _on(q.device, stream)
-    with device, torch.cuda.stream(stream):
+    where, stream = _on(q.device, stream)
+    with where:
         if into is None:
             into = [None if t is None else torch.empty((w.batch, w.seqlen, h, w.head_dim), dtype=torch.bfloat16,
                                                        device=q.device) for t, h in ((dq, w.hq), (dk, w.hkv), (dv, w.hkv))]
-        o = opts.struct(_token_strides(("q", "k", "v"), (q, k, None), w, q.device),
-                        _token_strides(("into[0]", "into[1]", "into[2]"), into, w, q.device), pos_begin)
+        o = opts._struct_of(_token_strides(("q", "k", "v"), (q, k, None), w, q.device),
+                            _token_strides(("into[0]", "into[1]", "into[2]"), into, w, q.device), pos_begin)
         dwq = None if wq is None or not opts.norm else torch.empty_like(wq)
         dwk = None if wk is None or not opts.norm else torch.empty_like(wk)
         n = loong_qk_norm_rope_bwd_workspace_size(desc, o)

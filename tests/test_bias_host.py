@@ -61,7 +61,7 @@ def test_bias_workspace_sizes(loong_lib, causal, mode):
     width = (W.hq // W.hkv) * (b.num_bounds + 1)
     part = up(4 * 16 * width * W.hkv * (W.seqlen // 128))
     assert ops.loong_attn_bias_workspace_size(d, b.struct(), 1) == \
-        up(ops.loong_attn_workspace_size(d, 1)) + lut + part + up(8 * 64 * W.hkv * width)
+        up(ops.loong_attn_workspace_size(d, 1)) + lut + part + 256 + up(8 * 64 * W.hkv * width)
 
 
 def test_bias_calls_refuse_before_any_cuda_call(loong_lib):
