@@ -99,6 +99,7 @@ struct BiasView {
   int64_t len = 0;
   int off = 0;
   int intervals = 0;
+  int v_ready = 0;  // forward: V's fp16 form and max |V| are in the workspace already
 };
 
 // What a run of places [at - reach, at + reach] looks like, in one word.

@@ -18,6 +18,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "v16.cuh"
 
 namespace loong {
 
@@ -32,6 +33,9 @@ constexpr float kMaskBelow = -1.2676506002282294e30f;  // -2^100
 constexpr float kMinScale = 5.9604645e-8f;             // 2^-24
 constexpr int64_t kMaxSeqlen = int64_t{1} << 29;       // places fit 32 bits
 constexpr int kSumSplits = 64;
+// V of at most this many vectors of 8 is converted by one block: measured at
+// 100 tokens of 2 heads of 64 (1,600 vectors) against the two launches.
+constexpr int64_t kBlockV = 4096;
 
 struct BucketMap {
   int intervals;
@@ -44,11 +48,20 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // One thread per distance: its interval and its pieces' by binary search, then
 // the bias of heads blockIdx.y, blockIdx.y + gridDim.y, ...; consecutive threads
 // write consecutive words.  The same launch clears the words that the pass adds
-// into: max |V| (forward), the gradient's parts and tickets (backward).
+// into: max |V| (forward), the gradient's parts and tickets (backward).  A short
+// forward's V (v_vecs vectors of 8) is also brought into its fp16 form here, by
+// the last column's first block alone: max |V| and the copy are two launches
+// otherwise, each longer than the work.
 __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ BucketMap m,
                                                           const __nv_bfloat16* __restrict__ table, int hq,
                                                           float inv_scale, BiasView out,
-                                                          uint4* __restrict__ zero, int64_t zero_vecs) {
+                                                          uint4* __restrict__ zero, int64_t zero_vecs,
+                                                          const uint4* __restrict__ v, uint4* __restrict__ v16,
+                                                          unsigned* __restrict__ amax, int v_vecs) {
+  if (v_vecs > 0 && blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) block_v_to_f16<kThreads>(v, v16, amax, v_vecs);
+    return;
+  }
   const int64_t nthreads = static_cast<int64_t>(gridDim.x) * gridDim.y * kThreads;
   for (int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x; z < zero_vecs;
        z += nthreads)
@@ -210,8 +223,9 @@ BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
   return w;
 }
 
+// v: the forward's V, or null.
 int expand(const loong_attn_desc& d, const loong_rel_bias& b, const BucketMap& m, const BiasWs& w, void* ws,
-           BiasView* view, cudaStream_t stream) {
+           const void* v, BiasView* view, cudaStream_t stream) {
   uint8_t* base = static_cast<uint8_t*>(ws);
   view->lut = reinterpret_cast<float*>(base + w.lut);
   view->interval = base + w.interval;
@@ -224,9 +238,14 @@ int expand(const loong_attn_desc& d, const loong_rel_bias& b, const BucketMap& m
   const int64_t nb = (w.len + kThreads - 1) / kThreads;
   // short sequences spread the heads over blocks as well
   const unsigned ny = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(d.hq, 608 / nb)));
-  expand_kernel<<<dim3(static_cast<unsigned>(nb), ny), kThreads, 0, stream>>>(
+  const int64_t v_vecs = d.batch * d.seqlen * d.hkv * d.head_dim / 8;
+  view->v_ready = v && v_vecs <= kBlockV;
+  const FwdWsLayout L = fwd_ws_layout(d);
+  expand_kernel<<<dim3(static_cast<unsigned>(nb + view->v_ready), ny), kThreads, 0, stream>>>(
       m, static_cast<const __nv_bfloat16*>(b.table), d.hq, 1.0f / scale, *view,
-      reinterpret_cast<uint4*>(base + w.zero), static_cast<int64_t>(w.zero_bytes / 16));
+      reinterpret_cast<uint4*>(base + w.zero), view->v_ready ? 0 : static_cast<int64_t>(w.zero_bytes / 16),
+      static_cast<const uint4*>(v), reinterpret_cast<uint4*>(base + L.v16), reinterpret_cast<unsigned*>(base + L.amax),
+      view->v_ready ? static_cast<int>(v_vecs) : 0);
   return check_launch();
 }
 
@@ -265,8 +284,8 @@ int loong_attn_bias_fwd(const loong_attn_desc* d, const loong_rel_bias* bias, co
   if (!on_device(ws) || !on_device(bias->table) || (o_res && !on_device(o_res))) return LOONG_ERR_INVALID_ARG;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   BiasView view;
-  if ((st = expand(*d, *bias, bucket_map(*bias), w, ws, &view, stream)) != LOONG_OK) return st;
-  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, &view);  // max |V| is cleared
+  if ((st = expand(*d, *bias, bucket_map(*bias), w, ws, v, &view, stream)) != LOONG_OK) return st;
+  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, &view);  // max |V| is cleared or formed
 }
 
 int loong_attn_bias_bwd(const loong_attn_desc* d, const loong_rel_bias* bias, const void* q, const void* k,
@@ -296,7 +315,7 @@ int loong_attn_bias_bwd(const loong_attn_desc* d, const loong_rel_bias* bias, co
   double* sums = reinterpret_cast<double*>(base + w.sums);
   const BucketMap m = bucket_map(*bias);
   BiasView view;
-  if ((st = expand(*d, *bias, m, w, ws, &view, stream)) != LOONG_OK) return st;
+  if ((st = expand(*d, *bias, m, w, ws, nullptr, &view, stream)) != LOONG_OK) return st;
   if ((st = run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, &view, part)) != LOONG_OK) return st;
   const RingGeom g = ring_geom(*d);
   const int nkt = g.nblocks * g.ntile;

@@ -11,6 +11,7 @@
 #include "fastdiv.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "v16.cuh"
 
 namespace loong {
 
@@ -90,10 +91,7 @@ __global__ void absmax_bf16_kernel(const uint4* __restrict__ in, int64_t nvec, u
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   unsigned m = 0;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < nvec; i += stride) {
-    const uint4 x = __ldg(in + i);
-    const unsigned w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) m = max(m, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
+    m = max(m, v16_absmax(__ldg(in + i)));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if ((threadIdx.x & 31) == 0 && m) atomicMax(amax, m << 16);
@@ -104,16 +102,9 @@ __global__ void absmax_bf16_kernel(const uint4* __restrict__ in, int64_t nvec, u
 __global__ void bf16_to_f16_scaled_kernel(const uint4* __restrict__ in, uint4* __restrict__ out, int64_t nvec,
                                           const unsigned* __restrict__ amax) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const float f = __int_as_float((127 - v16_shift(*amax)) << 23);  // 2^-e, -100 <= e <= 114
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < nvec; i += stride) {
-    const uint4 x = __ldg(in + i);
-    const unsigned w[4] = {x.x, x.y, x.z, x.w};
-    unsigned y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      y[u] = pack_f16(__uint_as_float(w[u] << 16) * f, __uint_as_float(w[u] & 0xFFFF0000u) * f);
-    out[i] = make_uint4(y[0], y[1], y[2], y[3]);
-  }
+  const float f = v16_factor(*amax);
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < nvec; i += stride)
+    out[i] = v16_scaled(__ldg(in + i), f);
 }
 
 // One lane segment per row: L = min(32, 2^ceil(log2 vpr)) lanes, 32 / L rows

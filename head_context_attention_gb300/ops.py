@@ -139,9 +139,18 @@ def _ptr(t):
 
 
 def _stream(stream):
+    """A cudaStream_t: of a torch stream, the current one (None), or given as a number."""
+    if type(stream) is int:
+        return stream
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _current_raw_stream(index):
+    """The current stream of a device as a number (a torch stream object costs 3 us)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def make_desc(w, mode=MODE_FUSED, scale=0.0, layout=LAYOUT_NATURAL):
@@ -476,7 +485,7 @@ def _on(device, stream):
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not {device}")
     if stream is None and device.index == torch.cuda.current_device():
-        return _NOTHING, torch.cuda.current_stream()
+        return _NOTHING, _current_raw_stream(device.index)
     where = contextlib.ExitStack()
     where.enter_context(torch.cuda.device(device))
     stream = torch.cuda.current_stream(device) if stream is None else stream
