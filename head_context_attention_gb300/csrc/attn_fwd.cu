@@ -126,11 +126,15 @@ static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bou
 // unscaled score.  The producer looks the tile and its seven kinds of piece up
 // (pieces on one diagonal are alike) a tile ahead.  A bias of -inf masks like a
 // causal mask; a row that it leaves nothing gets O = 0 and LSE = -inf.
+//
+// With BIAS, an odd group's last head (every head, in groups of one) pairs two
+// query tiles of its own, neighbours in a block, in the two head slots, where the
+// kernel without bias computes the head twice: 16 heads of 128 without groups,
+// twice 4K tokens, every key: 252 us for 402.
 struct FwdPiece {
-  float lo[2], hi[2];  // head slots 0 and 1: the difference before and, kPieceStep, from the boundary on
-  int kind;            // PieceKind
-  int step;            // kPieceStep: row r of the piece has passed the boundary up to column r + step
-  int pad[2];
+  float lo, hi;  // the difference before and, kPieceStep, from the boundary on
+  int kind;      // PieceKind
+  int step;      // kPieceStep: row r of the piece has passed the boundary up to column r + step
 };
 
 template <int D, bool STEP, bool BIAS>
@@ -141,9 +145,9 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  // BIAS, per tile: piece diagonal i < 7 (rows 32 (i - 3) ahead of the keys), and
+  // BIAS, per tile and slot: piece diagonal i < 7 (rows 32 (i - 3) ahead of the keys), and
   // as entry 7 the tile as a whole, its constant in `hi` and, in log2 units, `lo`
-  __shared__ FwdPiece piece_bias[BIAS ? C::NINFO : 1][8];
+  __shared__ FwdPiece piece_bias[BIAS ? C::NINFO : 1][2][8];
   __shared__ uint64_t bias_full[BIAS ? C::NINFO : 1];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -173,23 +177,33 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   // B blocks 2cp-1-c (paired placement), then A blocks c.
   const RingGeom& g = a.ring;
   int idx = blockIdx.x;
-  const int hpair = idx % a.npairs;
-  idx /= a.npairs;
   const int nr = a.rank_end - a.rank_begin;
   const int nqt = nr * rank_parts(g) * g.ntile;
-  const int r = idx % nqt;
-  idx /= nqt;
+  // BIAS: first the pairs of tiles of an odd group's last head, then the pairs of heads
+  const int npt = BIAS && (a.G & 1) ? nr * rank_parts(g) * ((g.ntile + 1) / 2) : 0;
+  const int npairs = BIAS ? a.G / 2 : a.npairs;
+  int item = idx % (npt + nqt * npairs);
+  idx /= npt + nqt * npairs;
+  const bool tile_pair = BIAS && item < npt;
+  if (!tile_pair) item -= npt;
+  const int hpair = tile_pair ? 0 : item % npairs;
+  const int r = tile_pair ? item : item / npairs;
   const int kvh = idx % a.hkv;
   const int b = idx / a.hkv;
-  const int jb = r / g.ntile;
+  const int per_block = tile_pair ? (g.ntile + 1) / 2 : g.ntile;
+  const int jb = r / per_block;
   const int bq = (g.zigzag && jb < nr) ? 2 * g.cp - 1 - a.rank_begin - jb
                                        : a.rank_end - 1 - (g.zigzag ? jb - nr : jb);
-  const int qi = g.ntile - 1 - r % g.ntile;
-  const int q0 = bq * g.blk + qi * kTile;
-  const int qlen = min(kTile, (bq + 1) * g.blk - q0);
-  const int head0 = kvh * a.G + 2 * hpair;
-  const bool dup = head0 + 1 >= (kvh + 1) * a.G;  // odd group: slot 1 repeats slot 0
-  const int head1 = dup ? head0 : head0 + 1;
+  const int from_last = r % per_block;
+  // the slots' query tiles; the walk follows the later one
+  const int qi0 = tile_pair ? 2 * (per_block - 1 - from_last) : g.ntile - 1 - from_last;
+  const int qi = tile_pair ? min(qi0 + 1, g.ntile - 1) : qi0;
+  const int head0 = kvh * a.G + (tile_pair ? a.G - 1 : 2 * hpair);
+  // slot 1 repeats slot 0: an odd group without bias, a last tile without a neighbour
+  const bool dup = BIAS ? tile_pair && qi == qi0 : head0 + 1 >= (kvh + 1) * a.G;
+  const int head1 = dup || tile_pair ? head0 : head0 + 1;
+  const int q0 = bq * g.blk + qi0 * kTile;   // slot 0's first row, slot 1's
+  const int q1 = bq * g.blk + qi * kTile;
 
   KvWalk walk;
   walk.init(g, bq, qi, a.t_begin, a.t_end);
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         mbar_expect_tx(q_full, C::NQ * C::TILE_BYTES);
         for (int h = 0; h < C::NQ; ++h) {
           int hc;
-          const int64_t qr64 = a.lay.view_row(b, q0, h ? head1 : head0, a.hq, hc);
+          const int64_t qr64 = a.lay.view_row(b, h ? q1 : q0, h ? head1 : head0, a.hq, hc);
           // checked build: the tile starts inside the tensor (TMA fills rows past its end with zeros)
           in_bounds(qr64 >= 0 && qr64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
           const int qr = static_cast<int>(qr64);
@@ -255,21 +269,21 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       }
       int jk = 0, jv = 0;
       const int c_q = block_owner(g, bq);  // the query tile's ring rank
-      // lanes 0-6: a piece diagonal of the tile the walk stands at, lane 7: the tile
+      // lanes 0-6: a piece diagonal of the tile the walk stands at, lane 7: the
+      // tile, for slot 0; lanes 8-15 the same for slot 1
       FwdPiece piece;
       int code = 0;
       auto look_up = [&]() {
         if constexpr (BIAS) {
-          if (lane < 8) {
-            const int64_t i0 = a.bias.off + q0 - walk.k0() + (lane < 7 ? 32 * (lane - 3) : 0);  // the middle distance
+          if (lane < 16) {
+            const int diag = lane & 7;
+            // the middle distance
+            const int64_t i0 = a.bias.off + (lane < 8 ? q0 : q1) - walk.k0() + (diag < 7 ? 32 * (diag - 3) : 0);
             // independent loads, waited for in the next trip
-            code = (lane < 7 ? a.bias.piece : a.bias.tile)[i0];
-            const float* l0 = a.bias.lut + head0 * a.bias.len + i0;
-            const float* l1 = a.bias.lut + head1 * a.bias.len + i0;
-            piece.lo[0] = l0[-31];
-            piece.lo[1] = l1[-31];
-            piece.hi[0] = l0[31];
-            piece.hi[1] = l1[31];
+            code = (diag < 7 ? a.bias.piece : a.bias.tile)[i0];
+            const float* l = a.bias.lut + (lane < 8 ? head0 : head1) * a.bias.len + i0;
+            piece.lo = l[-31];
+            piece.hi = l[31];
           }
         }
       };
@@ -293,15 +307,13 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         if constexpr (BIAS) {
           piece.kind = PieceCode::kind(code);
           piece.step = PieceCode::step(code);
-          const bool crossed = __shfl_sync(0xffffffffu, piece.kind, 7) != kPieceConst;
-#pragma unroll
-          for (int hs = 0; hs < 2; ++hs) {
-            float mid = __shfl_sync(0xffffffffu, piece.lo[hs], 7);
-            if (crossed && !isfinite(mid)) mid = 0.f;  // differences to it have to mean something
-            piece.lo[hs] = lane == 7 ? mid * a.scale_log2 : piece.lo[hs] - mid;
-            piece.hi[hs] = lane == 7 ? mid : piece.hi[hs] - mid;
-          }
-          if (lane < 8) piece_bias[j % C::NINFO][lane] = piece;
+          const bool crossed = __shfl_sync(0xffffffffu, piece.kind, lane | 7) != kPieceConst;
+          float mid = __shfl_sync(0xffffffffu, piece.lo, lane | 7);
+          if (crossed && !isfinite(mid)) mid = 0.f;  // differences to it have to mean something
+          const bool tile = (lane & 7) == 7;
+          piece.lo = tile ? mid * a.scale_log2 : piece.lo - mid;
+          piece.hi = tile ? mid : piece.hi - mid;
+          if (lane < 16) piece_bias[j % C::NINFO][lane >> 3][lane & 7] = piece;
           __syncwarp();
           if (leader) mbar_arrive(&bias_full[j % C::NINFO]);
           if (j + 1 < n) look_up();
@@ -422,13 +434,13 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
           ok = false;
           break;
         }
-        tile_b = piece_bias[e][7].lo[h];
-        crossed = piece_bias[e][7].kind != kPieceConst;
+        tile_b = piece_bias[e][h][7].lo;
+        crossed = piece_bias[e][h][7].kind != kPieceConst;
         if (crossed) {
 #pragma unroll
           for (int cb = 0; cb < 4; ++cb) {
-            const FwdPiece& pb = piece_bias[e][quarter - cb + 3];
-            needs |= pb.kind != kPieceConst || pb.lo[h] != 0.f ? 1u << cb : 0u;
+            const FwdPiece& pb = piece_bias[e][h][quarter - cb + 3];
+            needs |= pb.kind != kPieceConst || pb.lo != 0.f ? 1u << cb : 0u;
           }
         }
       }
@@ -438,18 +450,18 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       }
       tc_fence_after();
       if (BIAS && crossed) {
-        const float* lp = a.bias.lut + static_cast<int64_t>(h ? head1 : head0) * a.bias.len + a.bias.off + q0 + row -
-                          walk.k0();
+        const float* lp = a.bias.lut + static_cast<int64_t>(h ? head1 : head0) * a.bias.len + a.bias.off +
+                          (h ? q1 : q0) + row - walk.k0();
 #pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
           if (!(needs >> cb & 1)) continue;
           uint32_t x[32];
           tmem_ld32(tS + cb * 32, x);
-          const FwdPiece& pb = piece_bias[e][quarter - cb + 3];
-          const float lo = pb.lo[h], hi = pb.hi[h];
+          const FwdPiece& pb = piece_bias[e][h][quarter - cb + 3];
+          const float lo = pb.lo, hi = pb.hi;
           float2 add[16];
           if (pb.kind == kPieceMixed) {  // the kinds are uniform over the warp
-            const float mid = piece_bias[e][7].hi[h];
+            const float mid = piece_bias[e][h][7].hi;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               add[i] = make_float2(__ldg(lp - (cb * 32 + 2 * i)) - mid, __ldg(lp - (cb * 32 + 2 * i + 1)) - mid);
@@ -473,14 +485,16 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       }
       uint32_t sr[4][32];
       const int klen = walk.klen();
-      const bool dg = walk.diag();
+      // the causal diagonal tile; BIAS: or slot 0's, or one after it that only slot 1 sees
+      const bool dg = BIAS ? g.causal && walk.bk == bq && walk.kt >= (h ? qi : qi0) : walk.diag();
       // the tile's scores, masked columns at -inf (read again by the full path)
       auto load_s = [&]() {
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) tmem_ld32(tS + cb * 32, sr[cb]);
         tmem_wait_ld();
         if (dg || klen < kTile) {
-          const int lim = dg ? min(row, klen - 1) : klen - 1;
+          int lim = dg ? min(row, klen - 1) : klen - 1;
+          if (BIAS && dg && walk.kt > (h ? qi : qi0)) lim = -1;
 #pragma unroll
           for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
@@ -579,8 +593,10 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
     if (ok) {
       tc_fence_after();
       const int head = h ? head1 : head0;
-      const int64_t qv = a.lay.vec(b, q0 + row, head, a.hq);  // this row's d-vector in Q / O
-      const int64_t lse_i = (static_cast<int64_t>(b) * a.hq + head) * a.S + (q0 + row);
+      const int qh = h ? q1 : q0;
+      const int qlen = min(kTile, (bq + 1) * g.blk - qh);
+      const int64_t qv = a.lay.vec(b, qh + row, head, a.hq);  // this row's d-vector in Q / O
+      const int64_t lse_i = (static_cast<int64_t>(b) * a.hq + head) * a.S + (qh + row);
       // checked build: the row's O, accumulator and LSE entries lie inside their tensors
       const bool valid = row < qlen && !(h == 1 && dup) &&
                          in_bounds(qv >= 0 && qv < static_cast<int64_t>(a.batch) * a.S * a.hq && lse_i >= 0 &&
@@ -728,8 +744,10 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return cuda_fail(e);
     if (at.numRegs < C::BIAS_REGS) return LOONG_ERR_UNSUPPORTED;
   }
-  const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring) *
-                       a.ring.ntile * a.npairs;
+  const int64_t blocks = static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring);
+  const int64_t per_kvh = BIAS ? blocks * (a.ring.ntile * (a.G / 2) + (a.G & 1) * ((a.ring.ntile + 1) / 2))
+                               : blocks * a.ring.ntile * a.npairs;
+  const int64_t grid = d.batch * d.hkv * per_kvh;
   if (grid <= 0 || grid > 0x7fffffff) return LOONG_ERR_INVALID_ARG;
   if (!STEP) {
     a.t_begin = 0;

@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const __grid_consta
                                                              unsigned* __restrict__ ticket, int buckets,
                                                              __nv_bfloat16* __restrict__ dtable) {
   __shared__ bool last;
-  __shared__ double by_interval[kMaxIntervals];
+  __shared__ double by_interval[kMaxIntervals], shares[kThreads];
+  const int lots = max(1, kThreads / m.intervals);
   const int kvh = blockIdx.x;
   const int width = group * m.intervals;
   const int64_t j0 = pairs * blockIdx.y / gridDim.y, j1 = pairs * (blockIdx.y + 1) / gridDim.y;
@@ -141,10 +142,19 @@ __global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const __grid_consta
   __threadfence();
   for (int g = 0; g < group; ++g) {
     __syncthreads();  // the previous head's sums have been read
-    for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
-      const double* src = sums + static_cast<int64_t>(kvh) * width + g * m.intervals + i;
+    // the splits in `lots` shares of every interval, then the shares
+    for (int i = threadIdx.x; i < lots * m.intervals; i += kThreads) {
+      const int lot = i / m.intervals;
+      const double* src = sums + static_cast<int64_t>(kvh) * width + g * m.intervals + (i - lot * m.intervals);
       double s = 0.0;
-      for (unsigned sp = 0; sp < gridDim.y; ++sp) s += __ldcg(src + static_cast<int64_t>(sp) * hkv * width);
+#pragma unroll 4
+      for (unsigned sp = lot; sp < gridDim.y; sp += lots) s += __ldcg(src + static_cast<int64_t>(sp) * hkv * width);
+      shares[i] = s;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
+      double s = 0.0;
+      for (int lot = 0; lot < lots; ++lot) s += shares[lot * m.intervals + i];
       by_interval[i] = s;
     }
     __syncthreads();
@@ -194,8 +204,9 @@ struct BiasWs {
 
 BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
   BiasWs w{};
-  // a tile's distances reach 127 past the first and the last token's
-  w.off = static_cast<int>(d.causal ? 128 : d.seqlen + 128);
+  // a tile's distances reach 127 past the first and the last token's, a pair of
+  // tiles' first one another 128 (causal: where only the second sees the keys)
+  w.off = static_cast<int>(d.causal ? 256 : d.seqlen + 128);
   w.len = w.off + d.seqlen + 128;
   size_t at = up256(loong_attn_workspace_size(&d, pass));
   w.lut = at;

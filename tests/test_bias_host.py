@@ -55,7 +55,7 @@ def test_bias_workspace_sizes(loong_lib, causal, mode):
     up = lambda x: (x + 255) // 256 * 256
     d = _desc(causal=causal, mode=mode)
     b = ops.log_buckets(32, 128, causal=bool(causal))
-    length = (1 if causal else 2) * W.seqlen + 256
+    length = W.seqlen + 384 if causal else 2 * W.seqlen + 256
     lut = up(4 * W.hq * length) + up(length) + 2 * up(4 * length)
     assert ops.loong_attn_bias_workspace_size(d, b.struct(), 0) == up(ops.loong_attn_workspace_size(d, 0)) + lut
     width = (W.hq // W.hkv) * (b.num_bounds + 1)

@@ -51,6 +51,11 @@ CASES = {
     "empty-rows-ring": (384, 2, 1, 128, 1, 3, 3, 1, 1, 1, (4, [20, 140, 200]), "no-near"),
     "lowest": (300, 2, 1, 64, 1, 1, 1, 0, 1, 0, (4, [-20, 1, 130]), "lowest"),
     "nothing": (140, 2, 1, 64, 1, 1, 1, 0, 1, 1, (1, []), "no-near"),
+    "one-head-groups": (600, 3, 3, 128, 1, 1, 1, 0, 1, 1, (LOG, 32, 128), None),
+    "one-head-groups-even": (1024, 2, 2, 64, 1, 2, 2, 1, 1, 1, (LOG, 16, 400), None),
+    "one-head-not-causal": (513, 2, 2, 128, 1, 1, 1, 0, 2, 0, (LOG, 32, 128), None),
+    "groups-of-five": (420, 10, 2, 64, 1, 1, 1, 0, 1, 1, (LOG, 32, 128), None),
+    "one-head-window": (900, 2, 2, 64, 1, 1, 1, 0, 1, 1, (3, [150, 400]), "window"),
     "large-bias": (400, 2, 1, 64, 1, 1, 1, 0, 1, 1, (LOG, 16, 300), "large"),
 }
 
@@ -140,14 +145,15 @@ def test_matches_oracle(cuda_device, name):
     assert torch.equal(_run(w, x, t, buckets)[5].view(torch.int16), out[5].view(torch.int16))
 
 
-@pytest.mark.parametrize("name", ["gqa", "ragged-blocks", "not-causal", "not-causal-d128", "empty-rows-ring", "window"])
+@pytest.mark.parametrize("name", ["gqa", "ragged-blocks", "not-causal", "not-causal-d128", "empty-rows-ring", "window",
+                                  "one-head-groups-even", "groups-of-five"])
 def test_stepwise_matches_oracle(cuda_device, name):
     w, x, t, buckets = _make(name)
     _check(w, x, t, buckets, _run(w, x, t, buckets, mode=ops.MODE_STEPWISE))
 
 
 @pytest.mark.parametrize("mode", [ops.MODE_FUSED, ops.MODE_STEPWISE, ops.MODE_STEPWISE_COPY, ops.MODE_STEPWISE_COPY_AB])
-@pytest.mark.parametrize("name", ["gqa", "empty-rows-ring"])
+@pytest.mark.parametrize("name", ["gqa", "empty-rows-ring", "one-head-groups-even"])
 def test_ranks_layout(cuda_device, name, mode):
     w, x, t, buckets = _make(name)
     o, lse, dq, dk, dv, dt = _run(w, _pack(w, x), t, buckets, mode=mode, layout=ops.LAYOUT_RANK_MAJOR)
@@ -164,13 +170,13 @@ def test_without_the_residual(cuda_device):
     _within("dq", dq[0], r["dq"], 2.0 ** -8 * np.abs(r["dq"]) + 2.0 ** -6 * r["abs_dq"])
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_zero_table_is_the_plain_attention(cuda_device, d):
+@pytest.mark.parametrize("d,hq", [(64, 4), (128, 4), (64, 2), (128, 6)])
+def test_zero_table_is_the_plain_attention(cuda_device, d, hq):
     """A table of zeros leaves every output of the plain pass bit for bit, but dQ
     (whose adds have no fixed order: two runs of the plain pass differ as well)."""
-    w = inputs.small(640, 4, 2, d, cp=2)
+    w = inputs.small(640, hq, 2, d, cp=2)
     x = inputs.make_inputs(w, device="cuda")
-    t, buckets = torch.zeros((32, 4), device="cuda", dtype=torch.bfloat16), ops.log_buckets(32, 300)
+    t, buckets = torch.zeros((32, hq), device="cuda", dtype=torch.bfloat16), ops.log_buckets(32, 300)
     o, lse, o_res = ops.attn_fwd(w, x["q"], x["k"], x["v"])
     dq, dk, dv = ops.attn_bwd(w, x["q"], x["k"], x["v"], o, lse, x["do"], o_res=o_res)
     got = _run(w, x, t, buckets)
@@ -270,7 +276,7 @@ def test_run_of_the_positional_operators(cuda_device):
     assert ops.loong_get_device_status() == ops.LOONG_OK
 
 
-@pytest.mark.parametrize("name", ["gqa", "not-causal", "empty-rows-ring", "group-of-34"])
+@pytest.mark.parametrize("name", ["gqa", "not-causal", "empty-rows-ring", "group-of-34", "one-head-groups"])
 def test_checked_build(cuda_device, monkeypatch, name):
     """The build with device address checks finds nothing to report."""
     monkeypatch.setattr(ops, "LIB_PATH", ops.CHECKED_LIB_PATH)
