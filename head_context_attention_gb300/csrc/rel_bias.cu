@@ -107,10 +107,10 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
 }
 
 // Sum of the backward's parts over warps, key tiles and sequences, in a fixed
-// order: block (kv head, split) adds its share of the (sequence, key tile)
-// pairs, 16 warps' numbers in 32 bits and those sums in 64; the last block of a
-// kv head to finish (tickets, cleared by expand_kernel) adds the splits' sums and
-// then the intervals of every bucket.
+// order: block (head, split) adds its share of the (sequence, key tile) pairs,
+// `lots` threads per interval, in 32 bits over a pair's warps and in 64 beyond;
+// the last block of a head to finish (tickets, cleared by expand_kernel) adds the
+// splits' sums and then the intervals of every bucket.
 __global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const __grid_constant__ BucketMap m,
                                                              const float* __restrict__ part, int64_t pairs, int nkt,
                                                              int hkv, int group, double* __restrict__ sums,
@@ -118,52 +118,55 @@ __global__ void __launch_bounds__(kThreads) dbias_sum_kernel(const __grid_consta
                                                              __nv_bfloat16* __restrict__ dtable) {
   __shared__ bool last;
   __shared__ double by_interval[kMaxIntervals], shares[kThreads];
-  const int lots = max(1, kThreads / m.intervals);
-  const int kvh = blockIdx.x;
-  const int width = group * m.intervals;
+  const int h = blockIdx.x, hq = hkv * group;
+  const int kvh = h / group, g = h - kvh * group;
+  const int ni = m.intervals;
+  const int64_t width = static_cast<int64_t>(group) * ni;
+  const int lots = kThreads / ni;  // ni <= kThreads
+  const int lot = threadIdx.x / ni, ivl = threadIdx.x - lot * ni;
+  const bool mine = lot < lots;
+  // the lots' shares of an interval, in the order of the lots
+  auto add_shares = [&](double s) {
+    if (mine) shares[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x < ni) {
+      double t = 0.0;
+      for (int l = 0; l < lots; ++l) t += shares[l * ni + threadIdx.x];
+      by_interval[threadIdx.x] = t;
+    }
+    __syncthreads();
+  };
   const int64_t j0 = pairs * blockIdx.y / gridDim.y, j1 = pairs * (blockIdx.y + 1) / gridDim.y;
-  for (int e = threadIdx.x; e < width; e += kThreads) {
-    double acc = 0.0;
+  double acc = 0.0;
+  if (mine) {
     for (int64_t j = j0; j < j1; ++j) {
       const int64_t b = j / nkt;
-      const float* p = part + ((b * hkv + kvh) * nkt + (j - b * nkt)) * kBwdComputeWarps * width + e;
-      float s[4] = {};
-#pragma unroll
-      for (int w = 0; w < kBwdComputeWarps; ++w) s[w & 3] += __ldg(p + static_cast<int64_t>(w) * width);
-      acc += static_cast<double>((s[0] + s[1]) + (s[2] + s[3]));
+      const float* p = part + ((b * hkv + kvh) * nkt + (j - b * nkt)) * kBwdComputeWarps * width + g * ni + ivl;
+      float s = 0.f;
+#pragma unroll 4
+      for (int w = lot; w < kBwdComputeWarps; w += lots) s += __ldg(p + w * width);
+      acc += static_cast<double>(s);
     }
-    sums[(static_cast<int64_t>(blockIdx.y) * hkv + kvh) * width + e] = acc;
   }
+  add_shares(acc);
+  if (threadIdx.x < ni) sums[(static_cast<int64_t>(blockIdx.y) * hq + h) * ni + threadIdx.x] = by_interval[threadIdx.x];
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(ticket + kvh, 1u) == gridDim.y - 1;
+  if (threadIdx.x == 0) last = atomicAdd(ticket + h, 1u) == gridDim.y - 1;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  for (int g = 0; g < group; ++g) {
-    __syncthreads();  // the previous head's sums have been read
-    // the splits in `lots` shares of every interval, then the shares
-    for (int i = threadIdx.x; i < lots * m.intervals; i += kThreads) {
-      const int lot = i / m.intervals;
-      const double* src = sums + static_cast<int64_t>(kvh) * width + g * m.intervals + (i - lot * m.intervals);
-      double s = 0.0;
+  acc = 0.0;
+  if (mine) {
 #pragma unroll 4
-      for (unsigned sp = lot; sp < gridDim.y; sp += lots) s += __ldcg(src + static_cast<int64_t>(sp) * hkv * width);
-      shares[i] = s;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < m.intervals; i += kThreads) {
-      double s = 0.0;
-      for (int lot = 0; lot < lots; ++lot) s += shares[lot * m.intervals + i];
-      by_interval[i] = s;
-    }
-    __syncthreads();
-    for (int t = threadIdx.x; t < buckets; t += kThreads) {
-      double s = 0.0;
-      for (int i = 0; i < m.intervals; ++i)
-        if (m.bucket[i] == t) s += by_interval[i];
-      dtable[(static_cast<int64_t>(t) * hkv + kvh) * group + g] = __float2bfloat16_rn(static_cast<float>(s));
-    }
+    for (unsigned sp = lot; sp < gridDim.y; sp += lots) acc += __ldcg(sums + (static_cast<int64_t>(sp) * hq + h) * ni + ivl);
+  }
+  add_shares(acc);
+  for (int t = threadIdx.x; t < buckets; t += kThreads) {
+    double s = 0.0;
+    for (int i = 0; i < ni; ++i)
+      if (m.bucket[i] == t) s += by_interval[i];
+    dtable[static_cast<int64_t>(t) * hq + h] = __float2bfloat16_rn(static_cast<float>(s));
   }
 }
 
@@ -225,7 +228,7 @@ BiasWs bias_ws(const loong_attn_desc& d, const loong_rel_bias& b, int pass) {
     w.zero = w.part = at;
     at += up256(static_cast<size_t>(bwd_blocks(d)) * kBwdComputeWarps * width * 4);
     w.ticket = at;
-    at += up256(static_cast<size_t>(d.hkv) * 4);
+    at += up256(static_cast<size_t>(d.hq) * 4);
     w.zero_bytes = at - w.zero;
     w.sums = at;
     at += up256(static_cast<size_t>(kSumSplits) * d.hkv * width * 8);
@@ -328,12 +331,14 @@ int loong_attn_bias_bwd(const loong_attn_desc* d, const loong_rel_bias* bias, co
   BiasView view;
   if ((st = expand(*d, *bias, m, w, ws, nullptr, &view, stream)) != LOONG_OK) return st;
   if ((st = run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, &view, part)) != LOONG_OK) return st;
+  const int group = d->hq / d->hkv;
   const RingGeom g = ring_geom(*d);
   const int nkt = g.nblocks * g.ntile;
   const int64_t pairs = d->batch * nkt;
-  const int splits = static_cast<int>(std::min<int64_t>(kSumSplits, pairs));
-  dbias_sum_kernel<<<dim3(static_cast<unsigned>(d->hkv), static_cast<unsigned>(splits)), kThreads, 0, stream>>>(
-      m, part, pairs, nkt, d->hkv, d->hq / d->hkv, sums, reinterpret_cast<unsigned*>(base + w.ticket),
+  // about 1,200 blocks, a pair each at least
+  const int splits = static_cast<int>(std::min({int64_t{kSumSplits}, pairs, std::max<int64_t>(1, 1216 / d->hq)}));
+  dbias_sum_kernel<<<dim3(static_cast<unsigned>(d->hq), static_cast<unsigned>(splits)), kThreads, 0, stream>>>(
+      m, part, pairs, nkt, d->hkv, group, sums, reinterpret_cast<unsigned*>(base + w.ticket),
       bias->num_buckets, static_cast<__nv_bfloat16*>(dtable));
   return check_launch();
 }
