@@ -503,19 +503,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       // row statistics of this tile, staged by the producer with Q and dO
       const float* lse_row = sStat + (i % C::NS) * (2 * kTile);
       const float* d_row = lse_row + kTile;
-      // BIAS: this warp's piece; the stage's descriptor comes with Q(i)
+      // BIAS: this warp's piece
       float tile_b = 0.f;
       int kind = kPieceConst;
       const BwdPiece* piece = nullptr;
-      if constexpr (BIAS) {
-        if (!warp_wait(&q_full[i % C::NS], (i / C::NS) & 1)) {
-          ok = false;
-          break;
-        }
-        piece = sBias + (i % C::NS) * 8 + grp - quarter + 3;
-        kind = PieceCode::kind(piece->code);
-        if (kind == kPieceConst) tile_b = piece->lo * a.scale_log2;
-      }
       // ---- P^T = exp2(S^T * scale * log2e - LSE * log2e), two 32-query chunks
       if (!warp_wait(s_full, i & 1)) {
         ok = false;
@@ -525,6 +516,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       // S^T(i) read Q(i): the stage's descriptor is in place
       const int4 info = sInfo[i % C::NS];
       const int qlen = info.z;
+      if constexpr (BIAS) {
+        piece = sBias + (i % C::NS) * 8 + grp - quarter + 3;
+        kind = PieceCode::kind(piece->code);
+        if (kind == kPieceConst) tile_b = piece->lo * a.scale_log2;
+      }
       const bool dg = info.w & 1;
       float pv[C::GCH][32];
       {
