@@ -179,15 +179,23 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   int idx = blockIdx.x;
   const int nr = a.rank_end - a.rank_begin;
   const int nqt = nr * rank_parts(g) * g.ntile;
-  // BIAS: first the pairs of tiles of an odd group's last head, then the pairs of heads
-  const int npt = BIAS && (a.G & 1) ? nr * rank_parts(g) * ((g.ntile + 1) / 2) : 0;
-  const int npairs = BIAS ? a.G / 2 : a.npairs;
-  int item = idx % (npt + nqt * npairs);
-  idx /= npt + nqt * npairs;
-  const bool tile_pair = BIAS && item < npt;
-  if (!tile_pair) item -= npt;
-  const int hpair = tile_pair ? 0 : item % npairs;
-  const int r = tile_pair ? item : item / npairs;
+  int hpair, r;
+  bool tile_pair = false;
+  if constexpr (BIAS) {  // first the pairs of tiles of an odd group's last head, then the pairs of heads
+    const int npt = (a.G & 1) ? nr * rank_parts(g) * ((g.ntile + 1) / 2) : 0;
+    const int npairs = a.G / 2;
+    int item = idx % (npt + nqt * npairs);
+    idx /= npt + nqt * npairs;
+    tile_pair = item < npt;
+    if (!tile_pair) item -= npt;
+    hpair = tile_pair ? 0 : item % npairs;
+    r = tile_pair ? item : item / npairs;
+  } else {
+    hpair = idx % a.npairs;
+    idx /= a.npairs;
+    r = idx % nqt;
+    idx /= nqt;
+  }
   const int kvh = idx % a.hkv;
   const int b = idx / a.hkv;
   const int per_block = tile_pair ? (g.ntile + 1) / 2 : g.ntile;
@@ -204,6 +212,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   const int head1 = dup || tile_pair ? head0 : head0 + 1;
   const int q0 = bq * g.blk + qi0 * kTile;   // slot 0's first row, slot 1's
   const int q1 = bq * g.blk + qi * kTile;
+  const int qlen = min(kTile, (bq + 1) * g.blk - q0);  // slot 0's rows; without BIAS slot 1's too
 
   KvWalk walk;
   walk.init(g, bq, qi, a.t_begin, a.t_end);
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         }
       };
       look_up();
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < n; ++j, BIAS ? void() : walk.advance()) {
         const int s = j % C::NS;
         const int u = j / C::NS;
         int kvc;
@@ -296,7 +305,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
                                        : a.lay.view_row(b, walk.k0(), kvh, a.hkv, kvc);
         in_bounds(k064 >= 0 && k064 < a.lay.view_rows(a.batch) && kvc >= 0 && kvc < a.lay.view_heads(a.hkv), a.err);
         const int k0 = static_cast<int>(k064);
-        walk.advance();  // to tile j + 1, if there is one
+        if constexpr (BIAS) walk.advance();  // to tile j + 1, if there is one, for look_up
         if (j >= C::NS && !all(mbar_wait(&k_empty[s], (u - 1) & 1, abort_flag, a.err))) break;
         if (leader) {
           mbar_expect_tx(&k_full[s], C::TILE_BYTES);
@@ -594,11 +603,10 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       tc_fence_after();
       const int head = h ? head1 : head0;
       const int qh = h ? q1 : q0;
-      const int qlen = min(kTile, (bq + 1) * g.blk - qh);
       const int64_t qv = a.lay.vec(b, qh + row, head, a.hq);  // this row's d-vector in Q / O
       const int64_t lse_i = (static_cast<int64_t>(b) * a.hq + head) * a.S + (qh + row);
       // checked build: the row's O, accumulator and LSE entries lie inside their tensors
-      const bool valid = row < qlen && !(h == 1 && dup) &&
+      const bool valid = row < (BIAS ? min(kTile, (bq + 1) * g.blk - qh) : qlen) && !(h == 1 && dup) &&
                          in_bounds(qv >= 0 && qv < static_cast<int64_t>(a.batch) * a.S * a.hq && lse_i >= 0 &&
                                        lse_i < static_cast<int64_t>(a.batch) * a.hq * a.S,
                                    a.err);
