@@ -12,7 +12,9 @@
  *
  * Conventions shared by every entry point
  *   - Pointers named q, k, v, o, o_res, dout, dq, dk, dv, lse, ws, in, out,
- *     o_parts, lse_parts, o_out, lse_out are DEVICE pointers owned by the caller:
+ *     o_parts, lse_parts, o_out, lse_out, table, dtable, wq, wk, positions,
+ *     q_out, k_out, v_out, dq_out, dk_out, dv_out, dwq, dwk are DEVICE pointers
+ *     owned by the caller:
  *     memory of the current device, from cudaMalloc or managed.  A host
  *     pointer (pinned or not) or another device's memory is refused with
  *     LOONG_ERR_INVALID_ARG before any work is enqueued.  The
@@ -21,6 +23,8 @@
  *     and (STEPWISE_COPY) one side stream with its events per device, and
  *     synchronises only in loong_get_device_status.
  *   - All work is enqueued asynchronously on `stream` (0 = legacy default).
+ *     Calls (or replays of captured ones) that may run at the same time need
+ *     workspaces of their own.
  *   - Tensors are contiguous.  In the NATURAL layout Q, O, dO, dQ are bf16
  *     [B, S, Hq, d] and K, V, dK, dV bf16 [B, S, Hkv, d], natural token order.
  *     In the RANK_MAJOR layout (descriptor field `layout`) they are
@@ -378,10 +382,11 @@ LOONG_API int loong_attn_bias_fwd(const loong_attn_desc* desc, const loong_rel_b
 /*
  * loong_attn_bwd with the bias, and the gradient of the table:
  *   dtable  bf16 [num_buckets][hq], written: the sum of dS (see loong_attn_bwd)
- *           over every pair of the bucket, summed in fp32 and fp64 and rounded
- *           once; 0 for a bucket no pair falls in.  Its order of summation is
- *           fixed.  D carries the accuracy of o and o_res into it; without
- *           o_res it is as exact as bf16 O.
+ *           over every pair of the bucket, summed in fp32 within a compute warp
+ *           and in fp64 beyond, and rounded once; 0 for a bucket no pair falls
+ *           in.  The sums do not depend on the order in which blocks run.  D
+ *           carries the accuracy of o and o_res into it; without o_res it is as
+ *           exact as bf16 O.
  * o, o_res and lse are loong_attn_bias_fwd's for the same bias.  ws needs
  * loong_attn_bias_workspace_size(desc, bias, 1) bytes.
  */

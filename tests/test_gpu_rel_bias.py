@@ -283,3 +283,63 @@ def test_checked_build(cuda_device, monkeypatch, name):
     monkeypatch.setattr(ops, "_lib", None)
     w, x, t, buckets = _make(name)
     _check(w, x, t, buckets, _run(w, x, t, buckets))
+
+
+def test_long_context(cuda_device):
+    """20,010 tokens on a ring of five: walks over many intervals, blocks that are no multiple of a tile, far
+    boundaries.  Every output against float64 torch, rows of queries at a time, in the norm: each bf16 rounding
+    (P, dS, the result) contributes at most 2^-8 / sqrt 3 of random sign, D 2^-11."""
+    w = inputs.Workload("long", 20010, 2, 1, 64, 1, 5, 5, 1, True, placement=1)
+    x = inputs.make_inputs(w, device="cuda")
+    buckets = ops.RelBuckets(6, [1, 40, 1000, 5000, 15001])
+    t = torch.randn((6, 2), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(torch.bfloat16)
+    out = _run(w, x, t, buckets)
+    q, k, v, do = (x[n][0].double() for n in ("q", "k", "v", "do"))
+    S, scale = w.seqlen, 1 / 8
+    want = [torch.zeros_like(q), torch.zeros((2, S), dtype=torch.float64, device="cuda"), torch.zeros_like(q),
+            torch.zeros_like(k), torch.zeros_like(v), torch.zeros((6, 2), dtype=torch.float64, device="cuda")]
+    bounds = torch.tensor(buckets.bounds, device="cuda")
+    j = torch.arange(S, device="cuda")
+    for i0 in range(0, S, 2048):
+        i = torch.arange(i0, min(S, i0 + 2048), device="cuda")
+        keys = int(i[-1]) + 1
+        n = i[:, None] - j[:keys]
+        ids = torch.bucketize(n, bounds, right=True)
+        for h in range(2):
+            logits = (scale * q[i, h] @ k[:keys, 0].T + t.double()[ids, h]).masked_fill(n < 0, -torch.inf)
+            want[1][h, i] = torch.logsumexp(logits, -1)
+            p = logits.softmax(-1)
+            want[0][i, h] = p @ v[:keys, 0]
+            ds = p * (do[i, h] @ v[:keys, 0].T - (do[i, h] * want[0][i, h]).sum(-1, keepdim=True))
+            want[2][i, h] = scale * ds @ k[:keys, 0]
+            want[3][:keys, 0] += scale * ds.T @ q[i, h]
+            want[4][:keys, 0] += p.T @ do[i, h]
+            want[5][:, h] += torch.bincount(ids.flatten(), ds.flatten(), minlength=6)
+    far = lambda a, b: ((a.double() - b).norm() / b.norm()).item()
+    assert far(out[1][0], want[1]) < 2.0 ** -20
+    assert far(out[0][0], want[0]) < 2.0 ** -8
+    for got, ref in zip((out[2][0], out[3][0], out[4][0], out[5]), want[2:]):
+        assert far(got, ref) < 3 ** 0.5 * 2.0 ** -8
+
+
+def test_two_calls_at_once(cuda_device):
+    """Two streams at work together, each with workspaces of its own, give what they give alone."""
+    cases = [_make(n) for n in ("ragged-blocks", "256-buckets")]
+    alone = [_run(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in cases]
+    for _ in range(4):
+        for i, (s, (w, x, t, buckets)) in enumerate(zip(streams, cases)):
+            o, lse, res = ops.attn_bias_fwd(w, x["q"], x["k"], x["v"], t, buckets, stream=s)
+            got[i].append((o, lse) + ops.attn_bias_bwd(w, x["q"], x["k"], x["v"], o, lse, x["do"], t, buckets,
+                                                       o_res=res, stream=s))
+    torch.cuda.synchronize()
+    for want, runs in zip(alone, got):
+        for run in runs:
+            for n, (a, b) in enumerate(zip(run, want)):
+                if n == 2:    # dQ: its adds have no fixed order
+                    assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
+                else:
+                    assert torch.equal(a, b)
