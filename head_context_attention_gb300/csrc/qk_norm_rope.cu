@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_bwd_kernel(const __gr
               const Vec8 gx = mul(g, f);
               const float ss = head_sum<L::LPH>(dot(f, f)), gwx = head_sum<L::LPH>(dot(gx, w));
               const float r = rsqrtf(ss * (1.f / D) + a.eps);
-              dw = fma8(gx, r, dw);
+              dw = fma8(gx, h < h1 ? r : 0.f, dw);  // past the last head x is 0 and, with eps 0, r infinite
               // dx = r (g w - x r mean(g w x r))
               g = mul(fma8(f, -r * (r * gwx * (1.f / D)), mul(g, w)), r);
             }

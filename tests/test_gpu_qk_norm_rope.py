@@ -233,6 +233,28 @@ def test_zero_head_and_large_values(cuda_device):
     assert torch.allclose(dq[0, 0].float(), g[0, 0].float() * 100, rtol=2.0 ** -7, atol=0)
 
 
+@pytest.mark.parametrize("name", ["odd", "odd-heads-d64", "part-48-inter"])
+def test_eps_zero(cuda_device, name):
+    """Without eps, heads that do not fill a warp: the lanes past the last head add nothing to dw."""
+    c = _make(name)
+    opts = ops.make_qk_opts(c["w"].head_dim, eps=0.0, w_offset=W_OFFSET, rot_dim=c["rot"][0], base=10000.0,
+                            interleaved=c["rot"][1])
+    out = ops.qk_norm_rope_bwd(c["w"], opts, c["q"], c["k"], *[_lay(c, g) for g in c["grads"]], **_place(c))
+    for x, w, g, dx, dw in ((c["q"], c["wq"], c["grads"][0], out[0], out[3]),
+                            (c["k"], c["wk"], c["grads"][1], out[1], out[4])):
+        want_w, tol_w = 0, 0
+        for b in range(x.shape[0]):
+            m, x64 = _matrices(c, b), to64(x[b])
+            want, dwb = oqk.backward(x64, to64(w), m, 0.0, to64(g[b]), True, W_OFFSET)
+            gm = np.einsum("tba,thb->tha", _magnitude(c, m), np.abs(to64(g[b])))
+            r = 1 / np.sqrt((x64 ** 2).mean(-1, keepdims=True))
+            h, xr = gm * np.abs(to64(w) + W_OFFSET), np.abs(x64 * r)
+            _check("dx", dx[b], want,
+                   2.0 ** -8 * np.abs(want) + 2.0 ** -18 * r * (h + xr * (h * xr).mean(-1, keepdims=True)))
+            want_w, tol_w = want_w + dwb, tol_w + 2.0 ** -15 * (gm * xr).sum((0, 1))
+        _check("dw", dw, want_w, tol_w)
+
+
 def test_other_stream_and_graph(cuda_device):
     """On a stream of its own, and captured once and replayed on new inputs: the
     bits of the eager calls on the default stream."""
