@@ -131,6 +131,13 @@ static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bou
 // query tiles of its own, neighbours in a block, in the two head slots, where the
 // kernel without bias computes the head twice: 16 heads of 128 without groups,
 // twice 4K tokens, every key: 252 us for 402.
+//
+// A score that takes the difference to a constant far from its own bias loses
+// its low bits (the bias of a key beside masked ones at -30000), so in a crossed
+// tile a constant beyond kMaxMiddle (or not a number) gives way to 0.  Up to it a
+// logit is off by at most 2^-24 * 22, as one of that size is anyway.
+constexpr float kMaxMiddle = 32.0f;  // log2 units
+
 struct FwdPiece {
   float lo, hi;  // the difference before and, kPieceStep, from the boundary on
   int kind;      // PieceKind
@@ -318,7 +325,8 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
           piece.step = PieceCode::step(code);
           const bool crossed = __shfl_sync(0xffffffffu, piece.kind, lane | 7) != kPieceConst;
           float mid = __shfl_sync(0xffffffffu, piece.lo, lane | 7);
-          if (crossed && !isfinite(mid)) mid = 0.f;  // differences to it have to mean something
+          // differences to it have to keep the scores' bits
+          if (crossed && !(fabsf(mid * a.scale_log2) <= kMaxMiddle)) mid = 0.f;
           const bool tile = (lane & 7) == 7;
           piece.lo = tile ? mid * a.scale_log2 : piece.lo - mid;
           piece.hi = tile ? mid : piece.hi - mid;
@@ -610,12 +618,14 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
                          in_bounds(qv >= 0 && qv < static_cast<int64_t>(a.batch) * a.S * a.hq && lse_i >= 0 &&
                                        lse_i < static_cast<int64_t>(a.batch) * a.hq * a.S,
                                    a.err);
-      // l_run and O carry 2^kPBias; O also carries V's 2^-e
-      const float lse_p = l_run > 0.f ? (m_run + log2f(l_run) - kPBias) * kLn2 : -INFINITY;
+      // l_run and O carry 2^kPBias; O also carries V's 2^-e.  BIAS: a row without keys
+      // has l_run = 0, and one that met a NaN keeps it (in its LSE for the gradient as well)
+      const bool any = BIAS ? l_run != 0.f : l_run > 0.f;
+      const float lse_p = any ? (m_run + log2f(l_run) - kPBias) * kLn2 : -INFINITY;
       const float o_mul = __int_as_float((127 + v16_shift(*a.v_amax)) << 23);  // 2^e
       float* lse_ptr = a.lse + lse_i;
       if constexpr (!STEP) {
-        const float inv = l_run > 0.f ? o_mul / l_run : 0.f;
+        const float inv = any ? o_mul / l_run : 0.f;
         __nv_bfloat16* orow = a.o + qv * D;
         __nv_bfloat16* rrow = a.o_res ? a.o_res + qv * D : nullptr;
 #pragma unroll 1
@@ -665,9 +675,9 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
           const float wa = la == -INFINITY ? 0.f : exp2f((la - mm) * kLog2e);
           const float wp = lse_p == -INFINITY ? 0.f : exp2f((lse_p - mm) * kLog2e);
           const float tot = wa + wp;
-          if (tot > 0.f) {
+          if (BIAS ? tot != 0.f : tot > 0.f) {
             ca = wa / tot;
-            cpart = wp > 0.f ? wp * o_mul / (tot * l_run) : 0.f;  // an empty part has l_run = 0
+            cpart = BIAS && wp == 0.f ? 0.f : wp * o_mul / (tot * l_run);
             lse_new = mm + log2f(tot) * kLn2;
           }
         }

@@ -27,9 +27,12 @@ namespace {
 constexpr int kMaxIntervals = 256;
 constexpr int kMaxBuckets = 256;
 constexpr int kThreads = 256;
-// Below this a table value masks, as -inf does: the score's own part is lost in
-// it anyway, and divided by the smallest scale accepted it is still finite.
-constexpr float kMaskBelow = -1.2676506002282294e30f;  // -2^100
+// The finite values a bias may have.  From -kBound down it masks, as -inf does,
+// from kBound up it is as +inf: a softmax reference of that size, rounded to 24
+// bits, is off by up to 2^-3 in log2 units, which fp16 P still has room for (its
+// bound 2^15 is half of what fp16 holds), and a score beside it has 3 bits left.
+// Divided by the smallest scale accepted it is finite.
+constexpr float kBound = 1048576.f;  // 2^20
 constexpr float kMinScale = 5.9604645e-8f;             // 2^-24
 constexpr int64_t kMaxSeqlen = int64_t{1} << 29;       // places fit 32 bits
 constexpr int kSumSplits = 64;
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
   float* lut = const_cast<float*>(out.lut);
   for (int h = blockIdx.y; h < hq; h += gridDim.y) {
     const float v = __bfloat162float(row[h]);
-    lut[h * out.len + i] = v <= kMaskBelow ? -INFINITY : v * inv_scale;
+    lut[h * out.len + i] = v <= -kBound ? -INFINITY : v >= kBound ? INFINITY : v * inv_scale;
   }
 }
 

@@ -427,9 +427,9 @@ __global__ void __launch_bounds__(256) bwd_rowstats_kernel(
       const int64_t pos = bh * stat_len + static_cast<int64_t>(blk_i) * blk_pad + (si - blk_i * blk);
       if (in_bounds(pos >= 0 && pos < (bh + 1) * stat_len, err)) {
         dstat[pos] = acc;
-        // a row that a bias of -inf left nothing: its P must come out 0
+        // with a bias (sign -1) a row may have been left nothing: its P must come out 0
         const float l = lse[bh * S + s];
-        lse2[pos] = l == -INFINITY ? sign * INFINITY : l * (sign * kLog2e);
+        lse2[pos] = sign < 0.f && l == -INFINITY ? l : l * (sign * kLog2e);
       }
     }
   }

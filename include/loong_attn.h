@@ -339,10 +339,12 @@ LOONG_API int loong_headctx_pack_n(int32_t n, int64_t batch, int32_t cp, int32_t
  *                (several intervals may share one), or NULL: interval i is
  *                bucket i.
  *   table        DEVICE bf16 [num_buckets][hq], 2-byte aligned.  A value of
- *                -2^100 or less (the type's lowest and -inf included) masks: its
- *                keys get no weight.  A query that this leaves no key gets O = 0
- *                and LSE = -inf, and adds nothing to any gradient.  Masked keys
- *                are still read and multiplied.
+ *                -2^20 or less (-1e9, the type's lowest and -inf included)
+ *                masks: its keys get no weight.  A query that this leaves no
+ *                key gets O = 0 and LSE = -inf, and adds nothing to any
+ *                gradient.  Masked keys are still read and multiplied.  2^20 or
+ *                more counts as +inf: like NaN, it makes the outputs NaN that
+ *                it enters.  A bucket that no pair falls in is never used.
  * The two host arrays are read during the call only.
  */
 typedef struct {

@@ -285,6 +285,73 @@ def test_checked_build(cuda_device, monkeypatch, name):
     _check(w, x, t, buckets, _run(w, x, t, buckets))
 
 
+# S, hq, hkv, d, causal, buckets, the masked bucket: a window, a hole, many boundaries in a piece, both signs
+MASKED = {
+    "window": (900, 2, 1, 64, True, (3, [150, 400]), 2),
+    "hole": (700, 4, 2, 128, True, (4, [3, 60, 333]), 1),
+    "comb": (300, 2, 2, 64, True, (2, list(range(1, 200)), [i & 1 for i in range(200)]), 1),
+    "band": (513, 2, 1, 128, False, (3, [-99, 100]), 0),
+}
+
+
+@pytest.mark.parametrize("value", [-30000.0, -65504.0, -1e9, -1e30])
+@pytest.mark.parametrize("name", list(MASKED))
+def test_finite_masks(cuda_device, name, value):
+    """Masks written as large finite numbers: where every query keeps a key, exp(value) is 0 beside it in float64
+    as well, so every output is that of -inf, within the tolerances of the other buckets' logits."""
+    S, hq, hkv, d, causal, bk, at = MASKED[name]
+    w = inputs.Workload(name, S, hq, hkv, d, 1, 1, 1, 1, True, placement=0, causal=causal)
+    x, buckets = inputs.make_inputs(w, device="cuda"), ops.RelBuckets(*bk)
+    t = torch.randn((buckets.num_buckets, hq), generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    t[at] = value
+    t = t.to(torch.bfloat16)
+    out = _run(w, x, t, buckets)
+    t[at] = -torch.inf
+    _check(w, x, t, buckets, out)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e9])
+def test_buckets_out_of_reach(cuda_device, value):
+    """What stands in buckets that no pair falls in (ahead of a causal query, beyond the sequence) changes no bit
+    of what has a fixed order."""
+    w = inputs.Workload("reach", 300, 4, 2, 64, 1, 3, 3, 1, True, placement=0)
+    x, buckets = inputs.make_inputs(w, device="cuda"), ops.RelBuckets(5, [-40, 0, 33, 300])
+    t = torch.randn((5, 4), generator=torch.Generator(device="cuda").manual_seed(7), device="cuda").to(torch.bfloat16)
+    t[0], t[1], t[4] = 0, 0, 0
+    want = _run(w, x, t, buckets)
+    t[0], t[1], t[4] = value, value, value
+    got = _run(w, x, t, buckets)
+    for i in (0, 1, 3, 4, 5):
+        assert torch.equal(got[i], want[i])
+    assert (got[2].float() - want[2].float()).abs().max() <= 2.0 ** -7 * want[2].float().abs().max()
+
+
+@pytest.mark.parametrize("mode", [ops.MODE_FUSED, ops.MODE_STEPWISE])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 2.0 ** 20])
+def test_values_out_of_range_show(cuda_device, value, mode):
+    """Rows that meet one are NaN, the others as they were; so are the gradients of what those rows enter."""
+    w = inputs.Workload("range", 400, 2, 1, 64, 1, 2, 2, 1, True, placement=0)
+    x, buckets = inputs.make_inputs(w, device="cuda"), ops.RelBuckets(2, [170])
+    t = torch.zeros((2, 2), device="cuda", dtype=torch.bfloat16)
+    want = _run(w, x, t, buckets, mode=mode)
+    t[1] = value
+    o, lse, dq, dk, dv, dt = _run(w, x, t, buckets, mode=mode)
+    assert torch.equal(o[:, :170], want[0][:, :170]) and torch.equal(lse[..., :170], want[1][..., :170])
+    assert bool(o[:, 170:].isnan().all()) and bool(lse[..., 170:].isnan().all())
+    for name, grad in (("dq", dq[:, 170:]), ("dk", dk), ("dv", dv), ("dtable", dt)):
+        assert bool(grad.isnan().all()), name
+
+
+@pytest.mark.parametrize("mode", [ops.MODE_FUSED, ops.MODE_STEPWISE])
+def test_plain_attention_shows_nan(cuda_device, mode):
+    """Without a bias, a NaN key makes every row NaN that sees it."""
+    w = inputs.Workload("nan", 400, 2, 1, 64, 1, 2, 2, 1, True, placement=0)
+    x = inputs.make_inputs(w, device="cuda")
+    x["k"][:, 250, :, 3] = float("nan")
+    o = ops.attn_fwd(w, x["q"], x["k"], x["v"], mode=mode)[0]
+    assert bool(o[:, 250:].isnan().all()) and not bool(o[:, :250].isnan().any())
+
+
 def test_long_context(cuda_device):
     """20,010 tokens on a ring of five: walks over many intervals, blocks that are no multiple of a tile, far
     boundaries.  Every output against float64 torch, rows of queries at a time, in the norm: each bf16 rounding
