@@ -147,10 +147,12 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current_raw_stream(index):
     """The current stream of a device as a number (a torch stream object costs 3 us)."""
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def make_desc(w, mode=MODE_FUSED, scale=0.0, layout=LAYOUT_NATURAL):
@@ -245,6 +247,7 @@ class RelBuckets:
         p32 = ctypes.POINTER(ctypes.c_int32)
         self._struct = LoongRelBias(self.num_buckets, self.num_bounds, ctypes.cast(self._bounds, p32),
                                     None if self._bucket_of is None else ctypes.cast(self._bucket_of, p32), None)
+        self._problems = {}
 
     @property
     def bounds(self):
@@ -260,6 +263,23 @@ class RelBuckets:
         if table is not None:
             b.table = table.data_ptr()
         return b
+
+    def _problem(self, w, mode, layout):
+        """(descriptor, workspace bytes forward, backward), checked; kept for a
+        Workload, which cannot change (nor can these buckets)."""
+        kept = type(w) is Workload
+        if kept:
+            p = self._problems.get((w, mode, layout))
+            if p is not None:
+                return p
+        desc, bias = make_desc(w, mode, layout=layout), self.struct()
+        _check("loong_rel_bias_check", loong_rel_bias_check(desc, bias))
+        p = desc, loong_attn_bias_workspace_size(desc, bias, 0), loong_attn_bias_workspace_size(desc, bias, 1)
+        if kept:
+            if len(self._problems) >= 64:
+                self._problems.clear()
+            self._problems[w, mode, layout] = p
+        return p
 
 
 def log_buckets(num_buckets, max_distance, causal=True):
@@ -456,9 +476,9 @@ def default_scale(d):
 
 def _same(name, t, shape, dtype, device):
     """The tensor arguments of the calls below: what the C entry cannot see."""
-    if not torch.is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, not {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
 
@@ -493,28 +513,26 @@ def _on(device, stream):
     return where, stream
 
 
-@functools.lru_cache(maxsize=256)
-def _desc_kept(w, mode, layout):
-    return make_desc(w, mode, layout=layout)
+def _checked_desc(w, layout):
+    desc = make_desc(w, MODE_FUSED, layout=layout)
+    _check("loong_attn_check", loong_attn_check(desc))
+    return desc
 
 
-def _desc_of(w, mode, layout):
-    """make_desc for reading only: kept for a Workload, which cannot change."""
-    return _desc_kept(w, mode, layout) if type(w) is Workload else make_desc(w, mode, layout=layout)
+_kept_desc = functools.lru_cache(maxsize=256)(_checked_desc)
 
 
-def _bias_problem(w, table, buckets, mode, layout):
-    desc, bias = _desc_of(w, mode, layout), buckets.struct(table)
-    _check("loong_rel_bias_check", loong_rel_bias_check(desc, bias))
-    _contiguous("table", table, (buckets.num_buckets, w.hq), torch.bfloat16, table.device)
-    return desc, bias
+def _desc_of(w, layout):
+    """A checked descriptor for reading only: kept for a Workload, which cannot change."""
+    return _kept_desc(w, layout) if type(w) is Workload else _checked_desc(w, layout)
 
 
 def attn_bias_fwd(w, q, k, v, table, buckets, mode=MODE_FUSED, stream=None, layout=LAYOUT_NATURAL, res=True):
     """attn_fwd with a learned relative position bias: ``table`` bf16
     [num_buckets, hq], ``buckets`` a RelBuckets (log_buckets makes the usual
     ones).  Returns (o, lse, o_res); o_res is None when ``res`` is false."""
-    desc, bias = _bias_problem(w, table, buckets, mode, layout)
+    desc, nbytes, _ = buckets._problem(w, mode, layout)
+    _contiguous("table", table, (buckets.num_buckets, w.hq), torch.bfloat16, table.device)
     for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv)):
         _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, table.device)
     where, stream = _on(table.device, stream)
@@ -522,15 +540,16 @@ def attn_bias_fwd(w, q, k, v, table, buckets, mode=MODE_FUSED, stream=None, layo
         o = torch.empty_like(q)
         o_res = torch.empty_like(q) if res else None
         lse = torch.empty((w.batch, w.hq, w.seqlen), dtype=torch.float32, device=q.device)
-        ws = torch.empty(loong_attn_bias_workspace_size(desc, bias, 0), dtype=torch.uint8, device=q.device)
-        loong_attn_bias_fwd(desc, bias, q, k, v, o, lse, o_res, ws, stream)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        loong_attn_bias_fwd(desc, buckets.struct(table), q, k, v, o, lse, o_res, ws, stream)
     return o, lse, o_res
 
 
 def attn_bias_bwd(w, q, k, v, o, lse, do, table, buckets, o_res=None, mode=MODE_FUSED, stream=None,
                   layout=LAYOUT_NATURAL):
     """Gradient of attn_bias_fwd: (dq, dk, dv, dtable), dtable bf16 like the table."""
-    desc, bias = _bias_problem(w, table, buckets, mode, layout)
+    desc, _, nbytes = buckets._problem(w, mode, layout)
+    _contiguous("table", table, (buckets.num_buckets, w.hq), torch.bfloat16, table.device)
     for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv), ("o", o, w.hq), ("do", do, w.hq),
                     ("o_res", o_res, w.hq)):
         if t is not None or n != "o_res":
@@ -539,8 +558,8 @@ def attn_bias_bwd(w, q, k, v, o, lse, do, table, buckets, o_res=None, mode=MODE_
     where, stream = _on(table.device, stream)
     with where:
         dq, dk, dv, dtable = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(table)
-        ws = torch.empty(loong_attn_bias_workspace_size(desc, bias, 1), dtype=torch.uint8, device=q.device)
-        loong_attn_bias_bwd(desc, bias, q, k, v, o, o_res, lse, do, dq, dk, dv, dtable, ws, stream)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        loong_attn_bias_bwd(desc, buckets.struct(table), q, k, v, o, o_res, lse, do, dq, dk, dv, dtable, ws, stream)
     return dq, dk, dv, dtable
 
 
@@ -618,8 +637,7 @@ def qk_norm_rope(w, opts, q, k, v=None, wq=None, wk=None, positions=None, pos_be
     attention's layout, in one pass: projections [B, S, heads, d] (views of one
     fused projection, or contiguous) -> (q, k, v) as attn_fwd takes them.  ``v``
     is only brought into the layout; None leaves it out."""
-    desc = _desc_of(w, MODE_FUSED, layout)
-    _check("loong_attn_check", loong_attn_check(desc))
+    desc = _desc_of(w, layout)
     _qk_weights(w, wq, wk, positions, q.device)
     o = opts._struct_of(_token_strides(("q", "k", "v"), (q, k, v), w, q.device), pos_begin=pos_begin)
     where, stream = _on(q.device, stream)
@@ -637,8 +655,7 @@ def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions
     there is none).  ``into``: the three projection gradients to write, e.g.
     views of one fused gradient (the third None without dv); else they are made
     contiguous."""
-    desc = _desc_of(w, MODE_FUSED, layout)
-    _check("loong_attn_check", loong_attn_check(desc))
+    desc = _desc_of(w, layout)
     _qk_weights(w, wq, wk, positions, q.device)
     for n, t, h in (("dq", dq, w.hq), ("dk", dk, w.hkv), ("dv", dv, w.hkv)):
         if t is not None or n != "dv":
