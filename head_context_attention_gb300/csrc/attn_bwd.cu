@@ -703,61 +703,21 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           float* ph = part + head * a.bias.intervals;
           // lane l, column c: distance at place base + c - l
           const uint8_t* at = a.bias.interval + place.place + 32 * (grp - quarter);
-          // Two ways to the diagonals' sums.  d = 64, where the compute warps bind:
-          // columns joined pairwise in five levels of independent shuffles (1K and
-          // 2K token passes 48.3 and 114.2 us, the other way 52.1 and 118.8).
-          // d = 128: one column after the other, a chain of shuffles that fits the
-          // wait for dQ and half the code (16K token pass 5.15 ms, the other way
-          // 5.25: the code of tiles that never come here runs slower beside it).
-          float lower, upper;      // by lane: sums of the distances at places
-          int lower_at, upper_at;  // at[lower_at], at[upper_at]
+          // The diagonals' sums, one column after the other: a distance's sum moves one
+          // lane up with every column, a chain of shuffles that fits the wait for dQ.
+          // (Columns joined pairwise in five levels of independent shuffles: twice the
+          // code and no faster, 2K ragged tokens of 64 112.4 us for 110.9, 16K of 128
+          // 5.15 ms for 5.16.)
           int ln = lane;
-          asm volatile("" : "+r"(ln));  // keeps the lanes' shifts from being formed, and held, outside the loop
-          if constexpr (D == 64) {
-            // sum[c], over[c]: columns c .. c + w - 1 summed along the diagonals, by
-            // the lane a diagonal has in the last of them, and 32 lanes further on
-            float sum[32], over[32];
+          asm volatile("" : "+r"(ln));  // keeps the lanes' tests from being formed, and held, outside the loop
+          float acc = 0.f, fin = 0.f;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              sum[c] = pv[0][c];
-              over[c] = 0.f;
-            }
-            auto join = [&](int c, int w) {
-              const float x = __shfl_sync(0xffffffffu, sum[c], (ln - w) & 31);
-              const float y = w > 1 ? __shfl_sync(0xffffffffu, over[c], (ln - w) & 31) : 0.f;
-              sum[c] = sum[c + w] + (ln >= w ? x : 0.f);
-              over[c] = over[c + w] + y + (ln < w ? x : 0.f);  // y is 0 where it wrapped
-            };
-#pragma unroll
-            for (int c8 = 0; c8 < 32; c8 += 8) {  // eight columns at a time: fewer sums live
-#pragma unroll
-              for (int w = 1; w < 8; w <<= 1)
-#pragma unroll
-                for (int c = c8; c < c8 + 8; c += 2 * w) join(c, w);
-              __syncwarp();
-            }
-            join(0, 8);
-            join(16, 8);
-            join(0, 16);
-            upper = sum[0];
-            upper_at = 31 - ln;
-            lower = over[0];  // nothing in lane 31
-            lower_at = -1 - min(ln, 30);
-          } else {
-            // a distance's sum moves one lane up with every column
-            float acc = 0.f, fin = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              acc += pv[0][c];
-              const float done = __shfl_sync(0xffffffffu, acc, 31);  // complete: distance base + c - 31
-              if (ln == c) fin = done;
-              acc = __shfl_up_sync(0xffffffffu, acc, 1);
-              if (ln == 0) acc = 0.f;
-            }
-            lower = fin;
-            lower_at = ln - 31;
-            upper = acc;  // nothing in lane 0
-            upper_at = 32 - max(ln, 1);
+          for (int c = 0; c < 32; ++c) {
+            acc += pv[0][c];
+            const float done = __shfl_sync(0xffffffffu, acc, 31);  // complete: distance base + c - 31
+            if (ln == c) fin = done;
+            acc = __shfl_up_sync(0xffffffffu, acc, 1);
+            if (ln == 0) acc = 0.f;
           }
           // every interval is a run of lanes
           auto add_runs = [&](float v, int id) {
@@ -770,8 +730,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             const int before = __shfl_up_sync(0xffffffffu, id, 1);
             if (ln == 0 || before != id) atomicAdd(ph + id, v);
           };
-          add_runs(upper, at[upper_at]);
-          add_runs(lower, at[lower_at]);
+          add_runs(acc, at[32 - max(ln, 1)]);  // nothing in lane 0
+          add_runs(fin, at[ln - 31]);
         }
       }
 

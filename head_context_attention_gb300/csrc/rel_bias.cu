@@ -36,9 +36,11 @@ constexpr float kBound = 1048576.f;  // 2^20
 constexpr float kMinScale = 5.9604645e-8f;             // 2^-24
 constexpr int64_t kMaxSeqlen = int64_t{1} << 29;       // places fit 32 bits
 constexpr int kSumSplits = 64;
-// V of at most this many vectors of 8 is converted by one block: measured at
-// 100 tokens of 2 heads of 64 (1,600 vectors) against the two launches.
-constexpr int64_t kBlockV = 4096;
+// V of at most this many vectors of 8 is converted by one block, beside the
+// expansion, else by two launches.  The forward of heads of 64, one block and two
+// launches: 1,600 vectors 17.1 and 20.8 us, 4,096 21.0 and 23.0, 6,144 23.1 and
+// 24.7, 8,192 25.1 and 25.2, 12,288 29.2 and 27.1.
+constexpr int64_t kBlockV = 8192;
 
 struct BucketMap {
   int intervals;
