@@ -210,6 +210,21 @@ FwdWsLayout fwd_ws_layout(const loong_attn_desc& d) {
   return L;
 }
 
+BwdWsLayout bwd_ws_layout(const loong_attn_desc& d) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t q_elems = static_cast<size_t>(d.batch) * d.seqlen * d.hq * d.head_dim;
+  const size_t kv_elems = static_cast<size_t>(d.batch) * d.seqlen * d.hkv * d.head_dim;
+  const size_t stats = 2 * static_cast<size_t>(d.batch) * d.hq * stat_row_len(ring_geom(d));
+  BwdWsLayout L{};
+  L.dq_acc = 0;
+  L.stats = up(q_elems * 4);
+  L.dk_acc = L.stats + up(stats * 4);
+  L.dv_acc = L.dk_acc + up(kv_elems * 4);
+  L.recv = L.dv_acc + up(kv_elems * 4);
+  L.total = L.recv + (is_copy_mode(d) ? 4 * up(kv_elems * 2) : 0);  // two receive buffers each for K and V
+  return L;
+}
+
 // The forward's scratch pointers inside a workspace of fwd_ws_layout(d).total bytes.
 static FwdScratch fwd_scratch(const loong_attn_desc& d, void* ws, void* o_res) {
   const FwdWsLayout L = fwd_ws_layout(d);
@@ -239,18 +254,11 @@ int run_attn_fwd(const loong_attn_desc& d, const void* q, const void* k, const v
 int run_attn_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
                  const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
                  cudaStream_t stream, const BiasView* bias, float* dbias_part) {
-  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t q_elems = static_cast<size_t>(d.batch) * d.seqlen * d.hq * d.head_dim;
-  const size_t kv_elems = static_cast<size_t>(d.batch) * d.seqlen * d.hkv * d.head_dim;
-  const size_t stats = 2 * static_cast<size_t>(d.batch) * d.hq * stat_row_len(ring_geom(d));
+  const BwdWsLayout L = bwd_ws_layout(d);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  float* dq_acc = reinterpret_cast<float*>(w);
-  float* dvec = reinterpret_cast<float*>(w + up(q_elems * 4));
-  float* dk_acc = reinterpret_cast<float*>(w + up(q_elems * 4) + up(stats * 4));
-  float* dv_acc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dk_acc) + up(kv_elems * 4));
-  void* recv = is_copy_mode(d) ? reinterpret_cast<uint8_t*>(dv_acc) + up(kv_elems * 4) : nullptr;
-  return launch_bwd(d, q, k, v, o, o_res, lse, dout, dq, dk, dv, dq_acc, dvec, dk_acc, dv_acc, stream, recv, bias,
-                    dbias_part);
+  auto part = [&](size_t off) { return reinterpret_cast<float*>(w + off); };
+  return launch_bwd(d, q, k, v, o, o_res, lse, dout, dq, dk, dv, part(L.dq_acc), part(L.stats), part(L.dk_acc),
+                    part(L.dv_acc), stream, is_copy_mode(d) ? w + L.recv : nullptr, bias, dbias_part);
 }
 
 Layout layout_of(const loong_attn_desc& d) {
@@ -318,15 +326,8 @@ int loong_attn_check(const loong_attn_desc* d) {
 
 size_t loong_attn_workspace_size(const loong_attn_desc* d, int pass) {
   if (loong_attn_check(d) != LOONG_OK) return 0;
-  const size_t q_elems = static_cast<size_t>(d->batch) * d->seqlen * d->hq * d->head_dim;
-  const size_t kv_elems = static_cast<size_t>(d->batch) * d->seqlen * d->hkv * d->head_dim;
-  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  // STEPWISE_COPY: two receive buffers each for K and V, bf16
-  const size_t recv = is_copy_mode(*d) ? 4 * up(kv_elems * 2) : 0;
   if (pass == 0) return fwd_ws_layout(*d).total;
-  if (pass != 1) return 0;
-  const size_t stats = 2 * static_cast<size_t>(d->batch) * d->hq * stat_row_len(ring_geom(*d));
-  return up(q_elems * 4) + up(stats * 4) + 2 * up(kv_elems * 4) + recv;
+  return pass == 1 ? bwd_ws_layout(*d).total : 0;
 }
 
 int loong_ring_schedule(int32_t inner, int32_t outer, int32_t* src) {

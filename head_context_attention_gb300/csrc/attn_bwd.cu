@@ -999,7 +999,7 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
   const int64_t kv_elems = d.batch * d.seqlen * d.hkv * d.head_dim;
   const bool step = d.mode != LOONG_MODE_FUSED;
   int st;
-  cudaError_t e = cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
+  cudaError_t e = bias ? cudaSuccess : cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   // FUSED walks of at most kFlush (tile, head) pairs never touch the dK, dV accumulators
   const RingGeom g = ring_geom(d);
@@ -1008,13 +1008,13 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
       ((e = cudaMemsetAsync(dk_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess ||
        (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess))
     return cuda_fail(e);
-  if ((st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream, bias != nullptr)) != LOONG_OK) return st;
+  if (!bias && (st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream)) != LOONG_OK) return st;
   st = bias ? launch_bwd_b<true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,
                                  dbias_part)
             : launch_bwd_b<false>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, nullptr,
                                   nullptr);
   if (st != LOONG_OK) return st;
-  if ((st = launch_f32_to_bf16(dq_acc, dq, q_elems, stream)) != LOONG_OK) return st;
+  if (!bias && (st = launch_f32_to_bf16(dq_acc, dq, q_elems, stream)) != LOONG_OK) return st;
   if (step) {
     if ((st = launch_f32_to_bf16(dk_acc, dk, kv_elems, stream)) != LOONG_OK) return st;
     if ((st = launch_f32_to_bf16(dv_acc, dv, kv_elems, stream)) != LOONG_OK) return st;

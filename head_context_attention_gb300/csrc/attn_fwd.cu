@@ -831,9 +831,8 @@ int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const voi
                const BiasView* bias) {
   if (rank_end < 0) rank_end = d.cp;
   int st;
-  if (!(bias && bias->v_ready) &&
-      (st = launch_v_to_f16(v, sc.v16, sc.v_amax, d.batch * d.seqlen * d.hkv * d.head_dim, stream,
-                            bias != nullptr)) != LOONG_OK)
+  if (!bias && (st = launch_v_to_f16(v, sc.v16, sc.v_amax, d.batch * d.seqlen * d.hkv * d.head_dim, stream)) !=
+                   LOONG_OK)
     return st;
   return bias ? launch_fwd_b<true>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
               : launch_fwd_b<false>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr);

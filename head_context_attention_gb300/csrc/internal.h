@@ -88,6 +88,12 @@ struct FwdWsLayout {
 };
 FwdWsLayout fwd_ws_layout(const loong_attn_desc& d);
 
+// The same for the backward.
+struct BwdWsLayout {
+  size_t dq_acc, stats, dk_acc, dv_acc, recv, total;
+};
+BwdWsLayout bwd_ws_layout(const loong_attn_desc& d);
+
 // The relative bias as the attention kernels read it (rel_bias.cu fills it):
 // place off + n stands for distance n = q - k, for every distance that any tile
 // reaches (masked and ragged rows included).
@@ -99,7 +105,6 @@ struct BiasView {
   int64_t len = 0;
   int off = 0;
   int intervals = 0;
-  int v_ready = 0;  // forward: V's fp16 form and max |V| are in the workspace already
 };
 
 // What a run of places [at - reach, at + reach] looks like, in one word.
@@ -119,11 +124,13 @@ struct PieceCode {
 
 // Kernel launchers (asynchronous on `stream`).
 // Query rows of ring ranks [rank_begin, rank_end) only (all of them: 0, cp).
-// The forward first writes V's fp16 copy into sc.v16 (with a bias, *sc.v_amax is 0 already).
+// The forward first writes V's fp16 copy into sc.v16 (with a bias it is there already).
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
                float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin = 0, int rank_end = -1,
                const BiasView* bias = nullptr);
-// o_res: the forward's residual of O, or null (D from O alone).
+// o_res: the forward's residual of O, or null (D from O alone).  With a bias the
+// row statistics are in dvec and dq_acc is zeroed already, and dq_acc is left to
+// the caller to convert.
 int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v,
                const void* o, const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv,
                float* dq_acc, float* dvec, float* dk_acc, float* dv_acc, cudaStream_t stream,
@@ -142,9 +149,8 @@ inline int64_t bwd_blocks(const loong_attn_desc& d) {
   const RingGeom g = ring_geom(d);
   return d.batch * d.hkv * static_cast<int64_t>(g.nblocks) * g.ntile;
 }
-// max |V| into *amax (two launches: the maximum, then V * 2^-e as fp16 into v16).
-// cleared: *amax is 0 already.
-int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream, bool cleared = false);
+// max |V| into *amax and V * 2^-e as fp16 into v16, two launches.
+int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream);
 
 int launch_fill_f32(float* p, int64_t n, float value, cudaStream_t stream);
 // One CTA whose bounded mbarrier wait has nothing to wait for (selftest.cu).
@@ -166,8 +172,12 @@ inline int stat_block_pad(int blk) { return (blk + 3) & ~3; }
 inline int64_t stat_row_len(const RingGeom& g) {
   return static_cast<int64_t>(g.nblocks) * stat_block_pad(g.blk) + kTile;
 }
-// With o_res, D = rowsum(dO * (O + O_res)).  negate: the LSE part as -LSE*log2(e).
+// With o_res, D = rowsum(dO * (O + O_res)).
 int launch_bwd_rowstats(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout,
-                        const float* lse, float* stats, cudaStream_t stream, bool negate = false);
+                        const float* lse, float* stats, cudaStream_t stream);
+struct RowStatsArgs;  // rowstats.cuh
+// What a block needs for it, and the passes over the tokens of a (head, sequence).
+int rowstats_args(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout, const float* lse,
+                  float* stats, RowStatsArgs* a, int* passes);
 
 }  // namespace loong

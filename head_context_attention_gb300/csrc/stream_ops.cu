@@ -11,6 +11,7 @@
 #include "fastdiv.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "rowstats.cuh"
 #include "v16.cuh"
 
 namespace loong {
@@ -370,69 +371,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
   }
 }
 
-// Backward row statistics (see stat_row_len): for row (b, s, h) of O and dO
-// (read where `lay` keeps them), D = sum_d dO*O in fp32 and LSE*log2(e),
-// written at the padded position of token s.  With o_res, O is taken as
-// O + O_res (exact in fp32: the residual holds the next 8 bits).  16 threads
-// per row of 128 bf16 (8 elements each), 8 for d = 64.  A block covers
-// consecutive tokens of one head (blockIdx.y) of one sequence (blockIdx.z),
-// so a thread finds its token and part by shifts; only the layout map and
-// the block position divide (32-bit).
+// See rowstats.cuh: passes over the tokens, heads, sequences.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_rowstats_kernel(
-    const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ o_res,
-    const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse, float* __restrict__ lse2,
-    float* __restrict__ dstat, int64_t rows, int S, int hq, int blk, int blk_pad, int64_t stat_len, Layout lay,
-    float sign, unsigned* err) {
-  constexpr int TPR = D / 8;         // threads per row
-  constexpr int RPB = 256 / TPR;     // rows (tokens) per block and pass
-  const int h = blockIdx.y;
-  const int b = blockIdx.z;
-  const int part = threadIdx.x % TPR;
-  const int lane_row = (threadIdx.x & 31) / TPR;  // this lane's row within its warp
-  const int64_t bh = static_cast<int64_t>(b) * hq + h;
-  // The loop runs per warp (lanes leave together) so the shuffles below see
-  // every lane; TPR divides 32, so a row's lanes are all live or all idle.
-  const int64_t step = static_cast<int64_t>(gridDim.x) * RPB;
-  for (int64_t s = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR; s - lane_row < S; s += step) {
-    const bool live = s < S;
-    float acc = 0.f;
-    bool row_ok = true;
-    if (live) {
-      const int64_t off = lay.vec(b, s, h, hq) * D;
-      // checked build: the row's O / dO vectors lie inside the tensors
-      row_ok = in_bounds(off >= 0 && off + D <= rows * D, err);
-      if (row_ok) {
-        const uint4 ov = __ldg(reinterpret_cast<const uint4*>(o + off) + part);
-        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(dout + off) + part);
-        const uint4 rv = o_res ? __ldg(reinterpret_cast<const uint4*>(o_res + off) + part) : make_uint4(0, 0, 0, 0);
-        const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
-        const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&gv);
-        const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&rv);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 fa = __bfloat1622float2(a2[e]);
-          const float2 fr = __bfloat1622float2(r2[e]);
-          const float2 fb = __bfloat1622float2(b2[e]);
-          acc = fmaf(fa.x + fr.x, fb.x, acc);
-          acc = fmaf(fa.y + fr.y, fb.y, acc);
-        }
-      }
-    }
-#pragma unroll
-    for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (live && part == 0 && row_ok) {
-      const int si = static_cast<int>(s);  // s < S < 2^31
-      const int blk_i = si / blk;
-      const int64_t pos = bh * stat_len + static_cast<int64_t>(blk_i) * blk_pad + (si - blk_i * blk);
-      if (in_bounds(pos >= 0 && pos < (bh + 1) * stat_len, err)) {
-        dstat[pos] = acc;
-        // with a bias (sign -1) a row may have been left nothing: its P must come out 0
-        const float l = lse[bh * S + s];
-        lse2[pos] = sign < 0.f && l == -INFINITY ? l : l * (sign * kLog2e);
-      }
-    }
-  }
+__global__ void __launch_bounds__(kRowStatsThreads) bwd_rowstats_kernel(const __grid_constant__ RowStatsArgs a) {
+  rowstats_block<D, false>(a, blockIdx.x, gridDim.x, blockIdx.y, blockIdx.z);
 }
 
 }  // namespace
@@ -450,12 +392,10 @@ int launch_f32_to_bf16(const float* in, void* out, int64_t n, cudaStream_t strea
   return check_launch();
 }
 
-int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream, bool cleared) {
+int launch_v_to_f16(const void* v, void* v16, unsigned* amax, int64_t n, cudaStream_t stream) {
   if (n <= 0 || n % 8) return LOONG_ERR_INVALID_ARG;
-  if (!cleared) {
-    const cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(unsigned), stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
+  cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(unsigned), stream);
+  if (e != cudaSuccess) return cuda_fail(e);
   const int64_t nvec = n / 8;
   absmax_bf16_kernel<<<grid_for(nvec, 256, 8), 256, 0, stream>>>(static_cast<const uint4*>(v), nvec, amax);
   int st = check_launch();
@@ -548,35 +488,42 @@ int launch_headctx_pack(int n, int64_t batch, int cp, int P, int64_t s_local, co
   return check_launch();
 }
 
-int launch_bwd_rowstats(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout,
-                        const float* lse, float* stats, cudaStream_t stream, bool negate) {
-  const RingGeom g = ring_geom(d);
-  const int64_t rows = d.batch * d.seqlen * d.hq;
-  const int64_t stat_len = stat_row_len(g);
-  float* lse2 = stats;
-  float* dstat = stats + d.batch * d.hq * stat_len;
-  const auto* po = static_cast<const __nv_bfloat16*>(o);
-  const auto* pr = static_cast<const __nv_bfloat16*>(o_res);
-  const auto* pd = static_cast<const __nv_bfloat16*>(dout);
-  const int bp = stat_block_pad(g.blk);
-  unsigned* err = device_error_word();
-  if (!err) return LOONG_ERR_CUDA;
-  // grid: (passes over the tokens, heads, sequences); about 32 blocks of 256
-  // threads per SM in all, each striding over its (head, sequence) slice
+int rowstats_args(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout, const float* lse,
+                  float* stats, RowStatsArgs* a, int* passes) {
+  // about 32 blocks of 256 threads per SM in all, each striding over its (head, sequence) slice
   if (d.hq > 65535 || d.batch > 65535) return LOONG_ERR_INVALID_ARG;
-  const int rpb = 256 / (d.head_dim / 8);
-  const int64_t slices = static_cast<int64_t>(d.hq) * d.batch;
-  const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * 32 / slices);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((d.seqlen + rpb - 1) / rpb, want)),
-                  static_cast<unsigned>(d.hq), static_cast<unsigned>(d.batch));
+  if (d.head_dim != 128 && d.head_dim != 64) return LOONG_ERR_UNSUPPORTED;
+  const RingGeom g = ring_geom(d);
+  a->stat_len = stat_row_len(g);
+  a->lse2 = stats;
+  a->dstat = stats + d.batch * d.hq * a->stat_len;
+  a->o = static_cast<const __nv_bfloat16*>(o);
+  a->o_res = static_cast<const __nv_bfloat16*>(o_res);
+  a->dout = static_cast<const __nv_bfloat16*>(dout);
+  a->lse = lse;
+  a->rows = d.batch * d.seqlen * d.hq;
+  a->S = static_cast<int>(d.seqlen);
+  a->hq = d.hq;
+  a->blk = g.blk;
+  a->blk_pad = stat_block_pad(g.blk);
+  a->lay = layout_of(d);
+  if (!(a->err = device_error_word())) return LOONG_ERR_CUDA;
+  const int rpb = kRowStatsThreads / (d.head_dim / 8);
+  const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * 32 / (d.hq * d.batch));
+  *passes = static_cast<int>(std::min<int64_t>((d.seqlen + rpb - 1) / rpb, want));
+  return LOONG_OK;
+}
+
+int launch_bwd_rowstats(const loong_attn_desc& d, const void* o, const void* o_res, const void* dout,
+                        const float* lse, float* stats, cudaStream_t stream) {
+  RowStatsArgs a;
+  int passes, st;
+  if ((st = rowstats_args(d, o, o_res, dout, lse, stats, &a, &passes)) != LOONG_OK) return st;
+  const dim3 grid(static_cast<unsigned>(passes), static_cast<unsigned>(d.hq), static_cast<unsigned>(d.batch));
   if (d.head_dim == 128)
-    bwd_rowstats_kernel<128><<<grid, 256, 0, stream>>>(po, pr, pd, lse, lse2, dstat, rows, d.seqlen, d.hq, g.blk,
-                                                       bp, stat_len, layout_of(d), negate ? -1.f : 1.f, err);
-  else if (d.head_dim == 64)
-    bwd_rowstats_kernel<64><<<grid, 256, 0, stream>>>(po, pr, pd, lse, lse2, dstat, rows, d.seqlen, d.hq, g.blk,
-                                                      bp, stat_len, layout_of(d), negate ? -1.f : 1.f, err);
+    bwd_rowstats_kernel<128><<<grid, kRowStatsThreads, 0, stream>>>(a);
   else
-    return LOONG_ERR_UNSUPPORTED;
+    bwd_rowstats_kernel<64><<<grid, kRowStatsThreads, 0, stream>>>(a);
   return check_launch();
 }
 

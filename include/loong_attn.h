@@ -367,9 +367,10 @@ LOONG_API int loong_rel_bias_check(const loong_attn_desc* desc, const loong_rel_
  * loong_attn_bias_bwd (pass 1); 0 for invalid arguments.  Host-only.
  * loong_attn_workspace_size's, then the bias of every distance (fp32,
  * hq * (S + 384) values, hq * (2 S + 256) non-causal), its interval (bytes) and
- * two words on its surroundings, and for the backward the gradient's parts: 16 * (hq/hkv) * (num_bounds + 1)
- * fp32 for every (sequence, kv head, 128-key tile), a word for every head, and
- * 64 sums of the parts.
+ * two words on its surroundings; for the forward 1,216 words more; for the
+ * backward the gradient's parts, 16 * (hq/hkv) * (num_bounds + 1) fp32 for every
+ * (sequence, kv head, 128-key tile), a word for every head, and 64 sums of the
+ * parts.
  */
 LOONG_API size_t loong_attn_bias_workspace_size(const loong_attn_desc* desc, const loong_rel_bias* bias, int pass);
 

@@ -57,7 +57,8 @@ def test_bias_workspace_sizes(loong_lib, causal, mode):
     b = ops.log_buckets(32, 128, causal=bool(causal))
     length = W.seqlen + 384 if causal else 2 * W.seqlen + 256
     lut = up(4 * W.hq * length) + up(length) + 2 * up(4 * length)
-    assert ops.loong_attn_bias_workspace_size(d, b.struct(), 0) == up(ops.loong_attn_workspace_size(d, 0)) + lut
+    assert ops.loong_attn_bias_workspace_size(d, b.struct(), 0) == \
+        up(ops.loong_attn_workspace_size(d, 0)) + lut + up(1216 * 4)
     width = (W.hq // W.hkv) * (b.num_bounds + 1)
     part = up(4 * 16 * width * W.hkv * (W.seqlen // 128))
     assert ops.loong_attn_bias_workspace_size(d, b.struct(), 1) == \
