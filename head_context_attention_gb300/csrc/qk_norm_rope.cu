@@ -364,11 +364,14 @@ struct BatchWalk {
 
 // Slots per batch and batches per warp in shared memory: the loads of DEPTH - 1
 // batches are in flight while one is used.  Measured at 32 + 8 heads of 128
-// (ranks' layout), forward at 32K and backward at 128K tokens: forward 4 x 6
-// 131 us (6.1 TB/s), 4 x 3 133, 2 x 6 with three blocks per SM 142 (its 80
-// registers spill); backward 2 x 3 710 us (6.4 TB/s), 2 x 4 713, 4 x 3 1015,
-// 2 x 3 with three blocks 1840.
-constexpr int kFwdBatch = 4, kFwdDepth = 6, kFwdBlocks = 2;
+// (ranks' layout), forward at 32K and backward at 128K tokens: forward 2 x 6
+// 127 us (6.3 TB/s; a plain copy of the same bytes 121), 2 x 3 131, 3 x 4 132,
+// 4 x 6 130, 4 x 4 141, 1 x 8 135, three blocks per SM spill; backward 2 x 3
+// 678 us (6.7 TB/s), 2 x 2 727, 2 x 4 681, 1 x 6 700, 3 x 2 748.  Both store
+// with the streaming hint: what a pass writes is larger than L2 long before
+// time matters, and kept there it delays the loads (forward 141, backward 710 us
+// without).
+constexpr int kFwdBatch = 2, kFwdDepth = 6, kFwdBlocks = 2;
 constexpr int kBwdBatch = 2, kBwdDepth = 3, kBwdBlocks = 2;
 constexpr int kTableBytes = kWarps * 128 * 4;  // a warp's cosines and sines
 constexpr int kFwdSmem = kTableBytes + kWarps * kFwdDepth * kFwdBatch * 512;
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) qk_fwd_kernel(const __gr
             y = pack8(g);
           }
           if (h < h1 && in_bounds(out.at >= 0 && out.at + 8 <= a.out_elems[ti], a.err))
-            *reinterpret_cast<uint4*>(t.out + out.at) = y;
+            __stcs(reinterpret_cast<uint4*>(t.out + out.at), y);
           h += HPW;
           out.next<D>();
         }
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_bwd_kernel(const __gr
             }
             y = pack8(g);
           }
-          if (h < h1) *reinterpret_cast<uint4*>(dst) = y;
+          if (h < h1) __stcs(reinterpret_cast<uint4*>(dst), y);
           h += HPW;
           dst += HPW * D;
         }

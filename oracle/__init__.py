@@ -15,6 +15,8 @@ ring       a second, chunked oracle that walks the ring schedule block pair by
            block pair and merges the partial results by log-sum-exp.
 merge      n-way log-sum-exp merge of partial attention outputs.
 repack     the Ulysses head-context layout repack (S/P,H) <-> (S,H/P).
+qk         RMS norm and rotation of query and key heads, and their gradient.
+bias       attention with a bucketed relative position bias, and its gradients.
 
 Sources (page title, section):
   [G]  "Guide to LoongTrain: 2D Head-Context Parallelism for LLMs"
