@@ -606,27 +606,30 @@ def make_qk_opts(head_dim, **kw):
     return QkOpts(head_dim, **kw)
 
 
-def _token_stride(name, t, w, heads, device):
-    """Elements from token to token of a projection: a [B, S, heads, d] view
-    whose heads are contiguous and whose sequences follow each other."""
-    _same(name, t, (w.batch, w.seqlen, heads, w.head_dim), torch.bfloat16, device)
-    sb, ss, sh, sd = t.stride()
-    row = heads * w.head_dim
-    if w.seqlen == 1:  # the token's stride is the sequence's
-        ss = sb if w.batch > 1 else row
-    if sd != 1 or (sh != w.head_dim and heads > 1) or (w.batch > 1 and sb != w.seqlen * ss):
-        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, not strides {t.stride()}")
-    return ss
-
-
 def _token_strides(names, ts, w, device):
-    return [0 if t is None else _token_stride(n, t, w, h, device) for n, t, h in zip(names, ts, (w.hq, w.hkv, w.hkv))]
+    """Elements from token to token of projections: [B, S, heads, d] views whose
+    heads are contiguous and whose sequences follow each other; 0 for None."""
+    b, s, d = w.batch, w.seqlen, w.head_dim
+    out = []
+    for name, t, heads in zip(names, ts, (w.hq, w.hkv, w.hkv)):
+        if t is None:
+            out.append(0)
+            continue
+        _same(name, t, (b, s, heads, d), torch.bfloat16, device)
+        sb, ss, sh, sd = t.stride()
+        if s == 1:  # the token's stride is the sequence's
+            ss = sb if b > 1 else heads * d
+        if sd != 1 or (sh != d and heads > 1) or (b > 1 and sb != s * ss):
+            raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, not strides {t.stride()}")
+        out.append(ss)
+    return out
 
 
 def _qk_weights(w, wq, wk, positions, device):
-    for n, t in (("wq", wq), ("wk", wk)):
-        if t is not None:
-            _contiguous(n, t, (w.head_dim,), torch.float32, device)
+    if wq is not None:
+        _contiguous("wq", wq, (w.head_dim,), torch.float32, device)
+    if wk is not None:
+        _contiguous("wk", wk, (w.head_dim,), torch.float32, device)
     if positions is not None:
         _contiguous("positions", positions, (w.batch, w.seqlen), torch.int64, device)
 
@@ -642,7 +645,7 @@ def qk_norm_rope(w, opts, q, k, v=None, wq=None, wk=None, positions=None, pos_be
     o = opts._struct_of(_token_strides(("q", "k", "v"), (q, k, v), w, q.device), pos_begin=pos_begin)
     where, stream = _on(q.device, stream)
     with where:
-        out = [None if t is None else torch.empty(_attn_shape(w, h, layout), dtype=torch.bfloat16, device=q.device)
+        out = [None if t is None else q.new_empty(_attn_shape(w, h, layout))
                for t, h in ((q, w.hq), (k, w.hkv), (v, w.hkv))]
         loong_qk_norm_rope_fwd(desc, o, q, k, v, wq, wk, positions, *out, stream)
     return tuple(out)
@@ -665,8 +668,8 @@ def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions
     where, stream = _on(q.device, stream)
     with where:
         if into is None:
-            into = [None if t is None else torch.empty((w.batch, w.seqlen, h, w.head_dim), dtype=torch.bfloat16,
-                                                       device=q.device) for t, h in ((dq, w.hq), (dk, w.hkv), (dv, w.hkv))]
+            into = [None if t is None else q.new_empty((w.batch, w.seqlen, h, w.head_dim))
+                    for t, h in ((dq, w.hq), (dk, w.hkv), (dv, w.hkv))]
         o = opts._struct_of(_token_strides(("q", "k", "v"), (q, k, None), w, q.device),
                             _token_strides(("into[0]", "into[1]", "into[2]"), into, w, q.device), pos_begin)
         dwq = None if wq is None or not opts.norm else torch.empty_like(wq)
