@@ -68,9 +68,9 @@ struct FwdCfg {
   static constexpr int NBARS = 1 + 4 * NS + 3 + 3 + 2 + 2;
   // Bias: what the producer knows about the last NINFO key tiles.  Entry j is
   // rewritten for tile j + NINFO once K(j + NINFO - NS) has been read, which is
-  // after the softmax of tiles up to j + NINFO - NS - 2.
+  // after the softmax of tiles up to j + NINFO - NS - 2 (one slot: - NSB).
   static constexpr int NINFO = 8;
-  static_assert(NINFO >= NS + 2, "a tile's entry is read before it is rewritten");
+  static_assert(NINFO >= NS + NSB && NSB >= 2, "a tile's entry is read before it is rewritten");
   static constexpr int SMEM_BYTES = (NQ + 2 * NS) * TILE_BYTES + NBARS * 8 + 1024;
   static constexpr int THREADS = 320;
   // Bias: a third whole warpgroup (two of its warps idle), whose registers go to
@@ -148,7 +148,11 @@ struct FwdPiece {
   int step;      // kPieceStep: row r of the piece has passed the boundary up to column r + step
 };
 
-template <int D, bool STEP, bool BIAS>
+//
+// SLOTS = 1 (with BIAS): one head's query tile per block, where even such blocks do
+// not fill the SMs.  The second slot's warps idle; the scores of the next tiles, in
+// the other buffers, are computed while the softmax works.
+template <int D, bool STEP, bool BIAS, int SLOTS = 2>
 __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::THREADS, 1)
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
@@ -192,7 +196,12 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   const int nqt = nr * rank_parts(g) * g.ntile;
   int hpair, r;
   bool tile_pair = false;
-  if constexpr (BIAS) {  // first the pairs of tiles of an odd group's last head, then the pairs of heads
+  if constexpr (SLOTS == 1) {
+    hpair = idx % a.G;  // the head
+    idx /= a.G;
+    r = idx % nqt;
+    idx /= nqt;
+  } else if constexpr (BIAS) {  // first the pairs of tiles of an odd group's last head, then the pairs of heads
     const int npt = (a.G & 1) ? nr * rank_parts(g) * ((g.ntile + 1) / 2) : 0;
     const int npairs = a.G / 2;
     int item = idx % (npt + nqt * npairs);
@@ -217,10 +226,10 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   // the slots' query tiles; the walk follows the later one
   const int qi0 = tile_pair ? 2 * (per_block - 1 - from_last) : g.ntile - 1 - from_last;
   const int qi = tile_pair ? min(qi0 + 1, g.ntile - 1) : qi0;
-  const int head0 = kvh * a.G + (tile_pair ? a.G - 1 : 2 * hpair);
+  const int head0 = kvh * a.G + (tile_pair ? a.G - 1 : SLOTS * hpair);
   // slot 1 repeats slot 0: an odd group without bias, a last tile without a neighbour
   const bool dup = BIAS ? tile_pair && qi == qi0 : head0 + 1 >= (kvh + 1) * a.G;
-  const int head1 = dup || tile_pair ? head0 : head0 + 1;
+  const int head1 = SLOTS == 1 || dup || tile_pair ? head0 : head0 + 1;
   const int q0 = bq * g.blk + qi0 * kTile;   // slot 0's first row, slot 1's
   const int q1 = bq * g.blk + qi * kTile;
   const int qlen = min(kTile, (bq + 1) * g.blk - q0);  // slot 0's rows; without BIAS slot 1's too
@@ -276,8 +285,8 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       const bool leader = lane == 0;
       auto all = [&](bool x) { return BIAS ? __all_sync(0xffffffffu, x) != 0 : x; };
       if (leader) {
-        mbar_expect_tx(q_full, C::NQ * C::TILE_BYTES);
-        for (int h = 0; h < C::NQ; ++h) {
+        mbar_expect_tx(q_full, SLOTS * C::TILE_BYTES);
+        for (int h = 0; h < SLOTS; ++h) {
           int hc;
           const int64_t qr64 = a.lay.view_row(b, h ? q1 : q0, h ? head1 : head0, a.hq, hc);
           // checked build: the tile starts inside the tensor (TMA fills rows past its end with zeros)
@@ -385,29 +394,29 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         for (int kk = 0; kk < kTile / 16; ++kk)
           mma_ts_w(tbase + C::O_COL(h), tbase + C::S_COL(buf) + kk * 8, vb + (kk * 2048 >> 4), id_pv, acc || kk > 0);
       };
-      // Q K^T of job J = 2 jt + h into buffer J mod NSB; K(jt) is released
-      // after its second head
+      // Q K^T of job J = SLOTS jt + h into buffer J mod NSB; K(jt) is released
+      // after its last head
       auto issue_qk = [&](int J) {
-        const int jt = J >> 1, h = J & 1, st = jt % C::NS;
+        const int jt = J / SLOTS, h = J % SLOTS, st = jt % C::NS;
         if (h == 0) {
           if (!warp_wait(&k_full[st], (jt / C::NS) & 1, abort_flag, a.err)) return false;
           tc_fence_after();
         }
         qk(h, st, J % C::NSB);
         mma_commit_w(&s_full[J % C::NSB]);
-        if (h == 1) mma_commit_w(&k_empty[st]);
+        if (h == SLOTS - 1) mma_commit_w(&k_empty[st]);
         return true;
       };
       bool ok = warp_wait(q_full, 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
-        for (int J = 0; J < C::NSB && J < 2 * n && ok; ++J) ok = issue_qk(J);
+        for (int J = 0; J < C::NSB && J < SLOTS * n && ok; ++J) ok = issue_qk(J);
         for (int j = 0; j < n && ok; ++j) {
           const int s = j % C::NS;
           if (!warp_wait(&v_full[s], (j / C::NS) & 1, abort_flag, a.err)) break;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int J = 2 * j + h;
+          for (int h = 0; h < SLOTS; ++h) {
+            const int J = SLOTS * j + h;
             if (!warp_wait(&p_full[J % C::NSB], (J / C::NSB) & 1, abort_flag, a.err)) {
               ok = false;
               break;
@@ -415,8 +424,8 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
             tc_fence_after();
             pv(h, s, J % C::NSB, j > 0);
             mma_commit_w(&pv_done[h]);
-            if (h == 1) mma_commit_w(&v_empty[s]);
-            if (J + C::NSB < 2 * n && !issue_qk(J + C::NSB)) {
+            if (h == SLOTS - 1) mma_commit_w(&v_empty[s]);
+            if (J + C::NSB < SLOTS * n && !issue_qk(J + C::NSB)) {
               ok = false;
               break;
             }
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       mma_commit_w(drain);
       mbar_drain(drain, 0, a.err);
     }
-  } else if (!BIAS || warp < 8) {
+  } else if (!BIAS || warp < 4 * SLOTS) {
     if constexpr (BIAS) regs_inc<C::SOFTMAX_REGS>();
     // ------------------------------------------------------------ softmax
     const int h = warp >> 2;
@@ -442,7 +451,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
     bool ok = true;
     for (int j = 0; j < n; ++j, walk.advance()) {
       // Lanes leave together so the .sync.aligned TMEM accesses never diverge.
-      const int J = 2 * j + h;  // this tile's MMA job and its score buffer
+      const int J = SLOTS * j + h;  // this tile's MMA job and its score buffer
       const uint32_t tS = tbase + t_lane + C::S_COL(J % C::NSB);
       // BIAS: the tile's constant (log2 units), whether a boundary crosses it, and
       // which of this warp's pieces then add something
@@ -580,9 +589,10 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         // the whole warp takes the branch, rows that need none scale by 1.
         if (__any_sync(0xffffffffu, rescale)) {
           // O_h must hold the previous tile's P V: with two buffers the commit
-          // that signalled these scores follows it; with three, wait for it
-          // (completion j - 1 of pv_done[h]; completion j needs this tile's P)
-          if (C::NSB > 2 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[h], (j - 1) & 1, abort_flag, a.err))) {
+          // that signalled these scores follows it; with three (one slot: two),
+          // wait for it (completion j - 1 of pv_done[h]; completion j needs this
+          // tile's P)
+          if (C::NSB > SLOTS && !__all_sync(0xffffffffu, mbar_wait(&pv_done[h], (j - 1) & 1, abort_flag, a.err))) {
             ok = false;
             break;
           }
@@ -717,7 +727,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   }
 }
 
-template <int D, bool STEP, bool BIAS>
+template <int D, bool STEP, bool BIAS, int SLOTS = 2>
 int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o,
                  float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end,
                  const BiasView* bias) {
@@ -756,7 +766,7 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
 
-  auto kern = ring_fwd_kernel<D, STEP, BIAS>;
+  auto kern = ring_fwd_kernel<D, STEP, BIAS, SLOTS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   constexpr int threads = BIAS ? C::BIAS_THREADS : C::THREADS;
@@ -767,8 +777,9 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
     if (at.numRegs < C::BIAS_REGS) return LOONG_ERR_UNSUPPORTED;
   }
   const int64_t blocks = static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring);
-  const int64_t per_kvh = BIAS ? blocks * (a.ring.ntile * (a.G / 2) + (a.G & 1) * ((a.ring.ntile + 1) / 2))
-                               : blocks * a.ring.ntile * a.npairs;
+  const int64_t per_kvh = SLOTS == 1 ? blocks * a.ring.ntile * a.G
+                          : BIAS     ? blocks * (a.ring.ntile * (a.G / 2) + (a.G & 1) * ((a.ring.ntile + 1) / 2))
+                                     : blocks * a.ring.ntile * a.npairs;
   const int64_t grid = d.batch * d.hkv * per_kvh;
   if (grid <= 0 || grid > 0x7fffffff) return LOONG_ERR_INVALID_ARG;
   if (!STEP) {
@@ -815,10 +826,26 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   return LOONG_OK;
 }
 
+// With a bias, blocks of one slot where that many find an SM each: a block takes two
+// thirds of a two-slot block's time, so they pay in one round only.  One and two slots,
+// 4K tokens of 4 heads of 128 (128 and 64 blocks) 44.5 and 67.5 us, 2K of 8 + 2 heads of
+// 64 26.9 and 34, 512 of 4 of 128 18.5 and 25.5; 16 heads twice 4K (1,024 and 512 blocks)
+// would take seven rounds for four.
+constexpr int64_t kOneSlotBlocks = 152;
+
 template <bool BIAS>
 int launch_fwd_b(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
                  cudaStream_t stream, int rank_begin, int rank_end, const BiasView* bias) {
   const bool step = d.mode != LOONG_MODE_FUSED;
+  if constexpr (BIAS) {
+    const RingGeom g = ring_geom(d);
+    if (!step && d.batch * d.hq * g.nblocks * g.ntile <= kOneSlotBlocks) {
+      if (d.head_dim == 128)
+        return launch_fwd_t<128, false, true, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+      if (d.head_dim == 64)
+        return launch_fwd_t<64, false, true, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+    }
+  }
   if (d.head_dim == 128)
     return step ? launch_fwd_t<128, true, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
                 : launch_fwd_t<128, false, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);

@@ -145,6 +145,24 @@ def test_matches_oracle(cuda_device, name):
     assert torch.equal(_run(w, x, t, buckets)[5].view(torch.int16), out[5].view(torch.int16))
 
 
+@pytest.mark.parametrize("name", list(CASES))
+def test_many_sequences(cuda_device, name):
+    """Copies of a case's sequences, more than one block per SM: the blocks then hold two heads (or two query tiles of
+    one) where the few of the case alone hold one.  A row's arithmetic is the same: the same bits, but dQ's adds, and
+    the table's gradient the copies' sum (each rounded to bf16 once, 2^-8 of it)."""
+    w, x, t, buckets = _make(name)
+    one = _run(w, x, t, buckets)
+    copies = 160 // w.hq + 1
+    many = w.with_(batch=w.batch * copies)
+    out = _run(many, {n: v.repeat(copies, 1, 1, 1) for n, v in x.items()}, t, buckets)
+    for i in (0, 1, 3, 4):
+        a, b = out[i].unflatten(0, (copies, w.batch)), one[i]
+        assert all(torch.equal(c, b) for c in a), i
+    a = out[2].unflatten(0, (copies, w.batch))
+    assert (a.float() - one[2].float()).abs().max() <= 2.0 ** -7 * one[2].float().abs().max()
+    assert torch.all((out[5].float() - copies * one[5].float()).abs() <= 2.0 ** -7 * copies * one[5].float().abs() + 2.0 ** -14 * copies)
+
+
 @pytest.mark.parametrize("name", ["gqa", "ragged-blocks", "not-causal", "not-causal-d128", "empty-rows-ring", "window",
                                   "one-head-groups-even", "groups-of-five"])
 def test_stepwise_matches_oracle(cuda_device, name):
