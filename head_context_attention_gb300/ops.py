@@ -608,7 +608,10 @@ def make_qk_opts(head_dim, **kw):
 
 def _token_strides(names, ts, w, device):
     """Elements from token to token of projections: [B, S, heads, d] views whose
-    heads are contiguous and whose sequences follow each other; 0 for None."""
+    heads are contiguous and whose sequences follow each other; 0 for None.  An
+    expanded view repeats one token's memory: its stride of 0 is not the
+    library's 0 (contiguous), and neither it nor one below a token's elements is
+    taken."""
     b, s, d = w.batch, w.seqlen, w.head_dim
     out = []
     for name, t, heads in zip(names, ts, (w.hq, w.hkv, w.hkv)):
@@ -619,7 +622,7 @@ def _token_strides(names, ts, w, device):
         sb, ss, sh, sd = t.stride()
         if s == 1:  # the token's stride is the sequence's
             ss = sb if b > 1 else heads * d
-        if sd != 1 or (sh != d and heads > 1) or (b > 1 and sb != s * ss):
+        if sd != 1 or (sh != d and heads > 1) or (b > 1 and sb != s * ss) or ss < heads * d:
             raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, not strides {t.stride()}")
         out.append(ss)
     return out

@@ -88,3 +88,45 @@ def test_tensor_calls_refuse_wrong_tensors(loong_lib):
         ops.qk_norm_rope_bwd(W, opts, x["q"], x["k"], x["q"], x["k"], x["v"], into=(x["q"], x["k"], None))
     with pytest.raises(ValueError):
         ops.qk_norm_rope_bwd(W, opts, x["q"], x["k"], x["q"], x["k"][:, 1:], x["v"])
+
+
+# batch, tokens of the view that is expanded to it
+@pytest.mark.parametrize("batch,seqlen,b,s", [(1, 64, 1, 1), (2, 64, 1, 1), (8, 1, 1, 1), (2, 64, 1, 64)])
+def test_expanded_projections_refused(loong_lib, batch, seqlen, b, s):
+    """One token's (or one sequence's) memory repeated over a shape: the call
+    would read, and through ``into`` write, as if every token had its own."""
+    w = inputs.small(seqlen, 4, 2, 64, placement=0).with_(batch=batch)
+    full = lambda h: torch.zeros((batch, seqlen, h, 64), dtype=torch.bfloat16)
+    repeated = lambda h: torch.zeros((b, s, h, 64), dtype=torch.bfloat16).expand(batch, seqlen, h, 64)
+    good, opts = [full(4), full(2), full(2)], ops.make_qk_opts(64)
+    for i, heads in enumerate((4, 2, 2)):
+        bad = list(good)
+        bad[i] = repeated(heads)
+        with pytest.raises(ValueError, match="evenly spaced tokens"):
+            ops._token_strides("qkv", bad, w, bad[0].device)
+        with pytest.raises(ValueError, match="evenly spaced tokens"):
+            ops.qk_norm_rope(w, opts, *bad)
+    assert ops._token_strides("qkv", good, w, good[0].device) == [256, 128, 128]
+
+
+def test_overlapping_tokens_refused(loong_lib):
+    """A token's stride below its own elements."""
+    w = inputs.small(64, 4, 2, 64, placement=0)
+    q = torch.zeros(65 * 256, dtype=torch.bfloat16).as_strided((1, 64, 4, 64), (0, 248, 64, 1))
+    with pytest.raises(ValueError, match="evenly spaced tokens"):
+        ops._token_strides("q", [q], w, q.device)
+
+
+def test_expanded_gradients_refused(loong_lib, monkeypatch):
+    """The same for the projections' gradients, which the call writes."""
+    w = inputs.small(64, 4, 2, 64, placement=0)
+    full = [torch.zeros((1, 64, h, 64), dtype=torch.bfloat16) for h in (4, 2, 2)]
+    monkeypatch.setattr(ops, "_on", lambda device, stream: (ops._NOTHING, 0))    # past the device's check
+    launched = []
+    monkeypatch.setattr(ops, "loong_qk_norm_rope_bwd", lambda *a: launched.append(a))
+    for i in range(3):
+        into = list(full)
+        into[i] = full[i][:, :1].expand(1, 64, -1, 64)
+        with pytest.raises(ValueError, match="evenly spaced tokens"):
+            ops.qk_norm_rope_bwd(w, ops.make_qk_opts(64), *full[:2], *full, into=into)
+    assert not launched
