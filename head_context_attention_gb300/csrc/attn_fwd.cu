@@ -50,6 +50,7 @@
 #include <cmath>
 
 #include "exchange.h"
+#include "fwd_jobs.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -64,7 +65,7 @@ struct FwdCfg {
   static constexpr int ATOMS = D / 64;             // 128-byte swizzle atoms per row
   static constexpr int ATOM_BYTES = kTile * 128;   // one atom column of a tile
   static constexpr int TILE_BYTES = kTile * D * 2;
-  static constexpr int NSB = D == 64 ? 3 : 2;      // score buffers in tensor memory
+  static constexpr int NSB = fwd_max_score_buffers(D);  // score buffers with room in tensor memory
   static constexpr int NBARS = 1 + 4 * NS + 3 + 3 + 2 + 2;
   // Bias: what the producer knows about the last NINFO key tiles.  Entry j is
   // rewritten for tile j + NINFO once K(j + NINFO - NS) has been read, which is
@@ -150,13 +151,15 @@ struct FwdPiece {
 
 //
 // SLOTS = 1 (with BIAS): one head's query tile per block, where even such blocks do
-// not fill the SMs.  The second slot's warps idle; the scores of the next tiles, in
-// the other buffers, are computed while the softmax works.
+// not fill the SMs.  The second slot's warps idle; the scores of the next tile, in
+// the other buffer, are computed while the softmax works.
 template <int D, bool STEP, bool BIAS, int SLOTS = 2>
 __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::THREADS, 1)
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
   using C = FwdCfg<D>;
+  constexpr int NSB = fwd_score_buffers(D, SLOTS);
+  static_assert(NSB <= 2 * SLOTS, "a tile's scores prove P V of the tile two back");
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int sb = 0; sb < C::NSB; ++sb) {
+    for (int sb = 0; sb < NSB; ++sb) {
       mbar_init(&s_full[sb], 1);
       mbar_init(&p_full[sb], 4);
     }
@@ -402,30 +405,30 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
           if (!warp_wait(&k_full[st], (jt / C::NS) & 1, abort_flag, a.err)) return false;
           tc_fence_after();
         }
-        qk(h, st, J % C::NSB);
-        mma_commit_w(&s_full[J % C::NSB]);
+        qk(h, st, J % NSB);
+        mma_commit_w(&s_full[J % NSB]);
         if (h == SLOTS - 1) mma_commit_w(&k_empty[st]);
         return true;
       };
       bool ok = warp_wait(q_full, 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
-        for (int J = 0; J < C::NSB && J < SLOTS * n && ok; ++J) ok = issue_qk(J);
+        for (int J = 0; J < NSB && J < SLOTS * n && ok; ++J) ok = issue_qk(J);
         for (int j = 0; j < n && ok; ++j) {
           const int s = j % C::NS;
           if (!warp_wait(&v_full[s], (j / C::NS) & 1, abort_flag, a.err)) break;
 #pragma unroll
           for (int h = 0; h < SLOTS; ++h) {
             const int J = SLOTS * j + h;
-            if (!warp_wait(&p_full[J % C::NSB], (J / C::NSB) & 1, abort_flag, a.err)) {
+            if (!warp_wait(&p_full[J % NSB], (J / NSB) & 1, abort_flag, a.err)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            pv(h, s, J % C::NSB, j > 0);
+            pv(h, s, J % NSB, j > 0);
             mma_commit_w(&pv_done[h]);
             if (h == SLOTS - 1) mma_commit_w(&v_empty[s]);
-            if (J + C::NSB < SLOTS * n && !issue_qk(J + C::NSB)) {
+            if (J + NSB < SLOTS * n && !issue_qk(J + NSB)) {
               ok = false;
               break;
             }
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
     for (int j = 0; j < n; ++j, walk.advance()) {
       // Lanes leave together so the .sync.aligned TMEM accesses never diverge.
       const int J = SLOTS * j + h;  // this tile's MMA job and its score buffer
-      const uint32_t tS = tbase + t_lane + C::S_COL(J % C::NSB);
+      const uint32_t tS = tbase + t_lane + C::S_COL(J % NSB);
       // BIAS: the tile's constant (log2 units), whether a boundary crosses it, and
       // which of this warp's pieces then add something
       const int e = j % C::NINFO;
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
           }
         }
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[J % C::NSB], (J / C::NSB) & 1, abort_flag, a.err))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[J % NSB], (J / NSB) & 1, abort_flag, a.err))) {
         ok = false;
         break;
       }
@@ -590,9 +593,9 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         if (__any_sync(0xffffffffu, rescale)) {
           // O_h must hold the previous tile's P V: with two buffers the commit
           // that signalled these scores follows it; with three (one slot: two),
-          // wait for it (completion j - 1 of pv_done[h]; completion j needs this
-          // tile's P)
-          if (C::NSB > SLOTS && !__all_sync(0xffffffffu, mbar_wait(&pv_done[h], (j - 1) & 1, abort_flag, a.err))) {
+          // wait for it (completion j - 1 of pv_done[h]; completion j - 2 is in
+          // these scores' past, completion j needs this tile's P)
+          if (NSB > SLOTS && !__all_sync(0xffffffffu, mbar_wait(&pv_done[h], (j - 1) & 1, abort_flag, a.err))) {
             ok = false;
             break;
           }
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[J % C::NSB]);
+      if (lane == 0) mbar_arrive(&p_full[J % NSB]);
     }
     // ---------------------------------------------------------- epilogue
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_final, 0, abort_flag, a.err));

@@ -1,0 +1,26 @@
+// fwd_jobs.h -- the forward kernel's score buffers: how many, by what the order
+// of its matrix instructions lets the softmax conclude.
+//
+// Job J = slots * j + h is key tile j of query slot h.  The MMA warp issues Q K^T
+// of the first jobs, one per buffer, then P V of job J and Q K^T of job
+// J + buffers in turn; they execute in that order.  Scores of job J therefore
+// show that P V of jobs up to J - buffers is done, and no more.  A softmax that
+// rescales O_h waits for P V of its previous tile, job J - slots, on a barrier
+// with one phase per tile of the slot.  A wait tells a phase from the one before
+// by one bit, so the phase before (job J - 2 slots) has to be known as done, or
+// the wait passes while both are under way and O_h is read, scaled and stored
+// under them: J - buffers >= J - 2 slots.
+#pragma once
+
+namespace loong {
+
+// What tensor memory has room for: two slots' O and this many buffers of 128
+// columns in 512.
+constexpr int fwd_max_score_buffers(int head_dim) { return head_dim == 64 ? 3 : 2; }
+
+constexpr int fwd_score_buffers(int head_dim, int slots) {
+  const int room = fwd_max_score_buffers(head_dim);
+  return room < 2 * slots ? room : 2 * slots;
+}
+
+}  // namespace loong

@@ -428,3 +428,30 @@ def test_two_calls_at_once(cuda_device):
                     assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
                 else:
                     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,hq,hkv,copies", [(64, 2, 1, 1), (64, 3, 3, 1), (128, 2, 1, 1), (64, 3, 3, 20)])
+def test_maxima_rise_on_every_tile(cuda_device, d, hq, hkv, copies, causal):
+    """Keys whose scores rise by 8 from tile to tile, 11.5 in log2 units: every tile after the first rescales every
+    row's accumulator, with one query tile per block (the few blocks) and with two (the copies).  The logits reach
+    64, within what the tolerances count."""
+    w = inputs.Workload("rise", 1100, hq, hkv, d, 1, 1, 1, 1, True, placement=0, causal=causal, batch=copies)
+    x = inputs.make_inputs(w.with_(batch=1), device="cuda")
+    x["q"][..., 0] = d ** 0.5
+    x["k"][..., 0] = (8 * (torch.arange(1100, device="cuda") // 128)).to(torch.bfloat16)[None, :, None]
+    x["q"][..., 1:] /= 8
+    buckets = ops.log_buckets(16, 600, causal=causal)
+    t = torch.randn((16, hq), generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").to(torch.bfloat16)
+    out = _run(w, {n: v.repeat(copies, 1, 1, 1) for n, v in x.items()}, t, buckets)
+    r = obias.forward_backward(to64(x["q"][0]), to64(x["k"][0]), to64(x["v"][0]), to64(x["do"][0]), to64(t),
+                               buckets.bounds, buckets.bucket_of, ops.default_scale(d), causal, terms=True)
+    e = _e(w, r)
+    f = 2.0 ** -8 + 2.0 ** -11 + 2 * e + 2.0 ** -14
+    for b in range(copies):
+        _within("O", out[0][b], r["o"], 2.0 ** -8 * np.abs(r["o"]) + (2.0 ** -11 + e + 2.0 ** -16) * r["abs_o"])
+        _within("LSE", out[1][b], r["lse"], e + 2.0 ** -22 * np.abs(r["lse"]))
+        for nm, got in (("dq", out[2]), ("dk", out[3]), ("dv", out[4])):
+            _within(nm, got[b], r[nm], 2.0 ** -8 * np.abs(r[nm]) + f * r["abs_" + nm])
+    _within("dtable", out[5], copies * r["dtable"], copies * ((2.0 ** -11 + 2 * e + 2.0 ** -14) * r["abs_dtable"]
+                                                               + 2.0 ** -8 * np.abs(r["dtable"])))
