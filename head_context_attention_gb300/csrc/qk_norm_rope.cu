@@ -45,6 +45,7 @@ struct HeadTensor {
   const float* w;            // [D] or null (ones)
   int64_t x_stride;          // elements per token of x
   int64_t dx_stride;         // backward: elements per token of out
+  int64_t x_elems, dx_elems;  // checked build: elements from the first token's to the last one's end
   int64_t plane;             // attention side, elements of one (ring rank, head rank) plane
   int heads, hpr;            // heads, heads per head rank (heads when natural)
   int slots;                 // ceil(heads / heads per warp)
@@ -297,7 +298,8 @@ __device__ __forceinline__ Vec8 load_w(const float* w, float w_offset, int e) {
 }
 
 // 16 bytes from global to shared memory, asynchronously; `live` false writes
-// zeros and reads nothing.
+// zeros and reads nothing, from an address that has to lie in memory of the
+// call all the same.
 __device__ __forceinline__ void copy16(void* dst, const __nv_bfloat16* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
                : "memory");
@@ -307,6 +309,12 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Checked build: what a lane copies from tensor ti's projection, 8 elements from
+// p, lies in it; a lane past the last head names Q's first.
+__device__ __forceinline__ bool in_projection(const QkArgs& a, int ti, const __nv_bfloat16* p) {
+  return in_bounds(p == a.t[0].x || (p >= a.t[ti].x && p + 8 <= a.t[ti].x + a.t[ti].x_elems), a.err);
 }
 
 // A warp's items are tokens (or ranges of a token's slots: Q's, then K's, then
@@ -400,8 +408,11 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) qk_fwd_kernel(const __gr
         if (ahead.new_tensor) src = a.t[ahead.ti].x + ahead.tok * a.t[ahead.ti].x_stride + ahead.h * D + ln.li * 8;
         ahead.new_tensor = false;
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-          copy16(ring + (stage * U + k) * 32, src + k * HPW * D, ahead.h + k * HPW < ahead.h1);
+        for (int k = 0; k < U; ++k) {
+          const bool live = ahead.h + k * HPW < ahead.h1;
+          const __nv_bfloat16* from = live ? src + k * HPW * D : a.t[0].x;
+          if (in_projection(a, ahead.ti, from)) copy16(ring + (stage * U + k) * 32, from, live);
+        }
         src += U * HPW * D;
         ahead.h += U * HPW;
         ahead.left -= U;
@@ -514,8 +525,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_bwd_kernel(const __gr
         for (int k = 0; k < U; ++k) {
           const bool live = ahead.h < ahead.h1;
           const bool ok = live && in_bounds(in.at >= 0 && in.at + 8 <= a.out_elems[ahead.ti], a.err);
-          copy16(ring + (stage * 2 * U + k) * 32, t.dy + in.at, ok);
-          if (NORM && ahead.ti < 2) copy16(ring + ((stage * 2 + 1) * U + k) * 32, src + k * HPW * D, live);
+          copy16(ring + (stage * 2 * U + k) * 32, ok ? t.dy + in.at : a.t[0].dy, ok);
+          if (NORM && ahead.ti < 2) {
+            const __nv_bfloat16* from = live ? src + k * HPW * D : a.t[0].x;
+            if (in_projection(a, ahead.ti, from)) copy16(ring + ((stage * 2 + 1) * U + k) * 32, from, live);
+          }
           ahead.h += HPW;
           in.next<D>();
         }
@@ -584,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_bwd_kernel(const __gr
             }
             y = pack8(g);
           }
-          if (h < h1) __stcs(reinterpret_cast<uint4*>(dst), y);
+          if (h < h1 && in_bounds(dst >= t.out && dst + 8 <= t.out + t.dx_elems, a.err))
+            __stcs(reinterpret_cast<uint4*>(dst), y);
           h += HPW;
           dst += HPW * D;
         }
@@ -703,6 +718,8 @@ void fill_args(QkArgs& a, const loong_attn_desc& d, const loong_qk_opts& o, cons
     t.hpr = heads[i] / a.P;
     t.x_stride = x_stride[i] ? x_stride[i] : row;
     t.dx_stride = dx_stride[i] ? dx_stride[i] : row;
+    t.x_elems = (a.tokens - int64_t{1}) * t.x_stride + row;
+    t.dx_elems = (a.tokens - int64_t{1}) * t.dx_stride + row;
     t.plane = a.s_rank * t.hpr * d.head_dim;
     t.slots = i == 2 && !with_v ? 0 : (heads[i] + hpw - 1) / hpw;
     a.out_elems[i] = static_cast<int64_t>(a.tokens) * row;

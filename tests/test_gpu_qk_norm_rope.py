@@ -294,3 +294,15 @@ def test_checked_build(cuda_device, monkeypatch, name):
     ops.qk_norm_rope(c["w"], c["opts"], c["q"], c["k"], c["v"], **_place(c))
     ops.qk_norm_rope_bwd(c["w"], c["opts"], c["q"], c["k"], *[_lay(c, g) for g in c["grads"]], **_place(c))
     assert ops.loong_get_device_status() == ops.LOONG_OK
+
+
+@pytest.mark.parametrize("name", ["odd-heads-d64", "part-48-inter", "many-heads", "no-norm", "one-token", "two-tokens"])
+def test_checked_build_of_heads_that_do_not_fill_a_warp(cuda_device, monkeypatch, name):
+    """Every address a lane copies from or stores to lies in its tensor, those of lanes past the last head too."""
+    monkeypatch.setattr(ops, "LIB_PATH", ops.CHECKED_LIB_PATH)
+    monkeypatch.setattr(ops, "_lib", None)
+    c = _make(name)
+    got = ops.qk_norm_rope(c["w"], c["opts"], c["q"], c["k"], c["v"], **_place(c))
+    ops.qk_norm_rope_bwd(c["w"], c["opts"], c["q"], c["k"], *[_lay(c, g) for g in c["grads"]], **_place(c))
+    assert ops.loong_get_device_status() == ops.LOONG_OK
+    assert torch.equal(got[2].view(torch.int16), _lay(c, c["v"]).view(torch.int16))
