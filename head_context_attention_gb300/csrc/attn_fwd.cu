@@ -309,6 +309,13 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
         if constexpr (BIAS) {
           if (lane < 16) {
             const int diag = lane & 7;
+            // a tile wholly ahead of slot 0's queries (a pair's first tile) takes no bias: its
+            // scores are masked, and its buckets may hold anything where no pair meets them
+            if (SLOTS == 2 && lane == 7 && g.causal && walk.bk == bq && walk.kt > qi0) {
+              code = PieceCode::make(kPieceConst, 0, 0);
+              piece.lo = piece.hi = 0.f;
+              return;
+            }
             // the middle distance
             const int64_t i0 = a.bias.off + (lane < 8 ? q0 : q1) - walk.k0() + (diag < 7 ? 32 * (diag - 3) : 0);
             // independent loads, waited for in the next trip

@@ -344,7 +344,9 @@ LOONG_API int loong_headctx_pack_n(int32_t n, int64_t batch, int32_t cp, int32_t
  *                key gets O = 0 and LSE = -inf, and adds nothing to any
  *                gradient.  Masked keys are still read and multiplied.  2^20 or
  *                more counts as +inf: like NaN, it makes the outputs NaN that
- *                it enters.  A bucket that no pair falls in is never used.
+ *                it enters.  A bucket that no pair falls in adds to nothing, what
+ *                ever it holds (a finite value there may decide how a logit next
+ *                to it rounds).
  * The two host arrays are read during the call only.
  */
 typedef struct {

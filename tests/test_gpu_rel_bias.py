@@ -455,3 +455,26 @@ def test_maxima_rise_on_every_tile(cuda_device, d, hq, hkv, copies, causal):
             _within(nm, got[b], r[nm], 2.0 ** -8 * np.abs(r[nm]) + f * r["abs_" + nm])
     _within("dtable", out[5], copies * r["dtable"], copies * ((2.0 ** -11 + 2 * e + 2.0 ** -14) * r["abs_dtable"]
                                                                + 2.0 ** -8 * np.abs(r["dtable"])))
+
+
+@pytest.mark.parametrize("mode", [ops.MODE_FUSED, ops.MODE_STEPWISE, ops.MODE_STEPWISE_COPY])
+@pytest.mark.parametrize("d,hq,hkv,batch", [(64, 3, 1, 1), (64, 1, 1, 160), (128, 3, 1, 40), (128, 2, 2, 80)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 2.0 ** 20, -float("inf")])
+def test_a_whole_tile_ahead_of_its_queries(cuda_device, value, d, hq, hkv, batch, mode):
+    """The last head of an odd group pairs two of its query tiles, the first of which meets a key tile that lies
+    ahead of all its queries, one interval for the whole of it: what stands there changes no bit."""
+    w = inputs.Workload("ahead", 1068, hq, hkv, d, 1, 3, 3, 1, True, placement=0, batch=batch)
+    x, buckets = inputs.make_inputs(w, device="cuda"), ops.RelBuckets(4, [0, 33, 300])
+    t = torch.randn((4, hq), generator=torch.Generator(device="cuda").manual_seed(9), device="cuda").to(torch.bfloat16)
+    lay = ops.LAYOUT_NATURAL
+    if mode == ops.MODE_STEPWISE_COPY:
+        x, lay = _pack(w, x), ops.LAYOUT_RANK_MAJOR
+    t[0] = 0
+    want = _run(w, x, t, buckets, mode=mode, layout=lay)
+    t[0] = value
+    got = _run(w, x, t, buckets, mode=mode, layout=lay)
+    # in the stepwise modes dK and dV are summed by adds as well
+    for i in (0, 1, 5) if mode != ops.MODE_FUSED else (0, 1, 3, 4, 5):
+        assert torch.equal(got[i], want[i]), i
+    for i in (2, 3, 4):
+        assert (got[i].float() - want[i].float()).abs().max() <= 2.0 ** -7 * want[i].float().abs().max()
