@@ -500,7 +500,8 @@ _NOTHING = contextlib.nullcontext()
 
 def _on(device, stream):
     """The calls below run on the tensors' device, on its current stream unless
-    one is given: (what to enter, the stream).  Nothing to enter where both are
+    one is given, a torch stream or a number: (what to enter, the stream).  What
+    a call allocates belongs to that stream.  Nothing to enter where both are
     current already."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not {device}")
@@ -508,6 +509,8 @@ def _on(device, stream):
         return _NOTHING, _current_raw_stream(device.index)
     where = contextlib.ExitStack()
     where.enter_context(torch.cuda.device(device))
+    if type(stream) is int:  # 1 is the legacy default stream, as 0 is
+        stream = torch.cuda.ExternalStream(0 if stream == 1 else stream, device=device)
     stream = torch.cuda.current_stream(device) if stream is None else stream
     where.enter_context(torch.cuda.stream(stream))
     return where, stream

@@ -306,3 +306,27 @@ def test_checked_build_of_heads_that_do_not_fill_a_warp(cuda_device, monkeypatch
     ops.qk_norm_rope_bwd(c["w"], c["opts"], c["q"], c["k"], *[_lay(c, g) for g in c["grads"]], **_place(c))
     assert ops.loong_get_device_status() == ops.LOONG_OK
     assert torch.equal(got[2].view(torch.int16), _lay(c, c["v"]).view(torch.int16))
+
+
+def test_stream_as_a_number(cuda_device):
+    """The calls take a cudaStream_t as a number too, as loong_attn_fwd does: a stream's, 0 and 1 (the legacy
+    default stream)."""
+    from head_context_attention_gb300.ops import attn_bias_bwd, attn_bias_fwd, log_buckets
+    c = _make("ranks-zigzag")
+    dy = [_lay(c, g) for g in c["grads"]]
+    buckets, t = log_buckets(8, 40), torch.randn((8, 8), device="cuda").to(torch.bfloat16)
+
+    def run(stream):
+        q, k, v = ops.qk_norm_rope(c["w"], c["opts"], c["q"], c["k"], c["v"], stream=stream, **_place(c))
+        o, lse, res = attn_bias_fwd(c["w"], q, k, v, t, buckets, layout=c["layout"], stream=stream)
+        _, dk, dv, dt = attn_bias_bwd(c["w"], q, k, v, o, lse, o, t, buckets, o_res=res, layout=c["layout"],
+                                      stream=stream)
+        return (q, k, v, o, lse, dk, dv, dt) + ops.qk_norm_rope_bwd(c["w"], c["opts"], c["q"], c["k"], *dy,
+                                                                    stream=stream, **_place(c))
+    want = run(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for number in (side.cuda_stream, 0, 1):
+        got = run(number)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), number

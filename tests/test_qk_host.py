@@ -130,3 +130,23 @@ def test_expanded_gradients_refused(loong_lib, monkeypatch):
         with pytest.raises(ValueError, match="evenly spaced tokens"):
             ops.qk_norm_rope_bwd(w, ops.make_qk_opts(64), *full[:2], *full, into=into)
     assert not launched
+
+
+def test_stream_numbers(monkeypatch):
+    """A number stands for the stream of that handle, on the tensors' device."""
+    import contextlib
+    entered = []
+
+    class Stream:
+        def __init__(self, handle, device):
+            self.cuda_stream, self.device = handle, device
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s) or contextlib.nullcontext(s.device))
+    device = torch.device("cuda:0")
+    for number, handle in ((0x7f00, 0x7f00), (0, 0), (1, 0), (2, 2)):
+        where, stream = ops._on(device, number)
+        with where:
+            assert entered[-1] is stream and stream.cuda_stream == handle and stream.device == device
