@@ -595,13 +595,18 @@ class QkOpts:
         return LoongQkOpts(*x_strides, *dx_strides, pos_begin, base, inv, eps, w_offset, rot_scale, norm, rot_dim, inter)
 
     def _struct_of(self, x_strides, dx_strides=(0, 0, 0), pos_begin=0):
-        """struct(...), kept: a program calls with a few strides, and one pos_begin or a counting one."""
-        key = (*x_strides, *dx_strides, pos_begin)
+        """struct(...), kept by the strides, of which a program has a few; a
+        position of its own, which counts up from call to call, takes a copy (the
+        kept one may be in use by another thread's call)."""
+        key = (*x_strides, *dx_strides)
         o = self._structs.get(key)
         if o is None:
             if len(self._structs) >= 64:
                 self._structs.clear()
-            o = self._structs[key] = self.struct(x_strides, dx_strides, pos_begin, formed=True)
+            o = self._structs[key] = self.struct(x_strides, dx_strides, formed=True)
+        if pos_begin:
+            o = LoongQkOpts.from_buffer_copy(o)
+            o.pos_begin = pos_begin
         return o
 
 

@@ -150,3 +150,17 @@ def test_stream_numbers(monkeypatch):
         where, stream = ops._on(device, number)
         with where:
             assert entered[-1] is stream and stream.cuda_stream == handle and stream.device == device
+
+
+def test_counting_positions_keep_one_struct():
+    """A position that moves on with every call finds what is kept, and leaves the struct of an earlier call alone."""
+    opts = ops.make_qk_opts(64)
+    first = opts._struct_of((384, 384, 384), pos_begin=7)
+    for pos in range(200):
+        assert opts._struct_of((384, 384, 384), pos_begin=pos).pos_begin == pos
+    assert first.pos_begin == 7 and len(opts._structs) == 1
+    one = opts._struct_of((384, 384, 384), pos_begin=-3)
+    for name, _ in ops.LoongQkOpts._fields_:
+        if name not in ("pos_begin", "inv_freq"):
+            assert getattr(one, name) == getattr(opts.struct((384, 384, 384)), name), name
+    assert [one.inv_freq[i] for i in range(32)] == [10000.0 ** (-2.0 * i / 64) for i in range(32)]
