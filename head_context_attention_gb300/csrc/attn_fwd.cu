@@ -836,20 +836,13 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   return LOONG_OK;
 }
 
-// With a bias, blocks of one slot where that many find an SM each: a block takes two
-// thirds of a two-slot block's time, so they pay in one round only.  One and two slots,
-// 4K tokens of 4 heads of 128 (128 and 64 blocks) 44.5 and 67.5 us, 2K of 8 + 2 heads of
-// 64 26.9 and 34, 512 of 4 of 128 18.5 and 25.5; 16 heads twice 4K (1,024 and 512 blocks)
-// would take seven rounds for four.
-constexpr int64_t kOneSlotBlocks = 152;
-
 template <bool BIAS>
 int launch_fwd_b(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
                  cudaStream_t stream, int rank_begin, int rank_end, const BiasView* bias) {
   const bool step = d.mode != LOONG_MODE_FUSED;
   if constexpr (BIAS) {
     const RingGeom g = ring_geom(d);
-    if (!step && d.batch * d.hq * g.nblocks * g.ntile <= kOneSlotBlocks) {
+    if (!step && fwd_one_slot(d.batch * d.hq * g.nblocks * g.ntile, num_sms())) {
       if (d.head_dim == 128)
         return launch_fwd_t<128, false, true, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
       if (d.head_dim == 64)

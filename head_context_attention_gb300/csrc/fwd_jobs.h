@@ -1,6 +1,7 @@
-// fwd_jobs.h -- the forward kernel's score buffers: how many, by what the order
-// of its matrix instructions lets the softmax conclude.
+// fwd_jobs.h -- the forward kernel's query slots per block and score buffers.
 //
+// How many buffers, by what the order of its matrix instructions lets the softmax
+// conclude.
 // Job J = slots * j + h is key tile j of query slot h.  The MMA warp issues Q K^T
 // of the first jobs, one per buffer, then P V of job J and Q K^T of job
 // J + buffers in turn; they execute in that order.  Scores of job J therefore
@@ -22,5 +23,12 @@ constexpr int fwd_score_buffers(int head_dim, int slots) {
   const int room = fwd_max_score_buffers(head_dim);
   return room < 2 * slots ? room : 2 * slots;
 }
+
+// With a bias, blocks of one slot where `tiles` query tiles of single heads find an
+// SM each: a block takes two thirds of a two-slot block's time, so they pay in one
+// round only.  One and two slots, 4K tokens of 4 heads of 128 (128 and 64 blocks)
+// 44.5 and 67.5 us, 2K of 8 + 2 heads of 64 26.9 and 34, 512 of 4 of 128 18.5 and
+// 25.5; 16 heads twice 4K (1,024 and 512 blocks) would take seven rounds for four.
+constexpr bool fwd_one_slot(long long tiles, int sms) { return tiles <= sms; }
 
 }  // namespace loong

@@ -122,6 +122,9 @@ struct PieceCode {
   static __host__ __device__ int step(int c) { return (c >> 10) - 128; }   // kPieceStep: at - the second's first place
 };
 
+// SMs of the current device.
+int num_sms();
+
 // Kernel launchers (asynchronous on `stream`).
 // Query rows of ring ranks [rank_begin, rank_end) only (all of them: 0, cp).
 // The forward first writes V's fp16 copy into sc.v16 (with a bias it is there already).

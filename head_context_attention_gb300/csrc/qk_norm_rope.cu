@@ -726,14 +726,6 @@ void fill_args(QkArgs& a, const loong_attn_desc& d, const loong_qk_opts& o, cons
     a.freq[i] = turn_fraction(o.inv_freq ? o.inv_freq[i] : std::pow(o.rot_base, -2.0 * i / o.rot_dim));
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 152;
-  return n;
-}
-
 // Blocks of the launch, and in a.parts how many warps share a token: one when
 // the tokens alone give every resident warp one, more (up to one per slot of
 // heads) when they do not.  (Three items per warp instead of one: 3,003 tokens of
@@ -741,7 +733,7 @@ int sm_count() {
 // every item forms its token's angles again.)
 unsigned plan_grid(QkArgs& a, int blocks_per_sm, int max_blocks) {
   const int slots = a.t[0].slots + a.t[1].slots + a.t[2].slots;
-  const int64_t cap = std::min<int64_t>(static_cast<int64_t>(sm_count()) * blocks_per_sm, max_blocks);
+  const int64_t cap = std::min<int64_t>(static_cast<int64_t>(num_sms()) * blocks_per_sm, max_blocks);
   const int64_t warps = cap * kWarps;
   a.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(slots, warps / a.tokens)));
   const int64_t items = static_cast<int64_t>(a.tokens) * a.parts;

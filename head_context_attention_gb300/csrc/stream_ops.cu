@@ -16,11 +16,6 @@
 
 namespace loong {
 
-namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 int num_sms() {
   static int cached[64] = {0};
   int dev = 0;
@@ -33,6 +28,11 @@ int num_sms() {
   }
   return cached[dev];
 }
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 unsigned grid_for(int64_t work_items, int threads, int per_sm) {
   const int64_t want = (work_items + threads - 1) / threads;

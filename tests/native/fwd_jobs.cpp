@@ -32,6 +32,12 @@ int main() {
                         J - 2 * slots);
       }
     }
+  // one slot per block only where the device runs all blocks in one round
+  for (int sms : {1, 76, 132, 148, 152, 160})
+    if (!loong::fwd_one_slot(sms, sms) || loong::fwd_one_slot(sms + 1, sms)) {
+      std::printf("%d SMs: the rule for one slot does not follow them\n", sms);
+      ++bad;
+    }
   std::printf("%d jobs checked, %d open\n", checked, bad);
   return bad ? 1 : 0;
 }
