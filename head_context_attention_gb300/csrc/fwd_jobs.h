@@ -2,6 +2,7 @@
 //
 // How many buffers, by what the order of its matrix instructions lets the softmax
 // conclude.
+//
 // Job J = slots * j + h is key tile j of query slot h.  The MMA warp issues Q K^T
 // of the first jobs, one per buffer, then P V of job J and Q K^T of job
 // J + buffers in turn; they execute in that order.  Scores of job J therefore

@@ -26,6 +26,7 @@
 #include "fastdiv.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "turns.h"
 
 namespace loong {
 
@@ -65,9 +66,9 @@ struct QkArgs {
   float* dw_part;        // backward: [blocks][2][D]
   int64_t out_elems[3];  // checked build: elements of the attention side
   unsigned* err;
-  // inv_freq / (2 pi) modulo 1 in 64-bit fixed point: pos * freq modulo 2^64 is
-  // the angle in turns for any 64-bit position, with the table's own error
-  // (2^-53 relative to inv_freq) times pos.
+  // inv_freq / (2 pi) modulo 1 in 64-bit fixed point (turns.h): pos * freq modulo
+  // 2^64 is the angle in turns for any 64-bit position, with the table's own
+  // error times pos.
   uint64_t freq[kMaxFreqs];
 };
 
@@ -675,16 +676,6 @@ int check_opts(const loong_attn_desc& d, const loong_qk_opts* o) {
       return LOONG_ERR_INVALID_ARG;
   }
   return LOONG_OK;
-}
-
-// inv_freq / (2 pi) modulo 1 as a 64-bit fraction.
-uint64_t turn_fraction(double inv_freq) {
-  double t = inv_freq / 6.283185307179586476925;
-  t -= std::floor(t);
-  if (t >= 1.0) t = 0.0;  // a tiny negative frequency rounds up to a whole turn
-  const double hi = std::floor(t * 4294967296.0);
-  const double lo = (t * 4294967296.0 - hi) * 4294967296.0;  // exact: powers of two
-  return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo);
 }
 
 void fill_args(QkArgs& a, const loong_attn_desc& d, const loong_qk_opts& o, const int64_t* positions, bool with_v) {

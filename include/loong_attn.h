@@ -420,8 +420,8 @@ LOONG_API int loong_attn_bias_bwd(const loong_attn_desc* desc, const loong_rel_b
  *   rot_scale     factor of every cosine and sine (1 for a plain rotation).
  *   pos_begin     position of token 0 of every sequence, where no positions are
  *                 given.
- * Angles are reduced exactly in 64-bit fixed point: any 64-bit position turns
- * by its angle to 2^-24, plus position * inv_freq * 2^-53.
+ * Angles are reduced in 64-bit fixed point: any 64-bit position turns by its
+ * angle to 2^-23 + |position| (|inv_freq| 2^-52 + 2 pi 2^-64) of a radian.
  */
 typedef struct {
   int64_t q_stride, k_stride, v_stride;

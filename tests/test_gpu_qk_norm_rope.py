@@ -330,3 +330,26 @@ def test_stream_as_a_number(cuda_device):
         got = run(number)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), number
+
+
+def test_angles_of_any_position(cuda_device):
+    """Angles of positions up to 2^55, of frequencies of both signs, against decimals of 60 digits: the stated
+    2^-23 + |position| (|inv_freq| 2^-52 + 2 pi 2^-64) of a radian; then sincospi's and the product's 2^-22 and a
+    rounding to bf16."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    freqs = [1.0, -1.0, 1e-2, -1e-2, 500000.0 ** -0.98, -(500000.0 ** -0.98), 3.7e-7, -3.7e-7]
+    pos = [2 ** 45 + 12345, -(2 ** 45) - 777, 2 ** 50 + 3, 2 ** 55 - 1, 5 * 2 ** 52 + 99, -(2 ** 53), 2 ** 31 - 1, 131072]
+    w = inputs.small(len(pos), 1, 1, 64, placement=0)
+    q = torch.zeros((1, len(pos), 1, 64), device="cuda", dtype=torch.bfloat16)
+    q[..., :8] = 1    # pairs (i, i + 8): (1, 0) turns to (cos, sin)
+    opts = ops.make_qk_opts(64, norm=False, rot_dim=16, inv_freq=freqs)
+    y, _, _ = ops.qk_norm_rope(w, opts, q, q, positions=torch.tensor([pos], device="cuda"))
+    y = to64(y[0, :, 0])
+    for t, p in enumerate(pos):
+        for i, f in enumerate(freqs):
+            angle = float(Decimal(p) * Decimal(f) % two_pi)
+            tol = 2.0 ** -23 + abs(p) * (abs(f) * 2.0 ** -52 + 2 * np.pi * 2.0 ** -64) + 2.0 ** -22
+            for got, want in ((y[t, i], np.cos(angle)), (y[t, i + 8], np.sin(angle))):
+                assert abs(got - want) <= tol + 2.0 ** -8 * (abs(want) + tol), (p, f, got, want, tol)
