@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "fastdiv.cuh"
@@ -665,8 +666,8 @@ int check_opts(const loong_attn_desc& d, const loong_qk_opts* o) {
     if (o->inv_freq) {
       for (int i = 0; i < o->rot_dim / 2; ++i)
         if (!std::isfinite(o->inv_freq[i])) return LOONG_ERR_INVALID_ARG;
-    } else if (!(o->rot_base > 0.0) || !std::isfinite(o->rot_base)) {
-      return LOONG_ERR_INVALID_ARG;
+    } else if (!(o->rot_base >= DBL_MIN) || !std::isfinite(o->rot_base)) {
+      return LOONG_ERR_INVALID_ARG;  // below DBL_MIN the last frequencies are infinite
     }
   }
   const int64_t stride[6] = {o->q_stride, o->k_stride, o->v_stride, o->dq_stride, o->dk_stride, o->dv_stride};

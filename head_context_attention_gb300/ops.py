@@ -11,6 +11,7 @@ import ctypes
 import functools
 import math
 import os
+import sys
 
 import torch
 
@@ -581,7 +582,7 @@ class QkOpts:
             if len(inv) != n:
                 raise ValueError(f"inv_freq needs {n} values")
             self._inv = self._formed = (ctypes.c_double * max(1, n))(*inv)
-        elif 0 < base < math.inf:  # what the library would form from the base, once
+        elif sys.float_info.min <= base < math.inf:  # what the library would form from the base, once
             self._formed = (ctypes.c_double * max(1, n))(*[float(base) ** (-2.0 * i / self.rot_dim) for i in range(n)])
         self._structs = {}
         self._fixed = (float(base), float(eps), float(w_offset), float(rot_scale), 1 if norm else 0, self.rot_dim,

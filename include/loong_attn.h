@@ -416,7 +416,8 @@ LOONG_API int loong_attn_bias_bwd(const loong_attn_desc* desc, const loong_rel_b
  *                 interleaved = 1, (2i, 2i + 1).  Pair i turns by position *
  *                 inv_freq[i] (HOST array of rot_dim/2 finite values, read
  *                 during the call) or, inv_freq == NULL, by position *
- *                 rot_base^(-2i/rot_dim), rot_base > 0 finite.
+ *                 rot_base^(-2i/rot_dim), rot_base a positive normal
+ *                 double.
  *   rot_scale     factor of every cosine and sine (1 for a plain rotation).
  *   pos_begin     position of token 0 of every sequence, where no positions are
  *                 given.

@@ -164,3 +164,10 @@ def test_counting_positions_keep_one_struct():
         if name not in ("pos_begin", "inv_freq"):
             assert getattr(one, name) == getattr(opts.struct((384, 384, 384)), name), name
     assert [one.inv_freq[i] for i in range(32)] == [10000.0 ** (-2.0 * i / 64) for i in range(32)]
+
+
+def test_bases_whose_frequencies_are_infinite_refused(loong_lib):
+    for base in (5e-324, 1e-309):
+        assert ops.loong_qk_norm_rope_bwd_workspace_size(_desc(), ops.make_qk_opts(64, base=base).struct()) == 0
+    for base in (2.0 ** -1022, 1.7e308):
+        assert ops.loong_qk_norm_rope_bwd_workspace_size(_desc(), ops.make_qk_opts(64, base=base).struct()) > 0
