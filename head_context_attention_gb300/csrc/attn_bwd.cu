@@ -134,7 +134,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // up by interval.  Every warp adds to numbers of its own, so the sums do not depend on
 // the order in which blocks run.  The sums fit between dS and the wait for dQ; what
 // they cost is instructions: 32 + 8 heads of 128, 16K tokens, 64 buckets up to 8192
-// 5.2 ms (without a bias 4.8; tensor cores 47 %), 2K ragged tokens of 64 111 us (96).
+// 5.2-5.3 ms (without a bias 4.8; tensor cores 47 %), 2K ragged tokens of 64 111-113 us (96).
 struct BwdPiece {
   float lo, hi;  // the bias of the first and the last place
   int code;      // PieceCode; entry 7: the head in its group

@@ -129,8 +129,9 @@ static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bou
 // causal mask; a row that it leaves nothing gets O = 0 and LSE = -inf.
 // Bound as without a bias, by the matrix instructions and the softmax between
 // them, which a crossed tile lengthens: 32 + 8 heads of 128, 32K tokens with 32
-// buckets up to 128 5.9 ms (without a bias 5.7), 16K with 64 buckets up to 8192,
-// where about half of the tiles are crossed, 1.86 ms (1.45; tensor cores 51 %).
+// buckets up to 128 5.9-6.0 ms (without a bias 5.7), 16K with 64 buckets up to
+// 8192, where about half of the tiles are crossed, 1.86-1.91 ms (1.45-1.47; tensor
+// cores 51 %).
 //
 // With BIAS, an odd group's last head (every head, in groups of one) pairs two
 // query tiles of its own, neighbours in a block, in the two head slots, where the
