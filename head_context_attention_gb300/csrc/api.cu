@@ -239,26 +239,26 @@ static FwdScratch fwd_scratch(const loong_attn_desc& d, void* ws, void* o_res) {
 }
 
 int run_attn_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
-                 void* o_res, void* ws, cudaStream_t stream, const BiasView* bias) {
+                 void* o_res, void* ws, cudaStream_t stream, const BiasView* bias, const MaskView* mask) {
   const FwdScratch sc = fwd_scratch(d, ws, o_res);
-  if (d.mode == LOONG_MODE_FUSED) return launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias);
+  if (d.mode == LOONG_MODE_FUSED) return launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias, mask);
   const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
   cudaError_t e = cudaMemsetAsync(sc.o_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   int st;
   if ((st = launch_fill_f32(lse, d.batch * d.hq * d.seqlen, -INFINITY, stream)) != LOONG_OK) return st;
-  if ((st = launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias)) != LOONG_OK) return st;
+  if ((st = launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias, mask)) != LOONG_OK) return st;
   return launch_f32_to_bf16(sc.o_acc, o, q_elems, stream, o_res);
 }
 
 int run_attn_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
                  const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
-                 cudaStream_t stream, const BiasView* bias, float* dbias_part) {
+                 cudaStream_t stream, const BiasView* bias, float* dbias_part, const MaskView* mask) {
   const BwdWsLayout L = bwd_ws_layout(d);
   uint8_t* w = static_cast<uint8_t*>(ws);
   auto part = [&](size_t off) { return reinterpret_cast<float*>(w + off); };
   return launch_bwd(d, q, k, v, o, o_res, lse, dout, dq, dk, dv, part(L.dq_acc), part(L.stats), part(L.dk_acc),
-                    part(L.dv_acc), stream, is_copy_mode(d) ? w + L.recv : nullptr, bias, dbias_part);
+                    part(L.dv_acc), stream, is_copy_mode(d) ? w + L.recv : nullptr, bias, dbias_part, mask);
 }
 
 Layout layout_of(const loong_attn_desc& d) {

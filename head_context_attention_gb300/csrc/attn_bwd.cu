@@ -36,10 +36,13 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "exchange.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "softcap.cuh"
+#include "v16.cuh"
 
 namespace loong {
 
@@ -56,7 +59,8 @@ struct BwdCfg {
   static constexpr int STAT_BYTES = 2 * kTile * 4;  // LSE*log2e and D of one query tile
   // Tiles first (1024-byte aligned, checked at run time), then the row
   // statistics stages, the barriers, the TMEM base address and the abort
-  // flag, then per stage an iteration descriptor and the bias's pieces.
+  // flag, then per stage an iteration descriptor and the bias's pieces (with a
+  // mask: what a block and its iterations share).
   static constexpr int SMEM_BYTES =
       (2 + 2 * NS) * TILE_BYTES + DS_BYTES + NS * STAT_BYTES + NBARS * 8 + 16 + NS * 144;
   // Compute groups of four warps, each covering all 128 TMEM lanes: group g
@@ -118,6 +122,7 @@ struct BwdArgs {
   BiasView bias;      // BIAS: the bias by distance
   float* dbias_part;  // BIAS: [blocks][compute warps][G][intervals], zeroed
   unsigned* err;
+  MaskView mask;      // MASK: the keys that a query sees, the cap
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -141,12 +146,66 @@ struct BwdPiece {
   int place;     // entry 7: the place of distance q0 - k0
 };
 
-template <int D, bool STEP, bool BIAS>
+// MASK: every query sees a range of keys, scores may be capped (attn_fwd.cu).  A
+// block counts, all threads together, the query tiles some row of which sees one of
+// its keys, by the launch before's sums over their rows; the producer then looks 32
+// of them up at a time.  In a tile not all of whose rows see all keys, a warp
+// turns the ranges of its 32 queries, one in each lane, into bits for its 32 keys and
+// transposes the 32 x 32 bits by five exchanges, so that each lane has a word for
+// its key's row.  With a cap, dS takes the factor 1 - tanh^2, which P is multiplied
+// with once it has been stored for dV, so no further registers are held.
+// A product adds masked rows up with a factor 0, so what they hold has to be finite:
+// rows of K that are not are cleared in shared memory by the compute warps, rows of Q
+// and dO by the producer, in the tiles that the launch before marked.  Instead the
+// row's own P is NaN, for those that see it.
+enum BwdVariant { kBwdPlain, kBwdBias, kBwdMask };
+
+// The query tiles, in natural order, that see a block's keys [k0, k1), a word of 32
+// at a time, and the heads of the group for each.
+struct RangeQWalk {
+  const int4* tiles;
+  const RingGeom* g;
+  int k0, k1, last, G, rank;  // rank: the ring rank whose tiles count, -1: all
+  int base, hk;
+  unsigned live, part;  // of tiles base ..: seen, and not by all rows whole
+  int x;                // the tile
+
+  __device__ static bool sees(int4 r, int k0, int k1) { return r.x < k1 && r.y > k0 && r.x < r.y; }
+  __device__ void fetch(int lane) {
+    const int i = base + lane;
+    bool l = false, p = false;
+    if (i <= last) {
+      const int4 r = __ldg(tiles + i);
+      l = sees(r, k0, k1) && (rank < 0 || block_owner(*g, i / g->ntile) == rank);
+      p = !(r.z <= k0 && r.w >= k1) || k1 - k0 < kTile;
+    }
+    live = __ballot_sync(0xffffffffu, l);
+    part = __ballot_sync(0xffffffffu, p);
+  }
+  // There is a further tile (the caller counts).
+  __device__ void settle(int lane) {
+    while (live == 0 && base <= last) {
+      base += 32;
+      fetch(lane);
+    }
+    x = base + __ffs(live) - 1;
+    hk = 0;
+  }
+  __device__ void advance(int lane) {
+    if (++hk < G) return;
+    live &= live - 1;
+    settle(lane);
+  }
+  __device__ bool partial() const { return part >> (x - base) & 1; }
+};
+
+template <int D, bool STEP, int VARIANT>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     ring_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const __grid_constant__ CUtensorMap tmDQ, const BwdArgs a) {
   using C = BwdCfg<D>;
+  constexpr bool BIAS = VARIANT == kBwdBias, MASK = VARIANT == kBwdMask;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // uniform over the CTA; the swizzled tiles need it
     if (threadIdx.x == 0) atomicOr(a.err, kErrSmemAlign);
@@ -177,6 +236,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // staged into again only after the reducer has read it and it was reloaded
   uint64_t* staged_q = drain + 1;       // NS: dQ(i) columns staged in the Q half (warps -> reducer)
   uint64_t* staged_o = staged_q + C::NS;  // NS: dQ(i) columns staged in the dO half (warps -> reducer)
+  // MASK
+  uint64_t* k_ready = staged_o + C::NS;  // K's rows are finite (compute warps -> MMA)
+  uint64_t* patch = k_ready + 1;         // a stage whose rows the producer looks at first
   uint32_t& tmem_base_sh = *reinterpret_cast<uint32_t*>(bars + C::NBARS);
   int& abort_sh = *(reinterpret_cast<int*>(bars + C::NBARS) + 1);
   volatile int* abort_flag = &abort_sh;
@@ -189,7 +251,13 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // BIAS, per stage: piece diagonal i < 7 (queries 32 (i - 3) ahead of the keys);
   // entry 7: the tile's place and head.
   BwdPiece* sBias = reinterpret_cast<BwdPiece*>(sInfo + C::NS);
-  static_assert(!BIAS || (C::GW == 32 && C::GCH == 1), "a compute warp covers one 32 x 32 piece");
+  static_assert(VARIANT == kBwdPlain || (C::GW == 32 && C::GCH == 1), "a compute warp covers one 32 x 32 piece");
+  // MASK: the first query of every stage's tile (NS words), then the block's count of
+  // tiles, the first and the last of them, then a byte per row of K that is not finite
+  int* sQ0 = reinterpret_cast<int*>(sBias);
+  int* sWalk = sQ0 + 4;
+  uint8_t* sBadK = reinterpret_cast<uint8_t*>(sQ0 + 8);
+  static_assert(C::NS <= 4 && 32 + kTile <= C::NS * 128, "fits the bias's place");
 
   // ---- work item: (batch, kv head, key tile); early (heavy) key tiles first
   const RingGeom& g = a.ring;
@@ -204,10 +272,59 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   const int k0 = bk * g.blk + kt * kTile;
   const int klen = min(kTile, (bk + 1) * g.blk - k0);
 
-  QWalk walk;
-  walk.init(g, a.G, bk, kt, a.t_begin, a.t_end);
-  const int n = walk.total();
-  if (n == 0) return;
+  std::conditional_t<MASK, RangeQWalk, QWalk> walk;
+  int n;
+  if constexpr (MASK) {
+    const int nq = g.nblocks * g.ntile;
+    walk.tiles = a.mask.tiles + static_cast<int64_t>(b) * nq;
+    walk.g = &g;
+    walk.k0 = k0;
+    walk.k1 = k0 + klen;
+    walk.G = a.G;
+    walk.rank = STEP ? ring_dst(block_owner(g, bk), a.t_begin, g.inner, g.outer) : -1;
+    if (threadIdx.x == 0) {
+      sWalk[0] = 0;
+      sWalk[1] = nq;
+      sWalk[2] = -1;
+    }
+    __syncthreads();
+    int count = 0, first = nq, last = -1;
+    for (int i = threadIdx.x; i < nq; i += C::THREADS) {
+      if (RangeQWalk::sees(__ldg(walk.tiles + i), k0, k0 + klen) &&
+          (!STEP || block_owner(g, i / g.ntile) == walk.rank)) {
+        ++count;
+        first = min(first, i);
+        last = i;
+      }
+    }
+    count = __reduce_add_sync(0xffffffffu, count);
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    if ((threadIdx.x & 31) == 0 && count) {
+      atomicAdd(sWalk, count);
+      atomicMin(sWalk + 1, first);
+      atomicMax(sWalk + 2, last);
+    }
+    __syncthreads();
+    n = sWalk[0] * a.G;
+    walk.base = sWalk[1];
+    walk.last = sWalk[2];
+    if (n == 0) {
+      if constexpr (!STEP) {  // no query sees the keys
+        for (int i = threadIdx.x; i < klen * (D / 8); i += C::THREADS) {
+          const int64_t kv = a.lay.vec(b, k0 + i / (D / 8), kvh, a.hkv);
+          if (!in_bounds(kv >= 0 && kv < static_cast<int64_t>(a.batch) * a.S * a.hkv, a.err)) continue;
+          reinterpret_cast<uint4*>(a.dk + kv * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+          reinterpret_cast<uint4*>(a.dv + kv * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      return;
+    }
+  } else {
+    walk.init(g, a.G, bk, kt, a.t_begin, a.t_end);
+    n = walk.total();
+    if (n == 0) return;
+  }
   const int nflush = (n - 1) / kFlush;  // flushes before the final write
 
   const int warp = threadIdx.x >> 5;
@@ -234,6 +351,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     mbar_init(acc_empty, C::CW);
     mbar_init(done_bar, 1);
     mbar_init(drain, 1);
+    if constexpr (MASK) {
+      mbar_init(k_ready, C::CW);
+      mbar_init(patch, 1);
+    }
     abort_sh = 0;
     fence_mbar_init();
   }
@@ -247,6 +368,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     tma_prefetch_map(&tmV);
     tma_prefetch_map(&tmO);
     tma_prefetch_map(&tmDQ);
+  }
+  if constexpr (MASK) {
+    if (threadIdx.x < kTile) sBadK[threadIdx.x] = 0;
   }
   tc_fence_before();
   __syncthreads();
@@ -294,43 +418,100 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         }
       };
       look_up();
+      // MASK: whether the tile the walk stands at has rows to clear (for the next trip)
+      unsigned marked = 0, patches = 0;
+      auto look_up_mark = [&]() {
+        if constexpr (MASK)
+          marked = __ldg(a.mask.bad + (static_cast<int64_t>(b) * a.hq + kvh * a.G + walk.hk) * g.nblocks * g.ntile +
+                         walk.x);
+      };
+      if constexpr (MASK) {
+        walk.fetch(lane);
+        walk.settle(lane);
+      }
+      look_up_mark();
       for (int i = 0; i < n; ++i) {
         const int s = i % C::NS;
         const int u = i / C::NS;
         // coordinates first, off the wait's critical path
-        const int head = kvh * a.G + walk.head;
+        int head, q0, qlen, bq, qi, flags;
+        if constexpr (MASK) {
+          head = kvh * a.G + walk.hk;
+          bq = walk.x / g.ntile;
+          qi = walk.x - bq * g.ntile;
+          q0 = bq * g.blk + qi * kTile;
+          qlen = min(kTile, (bq + 1) * g.blk - q0);
+          flags = walk.partial() || qlen < kTile ? 4 : 0;
+        } else {
+          head = kvh * a.G + walk.head;
+          bq = walk.bq;
+          qi = walk.qi;
+          q0 = walk.q0();
+          qlen = walk.qlen();
+          flags = walk.diag() ? 1 : 0;
+        }
         int hc;
-        const int64_t qrow64 = a.lay.view_row(b, walk.q0(), head, a.hq, hc);
+        const int64_t qrow64 = a.lay.view_row(b, q0, head, a.hq, hc);
         in_bounds(qrow64 >= 0 && qrow64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
         const int qrow = static_cast<int>(qrow64);
         // checked build: a reduction never starts outside the accumulator (skipped if it would)
         const bool red_ok =
             in_bounds(qrow64 >= 0 && qrow64 < a.lay.view_rows(a.batch) && hc >= 0 && hc < a.lay.view_heads(a.hq), a.err);
         if (i >= C::NS && !warp_wait(&q_empty[s], (u - 1) & 1, abort_flag, a.err)) break;
-        if (leader) sInfo[s] = make_int4(qrow, hc, walk.qlen(), (walk.diag() ? 1 : 0) | (red_ok ? 2 : 0));
+        if (leader) sInfo[s] = make_int4(qrow, hc, qlen, flags | (red_ok ? 2 : 0));
+        if (MASK && leader) sQ0[s] = q0;
+        // a stage with rows to clear arrives on `patch` first
+        uint64_t* full = MASK && marked ? patch : &q_full[s];
         if constexpr (BIAS) {
           if (lane < 8) sBias[s * 8 + lane] = piece;
           __syncwarp();
         }
-        mbar_expect_tx_p(leader, &q_full[s], 2 * C::TILE_BYTES + C::STAT_BYTES);
+        mbar_expect_tx_p(leader, full, 2 * C::TILE_BYTES + C::STAT_BYTES);
         for (int at = 0; at < C::ATOMS; ++at) {
-          tma_load_3d_p(leader, sQ + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, &q_full[s], at * 64, hc, qrow);
-          tma_load_3d_p(leader, sdO + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmO, &q_full[s], at * 64, hc, qrow);
+          tma_load_3d_p(leader, sQ + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, full, at * 64, hc, qrow);
+          tma_load_3d_p(leader, sdO + s * C::TILE_BYTES + at * C::ATOM_BYTES, &tmO, full, at * 64, hc, qrow);
         }
         // this tile's row statistics: 16-byte aligned and in bounds by construction
-        int64_t srow = (static_cast<int64_t>(b) * a.hq + head) * a.stat_len + walk.bq * a.blk_pad +
-                       walk.qi * kTile;
+        int64_t srow = (static_cast<int64_t>(b) * a.hq + head) * a.stat_len + bq * a.blk_pad + qi * kTile;
         // checked build: a plain bulk copy must stay inside the statistics rows
         // (else it reads row 0 instead, keeping the barrier's byte count)
         if (!in_bounds(srow >= 0 && srow % 4 == 0 &&
                            srow + kTile <= (static_cast<int64_t>(b) * a.hq + head + 1) * a.stat_len,
                        a.err))
           srow = 0;
-        bulk_load_p(leader, sStat + s * (2 * kTile), a.lse2 + srow, kTile * 4, &q_full[s]);
-        bulk_load_p(leader, sStat + s * (2 * kTile) + kTile, a.dstat + srow, kTile * 4, &q_full[s]);
+        bulk_load_p(leader, sStat + s * (2 * kTile), a.lse2 + srow, kTile * 4, full);
+        bulk_load_p(leader, sStat + s * (2 * kTile) + kTile, a.dstat + srow, kTile * 4, full);
+        if constexpr (MASK) {
+          if (marked) {  // uniform over the warp
+            if (!warp_wait(patch, patches++ & 1, abort_flag, a.err)) {
+              mbar_drain(patch, (patches - 1) & 1, a.err);
+              break;
+            }
+            const float* lse_row = sStat + s * (2 * kTile);
+            const int line = lane & (D / 8 - 1);  // 16 bytes of a row of Q; D = 128: the upper lanes' of dO
+#pragma unroll 1
+            for (int r0 = 0; r0 < kTile; r0 += 32) {
+              unsigned m = __ballot_sync(0xffffffffu, !(fabsf(lse_row[r0 + lane]) < INFINITY) || r0 + lane >= qlen);
+              for (; m; m &= m - 1) {
+                const int at = s * C::TILE_BYTES + (line >> 3) * C::ATOM_BYTES + (r0 + __ffs(m) - 1) * 128 + (line & 7) * 16;
+                if (D == 64 || lane < 16) *reinterpret_cast<uint4*>(sQ + at) = make_uint4(0, 0, 0, 0);
+                if (D == 64 || lane >= 16) *reinterpret_cast<uint4*>(sdO + at) = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_p(leader, &q_full[s]);
+          }
+        }
         ++issued;
-        walk.advance();
-        if (BIAS && i + 1 < n) look_up();  // used in the next trip
+        if constexpr (MASK)
+          walk.advance(lane);
+        else
+          walk.advance();
+        if (i + 1 < n) {  // used in the next trip
+          look_up();
+          look_up_mark();
+        }
       }
       mbar_drain(kv_full, 0, a.err);
       for (int s = 0; s < C::NS; ++s) {
@@ -364,7 +545,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           mma_ss_w(tbase + dst, a_desc + off, b_desc + off, id_s, kk > 0);
         }
       };
-      bool ok = warp_wait(kv_full, 0, abort_flag, a.err) && warp_wait(&q_full[0], 0, abort_flag, a.err);
+      bool ok = warp_wait(kv_full, 0, abort_flag, a.err) && (!MASK || warp_wait(k_ready, 0, abort_flag, a.err)) &&
+                warp_wait(&q_full[0], 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
         mm_s(C::R0, k16, d16(q_addr));
@@ -501,7 +683,29 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         atomicAdd(part + (sum_block * 32 + lane) * a.bias.intervals + sum_ivl, run_sum);
       run_sum = 0.f;
     };
-    for (int i = 0; i < n; ++i) {
+    // MASK: clear the rows of K that are not finite; four threads look at a row
+    bool key_bad = false;
+    if constexpr (MASK) {
+      ok = warp_wait(kv_full, 0);
+      constexpr int V = D / 8 / C::GROUPS;  // 16-byte parts of a thread
+      uint8_t* line = sK + (grp * V / 8) * C::ATOM_BYTES + row * 128 + (grp * V % 8) * 16;
+      unsigned m = 0;
+      if (ok) {
+#pragma unroll
+        for (int u = 0; u < V; ++u) v16_finite(*reinterpret_cast<const uint4*>(line + u * 16), m);
+      }
+      if (m) sBadK[row] = 1;
+      asm volatile("bar.sync 1, %0;" ::"n"(C::CW * 32) : "memory");
+      key_bad = sBadK[row];
+      if (key_bad) {
+#pragma unroll
+        for (int u = 0; u < V; ++u) *reinterpret_cast<uint4*>(line + u * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      mbar_arrive_p(lane == 0, k_ready);
+    }
+    for (int i = 0; i < n && ok; ++i) {
       // row statistics of this tile, staged by the producer with Q and dO
       const float* lse_row = sStat + (i % C::NS) * (2 * kTile);
       const float* d_row = lse_row + kTile;
@@ -571,12 +775,55 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       // have every column live and skip the per-element mask.
       const int lo = dg ? row : 0;
       const int hi = key_ok ? qlen : 0;
-      const bool unmasked = __all_sync(0xffffffffu, lo == 0 && hi == kTile);
+      const bool unmasked = MASK ? !(info.w & 4) : __all_sync(0xffffffffu, lo == 0 && hi == kTile);
+      // MASK: the queries of the warp's columns that see this lane's key
+      unsigned seen = 0xffffffffu;
+      if constexpr (MASK) {
+        if (!unmasked) {
+          const int c = grp * 32 + lane, t = sQ0[i % C::NS] + c;
+          const int2 r = c < qlen ? mask_range(a.mask, b, t, a.S, g.causal) : make_int2(0, 0);
+          const int kq = k0 + quarter * 32;
+          seen = transpose_bits(low_bits(min(r.y - kq, klen - quarter * 32)) & ~low_bits(r.x - kq), lane);
+        }
+        if (a.mask.cap_inv > 0.f) {
+          uint32_t sv[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv[e] = __float_as_uint(pv[0][e]);
+          cap_scores(sv, a.mask.cap_inv);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pv[0][e] = __uint_as_float(sv[e]);
+        }
+        if (key_bad) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pv[0][e] = __int_as_float(0x7fffffff);
+        }
+      }
 #pragma unroll
       for (int ch = 0; ch < C::GCH; ++ch) {
         const int cbase = grp * C::GW + ch * 32;  // first query column of the chunk
         uint32_t pk[16];
-        if (unmasked) {
+        if constexpr (MASK) {
+          const bool capped = a.mask.cap_inv > 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse_row + cbase + e);
+            const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              const float t0 = pv[0][e + u], t1 = pv[0][e + u + 1];
+              float x, y;
+              form_p(t0, t1, lv[u], lv[u + 1], x, y);
+              if (!unmasked) {
+                x = seen >> (e + u) & 1 ? x : 0.f;
+                y = seen >> (e + u + 1) & 1 ? y : 0.f;
+              }
+              pk[(e + u) / 2] = pack_bf16(x, y);
+              // from here on P with the cap's derivative, for dS
+              pv[0][e + u] = capped && x != 0.f ? x * fmaf(-t0, t0, 1.f) : x;
+              pv[0][e + u + 1] = capped && y != 0.f ? y * fmaf(-t1, t1, 1.f) : y;
+            }
+          }
+        } else if (unmasked) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             // the same query indices in every lane: broadcast shared-memory reads
@@ -600,8 +847,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             }
           }
         }
+        if constexpr (!MASK) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16(pv[ch][e], pv[ch][e + 1]);
+          for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16(pv[ch][e], pv[ch][e + 1]);
+        }
         // P^T (bf16 pairs) into this group's own columns of R0,
         // [GW grp + 16 ch, +16): already read by this group, never read by another.
         asm volatile(
@@ -882,10 +1131,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool STEP, bool BIAS>
+template <int D, bool STEP, int VARIANT>
 int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* dout,
                  const float* stats, float* dq_acc, void* dk, void* dv, float* dk_acc,
-                 float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias, float* dbias_part) {
+                 float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias, float* dbias_part,
+                 const MaskView* mask) {
   using C = BwdCfg<D>;
   const Layout lay = layout_of(d);
   const int64_t rows = lay.view_rows(d.batch);
@@ -908,7 +1158,8 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   a.G = d.hq / d.hkv;
   a.ring = ring_geom(d);
   a.scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
-  a.scale_log2 = a.scale * kLog2e;
+  a.mask = VARIANT == kBwdMask ? *mask : MaskView{};
+  a.scale_log2 = (a.mask.cap_inv > 0.f ? a.scale / a.mask.cap_inv : a.scale) * kLog2e;
   a.lse2 = stats;
   a.blk_pad = stat_block_pad(a.ring.blk);
   a.stat_len = static_cast<int>(stat_row_len(a.ring));
@@ -918,11 +1169,11 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dk_acc = dk_acc;
   a.dv_acc = dv_acc;
-  a.bias = BIAS ? *bias : BiasView{};
+  a.bias = VARIANT == kBwdBias ? *bias : BiasView{};
   a.dbias_part = dbias_part;
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
-  auto kern = ring_bwd_kernel<D, STEP, BIAS>;
+  auto kern = ring_bwd_kernel<D, STEP, VARIANT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(a.ring.nblocks) * a.ring.ntile;
@@ -973,21 +1224,21 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   return LOONG_OK;
 }
 
-template <bool BIAS>
-int launch_bwd_b(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* dout,
+template <int VARIANT>
+int launch_bwd_v(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* dout,
                  const float* stats, float* dq_acc, void* dk, void* dv, float* dk_acc, float* dv_acc,
-                 cudaStream_t stream, void* kv_recv, const BiasView* bias, float* part) {
+                 cudaStream_t stream, void* kv_recv, const BiasView* bias, float* part, const MaskView* mask) {
   const bool step = d.mode != LOONG_MODE_FUSED;
   if (d.head_dim == 128)
-    return step ? launch_bwd_t<128, true, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
-                                                kv_recv, bias, part)
-                : launch_bwd_t<128, false, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
-                                                 kv_recv, bias, part);
+    return step ? launch_bwd_t<128, true, VARIANT>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                   kv_recv, bias, part, mask)
+                : launch_bwd_t<128, false, VARIANT>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                    kv_recv, bias, part, mask);
   if (d.head_dim == 64)
-    return step ? launch_bwd_t<64, true, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
-                                               kv_recv, bias, part)
-                : launch_bwd_t<64, false, BIAS>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
-                                                kv_recv, bias, part);
+    return step ? launch_bwd_t<64, true, VARIANT>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                  kv_recv, bias, part, mask)
+                : launch_bwd_t<64, false, VARIANT>(d, q, k, v, dout, stats, dq_acc, dk, dv, dk_acc, dv_acc, stream,
+                                                   kv_recv, bias, part, mask);
   return LOONG_ERR_UNSUPPORTED;
 }
 
@@ -996,12 +1247,12 @@ int launch_bwd_b(const loong_attn_desc& d, const void* q, const void* k, const v
 int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
                const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, float* dq_acc, float* dvec,
                float* dk_acc, float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias,
-               float* dbias_part) {
+               float* dbias_part, const MaskView* mask) {
   const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
   const int64_t kv_elems = d.batch * d.seqlen * d.hkv * d.head_dim;
   const bool step = d.mode != LOONG_MODE_FUSED;
   int st;
-  cudaError_t e = bias ? cudaSuccess : cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
+  cudaError_t e = bias || mask ? cudaSuccess : cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   // FUSED walks of at most kFlush (tile, head) pairs never touch the dK, dV accumulators
   const RingGeom g = ring_geom(d);
@@ -1010,11 +1261,13 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
       ((e = cudaMemsetAsync(dk_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess ||
        (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess))
     return cuda_fail(e);
-  if (!bias && (st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream)) != LOONG_OK) return st;
-  st = bias ? launch_bwd_b<true>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,
-                                 dbias_part)
-            : launch_bwd_b<false>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, nullptr,
-                                  nullptr);
+  if (!bias && !mask && (st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream)) != LOONG_OK) return st;
+  st = bias   ? launch_bwd_v<kBwdBias>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,
+                                       dbias_part, nullptr)
+       : mask ? launch_bwd_v<kBwdMask>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv,
+                                       nullptr, nullptr, mask)
+              : launch_bwd_v<kBwdPlain>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv,
+                                        nullptr, nullptr, nullptr);
   if (st != LOONG_OK) return st;
   if (!bias && (st = launch_f32_to_bf16(dq_acc, dq, q_elems, stream)) != LOONG_OK) return st;
   if (step) {

@@ -48,11 +48,14 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "exchange.h"
 #include "fwd_jobs.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "softcap.cuh"
+#include "v16.cuh"
 
 namespace loong {
 
@@ -74,10 +77,10 @@ struct FwdCfg {
   static_assert(NINFO >= NS + NSB && NSB >= 2, "a tile's entry is read before it is rewritten");
   static constexpr int SMEM_BYTES = (NQ + 2 * NS) * TILE_BYTES + NBARS * 8 + 1024;
   static constexpr int THREADS = 320;
-  // Bias: a third whole warpgroup (two of its warps idle), whose registers go to
+  // With a bias or a mask: a third whole warpgroup (two of its warps idle), whose registers go to
   // the softmax warps: 256 * 216 + 128 * 72 = 384 * 168, what the block starts with.
-  static constexpr int BIAS_THREADS = 384, BIAS_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
-  static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= BIAS_THREADS * BIAS_REGS, "register split");
+  static constexpr int SPLIT_THREADS = 384, SPLIT_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
+  static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= SPLIT_THREADS * SPLIT_REGS, "register split");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int buf) { return static_cast<uint32_t>(buf) * 128u; }
   __host__ __device__ static constexpr uint32_t O_COL(int h) { return NSB * 128u + static_cast<uint32_t>(h) * D; }
@@ -99,6 +102,7 @@ struct FwdArgs {
   const unsigned* v_amax;  // bit pattern of max |V|: V was stored as V * 2^-v16_shift
   BiasView bias;           // BIAS: the bias by distance
   unsigned* err;
+  MaskView mask;           // MASK: the keys that a query sees, the cap
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -144,6 +148,18 @@ static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bou
 // logit is off by at most 2^-24 * 22, as one of that size is anyway.
 constexpr float kMaxMiddle = 32.0f;  // log2 units
 
+// MASK gives every query a range of keys and may cap the scores (softcap.cuh;
+// scale_log2 is then the cap's).  A block walks the tiles between the first and the
+// last key that any of its rows sees (RangeWalk), which the launch before summed up
+// for it; a block whose rows see nothing only writes that.  A softmax warp some of
+// whose rows do not see a whole tile masks it by four words of bits a row.  Columns of
+// masked keys are replaced, so what the keys hold does not matter; V, whose rows a
+// product adds up with P = 0, is 0 in its copy where it is not finite, and where
+// there was such a value (v_amax[1]) the scores of its key become NaN for the rows
+// that see it.
+// Pairs of heads and of tiles are formed as with a bias.
+enum FwdVariant { kFwdPlain, kFwdBias, kFwdMask };
+
 struct FwdPiece {
   float lo, hi;  // the difference before and, kPieceStep, from the boundary on
   int kind;      // PieceKind
@@ -151,14 +167,15 @@ struct FwdPiece {
 };
 
 //
-// SLOTS = 1 (with BIAS): one head's query tile per block, where even such blocks do
+// SLOTS = 1 (with BIAS or MASK): one head's query tile per block, where even such blocks do
 // not fill the SMs.  The second slot's warps idle; the scores of the next tile, in
 // the other buffer, are computed while the softmax works.
-template <int D, bool STEP, bool BIAS, int SLOTS = 2>
-__global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::THREADS, 1)
+template <int D, bool STEP, int VARIANT, int SLOTS = 2>
+__global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREADS : FwdCfg<D>::THREADS, 1)
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
   using C = FwdCfg<D>;
+  constexpr bool BIAS = VARIANT == kFwdBias, MASK = VARIANT == kFwdMask, PAIRS = VARIANT != kFwdPlain;
   constexpr int NSB = fwd_score_buffers(D, SLOTS);
   static_assert(NSB <= 2 * SLOTS, "a tile's scores prove P V of the tile two back");
   extern __shared__ uint8_t smem_raw[];
@@ -205,7 +222,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
     idx /= a.G;
     r = idx % nqt;
     idx /= nqt;
-  } else if constexpr (BIAS) {  // first the pairs of tiles of an odd group's last head, then the pairs of heads
+  } else if constexpr (PAIRS) {  // first the pairs of tiles of an odd group's last head, then the pairs of heads
     const int npt = (a.G & 1) ? nr * rank_parts(g) * ((g.ntile + 1) / 2) : 0;
     const int npairs = a.G / 2;
     int item = idx % (npt + nqt * npairs);
@@ -232,16 +249,36 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   const int qi = tile_pair ? min(qi0 + 1, g.ntile - 1) : qi0;
   const int head0 = kvh * a.G + (tile_pair ? a.G - 1 : SLOTS * hpair);
   // slot 1 repeats slot 0: an odd group without bias, a last tile without a neighbour
-  const bool dup = BIAS ? tile_pair && qi == qi0 : head0 + 1 >= (kvh + 1) * a.G;
+  const bool dup = PAIRS ? tile_pair && qi == qi0 : head0 + 1 >= (kvh + 1) * a.G;
   const int head1 = SLOTS == 1 || dup || tile_pair ? head0 : head0 + 1;
   const int q0 = bq * g.blk + qi0 * kTile;   // slot 0's first row, slot 1's
   const int q1 = bq * g.blk + qi * kTile;
-  const int qlen = min(kTile, (bq + 1) * g.blk - q0);  // slot 0's rows; without BIAS slot 1's too
+  const int qlen = min(kTile, (bq + 1) * g.blk - q0);  // slot 0's rows; without PAIRS slot 1's too
 
-  KvWalk walk;
-  walk.init(g, bq, qi, a.t_begin, a.t_end);
+  std::conditional_t<MASK, RangeWalk, KvWalk> walk;
+  if constexpr (MASK) {
+    const int4* tiles = a.mask.tiles + (static_cast<int64_t>(b) * g.nblocks + bq) * g.ntile;
+    const int4 t0 = tiles[qi0], t1 = tiles[qi];
+    walk.init(g, block_owner(g, bq), a.t_begin, a.t_end, min(t0.x, t1.x), max(t0.y, t1.y));
+  } else {
+    walk.init(g, bq, qi, a.t_begin, a.t_end);
+  }
   const int n = walk.total();
-  if (n == 0) return;  // uniform over the CTA: nothing of this tile in these steps
+  if (n == 0) {  // uniform over the CTA: nothing of this tile in these steps
+    if constexpr (MASK && !STEP) {  // no row sees a key
+      for (int i = threadIdx.x; i < SLOTS * kTile * (D / 8); i += C::SPLIT_THREADS) {
+        const int h = i / (kTile * (D / 8)), row = i / (D / 8) % kTile, part = i % (D / 8);
+        const int qh = h ? q1 : q0, head = h ? head1 : head0;
+        if (row >= min(kTile, (bq + 1) * g.blk - qh)) continue;
+        const int64_t qv = a.lay.vec(b, qh + row, head, a.hq);
+        if (!in_bounds(qv >= 0 && qv < static_cast<int64_t>(a.batch) * a.S * a.hq, a.err)) continue;
+        reinterpret_cast<uint4*>(a.o + qv * D)[part] = make_uint4(0, 0, 0, 0);
+        if (a.o_res) reinterpret_cast<uint4*>(a.o_res + qv * D)[part] = make_uint4(0, 0, 0, 0);
+        if (part == 0) a.lse[(static_cast<int64_t>(b) * a.hq + head) * a.S + qh + row] = -INFINITY;
+      }
+    }
+    return;
+  }
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -279,7 +316,7 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = tmem_base_sh;
-  if constexpr (BIAS) {
+  if constexpr (PAIRS) {
     if (warp >= 8) regs_dec<C::OTHER_REGS>();
   }
 
@@ -448,8 +485,8 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       mma_commit_w(drain);
       mbar_drain(drain, 0, a.err);
     }
-  } else if (!BIAS || warp < 4 * SLOTS) {
-    if constexpr (BIAS) regs_inc<C::SOFTMAX_REGS>();
+  } else if (!PAIRS || warp < 4 * SLOTS) {
+    if constexpr (PAIRS) regs_inc<C::SOFTMAX_REGS>();
     // ------------------------------------------------------------ softmax
     const int h = warp >> 2;
     const int quarter = warp & 3;
@@ -460,6 +497,14 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
     float m_run = -INFINITY;
     float l_run = 0.f;
     bool ok = true;
+    // MASK: the keys of this row (rows past the block see all, they are not stored)
+    int2 see = make_int2(0, 0);
+    bool v_bad = false;
+    if constexpr (MASK) {
+      const int tok = (h ? q1 : q0) + row;
+      see = tok < (bq + 1) * g.blk ? mask_range(a.mask, b, tok, a.S, g.causal) : make_int2(0, 0x7fffffff);
+      v_bad = a.v_amax[1] != 0;
+    }
     for (int j = 0; j < n; ++j, walk.advance()) {
       // Lanes leave together so the .sync.aligned TMEM accesses never diverge.
       const int J = SLOTS * j + h;  // this tile's MMA job and its score buffer
@@ -527,12 +572,56 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       uint32_t sr[4][32];
       const int klen = walk.klen();
       // the causal diagonal tile; BIAS: or slot 0's, or one after it that only slot 1 sees
-      const bool dg = BIAS ? g.causal && walk.bk == bq && walk.kt >= (h ? qi : qi0) : walk.diag();
+      const bool dg = [&]() {
+        if constexpr (MASK)
+          return false;
+        else
+          return BIAS ? g.causal && walk.bk == bq && walk.kt >= (h ? qi : qi0) : walk.diag();
+      }();
+      const int k0 = walk.k0();
+      // MASK: NaN for the keys whose V holds values that are not finite
+      auto poison = [&](uint32_t(&s)[4][32]) {
+        if constexpr (MASK) {
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb) {
+            bool bad = false;  // of the lane's key
+            const int key = cb * 32 + lane;
+            if (key < klen) {
+              const uint4* vv = reinterpret_cast<const uint4*>(a.mask.v + a.lay.vec(b, k0 + key, kvh, a.hkv) * D);
+              unsigned m = 0;
+              for (int i = 0; i < D / 8; ++i) v16_finite(__ldg(vv + i), m);
+              bad = m != 0;
+            }
+            const unsigned keys = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (keys >> i & 1) s[cb][i] = 0x7fffffffu;
+          }
+        }
+      };
       // the tile's scores, masked columns at -inf (read again by the full path)
       auto load_s = [&]() {
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) tmem_ld32(tS + cb * 32, sr[cb]);
         tmem_wait_ld();
+        if constexpr (MASK) {
+          if (a.mask.cap_inv > 0.f) {
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) cap_scores(sr[cb], a.mask.cap_inv);
+          }
+          if (v_bad) poison(sr);
+          const int lo = see.x - k0, hi = min(see.y - k0, klen);  // columns that the row sees
+          if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+              const uint32_t bits = low_bits(hi - cb * 32) & ~low_bits(lo - cb * 32);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1)) sr[cb][i] = __float_as_uint(-INFINITY);
+            }
+          }
+          return;
+        }
         if (dg || klen < kTile) {
           int lim = dg ? min(row, klen - 1) : klen - 1;
           if (BIAS && dg && walk.kt > (h ? qi : qi0)) lim = -1;
@@ -639,13 +728,13 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
       const int64_t qv = a.lay.vec(b, qh + row, head, a.hq);  // this row's d-vector in Q / O
       const int64_t lse_i = (static_cast<int64_t>(b) * a.hq + head) * a.S + (qh + row);
       // checked build: the row's O, accumulator and LSE entries lie inside their tensors
-      const bool valid = row < (BIAS ? min(kTile, (bq + 1) * g.blk - qh) : qlen) && !(h == 1 && dup) &&
+      const bool valid = row < (PAIRS ? min(kTile, (bq + 1) * g.blk - qh) : qlen) && !(h == 1 && dup) &&
                          in_bounds(qv >= 0 && qv < static_cast<int64_t>(a.batch) * a.S * a.hq && lse_i >= 0 &&
                                        lse_i < static_cast<int64_t>(a.batch) * a.hq * a.S,
                                    a.err);
-      // l_run and O carry 2^kPBias; O also carries V's 2^-e.  BIAS: a row without keys
+      // l_run and O carry 2^kPBias; O also carries V's 2^-e.  PAIRS: a row without keys
       // has l_run = 0, and one that met a NaN keeps it (in its LSE for the gradient as well)
-      const bool any = BIAS ? l_run != 0.f : l_run > 0.f;
+      const bool any = PAIRS ? l_run != 0.f : l_run > 0.f;
       const float lse_p = any ? (m_run + log2f(l_run) - kPBias) * kLn2 : -INFINITY;
       const float o_mul = __int_as_float((127 + v16_shift(*a.v_amax)) << 23);  // 2^e
       float* lse_ptr = a.lse + lse_i;
@@ -700,9 +789,9 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
           const float wa = la == -INFINITY ? 0.f : exp2f((la - mm) * kLog2e);
           const float wp = lse_p == -INFINITY ? 0.f : exp2f((lse_p - mm) * kLog2e);
           const float tot = wa + wp;
-          if (BIAS ? tot != 0.f : tot > 0.f) {
+          if (PAIRS ? tot != 0.f : tot > 0.f) {
             ca = wa / tot;
-            cpart = BIAS && wp == 0.f ? 0.f : wp * o_mul / (tot * l_run);
+            cpart = PAIRS && wp == 0.f ? 0.f : wp * o_mul / (tot * l_run);
             lse_new = mm + log2f(tot) * kLn2;
           }
         }
@@ -738,11 +827,12 @@ __global__ void __launch_bounds__(BIAS ? FwdCfg<D>::BIAS_THREADS : FwdCfg<D>::TH
   }
 }
 
-template <int D, bool STEP, bool BIAS, int SLOTS = 2>
+template <int D, bool STEP, int VARIANT, int SLOTS = 2>
 int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o,
                  float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end,
-                 const BiasView* bias) {
+                 const BiasView* bias, const MaskView* mask) {
   using C = FwdCfg<D>;
+  constexpr bool BIAS = VARIANT == kFwdBias, MASK = VARIANT == kFwdMask;
   const Layout lay = layout_of(d);
   const int64_t rows = lay.view_rows(d.batch);
   CUtensorMap mq, mk, mv;
@@ -767,7 +857,8 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   a.rank_end = rank_end;
   a.kv_held = 0;
   const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
-  a.scale_log2 = scale * kLog2e;
+  a.mask = MASK ? *mask : MaskView{};
+  a.scale_log2 = (a.mask.cap_inv > 0.f ? scale / a.mask.cap_inv : scale) * kLog2e;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_res = static_cast<__nv_bfloat16*>(sc.o_res);
   a.lse = lse;
@@ -777,19 +868,19 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
 
-  auto kern = ring_fwd_kernel<D, STEP, BIAS, SLOTS>;
+  auto kern = ring_fwd_kernel<D, STEP, VARIANT, SLOTS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
-  constexpr int threads = BIAS ? C::BIAS_THREADS : C::THREADS;
-  if constexpr (BIAS) {
+  constexpr int threads = VARIANT != kFwdPlain ? C::SPLIT_THREADS : C::THREADS;
+  if constexpr (VARIANT != kFwdPlain) {
     // the register split draws on what the block starts with: less would wait for ever
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return cuda_fail(e);
-    if (at.numRegs < C::BIAS_REGS) return LOONG_ERR_UNSUPPORTED;
+    if (at.numRegs < C::SPLIT_REGS) return LOONG_ERR_UNSUPPORTED;
   }
   const int64_t blocks = static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring);
   const int64_t per_kvh = SLOTS == 1 ? blocks * a.ring.ntile * a.G
-                          : BIAS     ? blocks * (a.ring.ntile * (a.G / 2) + (a.G & 1) * ((a.ring.ntile + 1) / 2))
+                          : BIAS || MASK ? blocks * (a.ring.ntile * (a.G / 2) + (a.G & 1) * ((a.ring.ntile + 1) / 2))
                                      : blocks * a.ring.ntile * a.npairs;
   const int64_t grid = d.batch * d.hkv * per_kvh;
   if (grid <= 0 || grid > 0x7fffffff) return LOONG_ERR_INVALID_ARG;
@@ -837,25 +928,25 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   return LOONG_OK;
 }
 
-template <bool BIAS>
-int launch_fwd_b(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
-                 cudaStream_t stream, int rank_begin, int rank_end, const BiasView* bias) {
+template <int VARIANT>
+int launch_fwd_v(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
+                 cudaStream_t stream, int rank_begin, int rank_end, const BiasView* bias, const MaskView* mask) {
   const bool step = d.mode != LOONG_MODE_FUSED;
-  if constexpr (BIAS) {
+  if constexpr (VARIANT != kFwdPlain) {
     const RingGeom g = ring_geom(d);
     if (!step && fwd_one_slot(d.batch * d.hq * g.nblocks * g.ntile, num_sms())) {
       if (d.head_dim == 128)
-        return launch_fwd_t<128, false, true, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+        return launch_fwd_t<128, false, VARIANT, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
       if (d.head_dim == 64)
-        return launch_fwd_t<64, false, true, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+        return launch_fwd_t<64, false, VARIANT, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
     }
   }
   if (d.head_dim == 128)
-    return step ? launch_fwd_t<128, true, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
-                : launch_fwd_t<128, false, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+    return step ? launch_fwd_t<128, true, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask)
+                : launch_fwd_t<128, false, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
   if (d.head_dim == 64)
-    return step ? launch_fwd_t<64, true, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
-                : launch_fwd_t<64, false, BIAS>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias);
+    return step ? launch_fwd_t<64, true, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask)
+                : launch_fwd_t<64, false, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
   return LOONG_ERR_UNSUPPORTED;
 }
 
@@ -863,14 +954,13 @@ int launch_fwd_b(const loong_attn_desc& d, const void* q, const void* k, void* o
 
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
                float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end,
-               const BiasView* bias) {
+               const BiasView* bias, const MaskView* mask) {
   if (rank_end < 0) rank_end = d.cp;
-  int st;
-  if (!bias && (st = launch_v_to_f16(v, sc.v16, sc.v_amax, d.batch * d.seqlen * d.hkv * d.head_dim, stream)) !=
-                   LOONG_OK)
-    return st;
-  return bias ? launch_fwd_b<true>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias)
-              : launch_fwd_b<false>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr);
+  if (bias) return launch_fwd_v<kFwdBias>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, nullptr);
+  if (mask) return launch_fwd_v<kFwdMask>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr, mask);
+  const int st = launch_v_to_f16(v, sc.v16, sc.v_amax, d.batch * d.seqlen * d.hkv * d.head_dim, stream);
+  if (st != LOONG_OK) return st;
+  return launch_fwd_v<kFwdPlain>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr, nullptr);
 }
 
 }  // namespace loong

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -122,29 +123,52 @@ struct PieceCode {
   static __host__ __device__ int step(int c) { return (c >> 10) - 128; }   // kPieceStep: at - the second's first place
 };
 
+// What a mask leaves of the attention, as the attention kernels read it
+// (mask_attn.cu fills it): a range of keys for every query and the cap of the
+// scores.  `tiles` sums the ranges of every 128-row query tile up, [B][nblocks *
+// ntile] in natural order: x, y: the first key that any row sees and the one past
+// the last (x >= y: none); z, w: the keys from z on and before w are seen by every
+// row.  Both take the causal limit in.
+struct MaskView {
+  const int2* range = nullptr;  // [B][S] first key and the one past the last, or null: every key
+  const int4* tiles = nullptr;
+  const uint8_t* bad = nullptr;  // backward: [B][hq][nblocks * ntile], tiles with rows to clear
+  const __nv_bfloat16* v = nullptr;  // forward: V as given
+  float cap_inv = 0.f;           // softmax scale / cap, 0: no cap
+};
+
+// The keys [x, y) that query t of sequence b sees; (0, 0) where none.
+__device__ __forceinline__ int2 mask_range(const MaskView& m, int b, int t, int S, int causal) {
+  int2 r = m.range ? __ldg(m.range + static_cast<int64_t>(b) * S + t) : make_int2(0, S);
+  r.x = max(r.x, 0);
+  r.y = min(r.y, causal ? t + 1 : S);
+  return r.x < r.y ? r : make_int2(0, 0);
+}
+
 // SMs of the current device.
 int num_sms();
 
 // Kernel launchers (asynchronous on `stream`).
 // Query rows of ring ranks [rank_begin, rank_end) only (all of them: 0, cp).
-// The forward first writes V's fp16 copy into sc.v16 (with a bias it is there already).
+// The forward first writes V's fp16 copy into sc.v16 (with a bias or a mask it is there already).
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
                float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin = 0, int rank_end = -1,
-               const BiasView* bias = nullptr);
+               const BiasView* bias = nullptr, const MaskView* mask = nullptr);
 // o_res: the forward's residual of O, or null (D from O alone).  With a bias the
 // row statistics are in dvec and dq_acc is zeroed already, and dq_acc is left to
-// the caller to convert.
+// the caller to convert; with a mask the former two.
 int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v,
                const void* o, const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv,
                float* dq_acc, float* dvec, float* dk_acc, float* dv_acc, cudaStream_t stream,
-               void* kv_recv = nullptr, const BiasView* bias = nullptr, float* dbias_part = nullptr);
+               void* kv_recv = nullptr, const BiasView* bias = nullptr, float* dbias_part = nullptr,
+               const MaskView* mask = nullptr);
 // The whole passes behind the entry points, on checked arguments, in a
 // workspace of loong_attn_workspace_size bytes.
 int run_attn_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
-                 void* o_res, void* ws, cudaStream_t stream, const BiasView* bias);
+                 void* o_res, void* ws, cudaStream_t stream, const BiasView* bias, const MaskView* mask = nullptr);
 int run_attn_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
                  const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
-                 cudaStream_t stream, const BiasView* bias, float* dbias_part);
+                 cudaStream_t stream, const BiasView* bias, float* dbias_part, const MaskView* mask = nullptr);
 // Blocks of a backward launch (key tiles of every kv head and sequence) and
 // compute warps of each: the rows of dbias_part.
 constexpr int kBwdComputeWarps = 16;

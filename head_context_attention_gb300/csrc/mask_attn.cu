@@ -1,0 +1,321 @@
+// mask_attn.cu -- ring attention in which every query sees a range of keys of its
+// own and scores may be capped: the entry points and the launches in front of the
+// attention kernels (the scores themselves in attn_fwd.cu, attn_bwd.cu).
+//
+//   z_ij = cap tanh(scale q_i.k_j / cap), over begin_i <= j < end_i (and j <= i, causal)
+//   P = softmax(z), O = P V;  dS = P (dP - D) (1 - (z / cap)^2)
+//
+// A range covers what training on long sequences masks with: packed documents,
+// prefixes, windows, padding.  The attention kernels visit only the tiles that some
+// row sees, so before them every 128-row query tile's ranges are summed up (16 bytes
+// for 128 * 8), in the launch that prepares V or the row statistics anyway.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowstats.cuh"
+#include "v16.cuh"
+
+namespace loong {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 1216;                  // of a launch that strides over its data: 8 per SM
+constexpr int64_t kMaxSeqlen = int64_t{1} << 30;  // a tile past the last token still has a 32-bit number
+// A capped logit is at most the cap; up to 2^20 the softmax's reference, rounded to
+// 24 bits, is off by at most 2^-3 in log2 units, which fp16 P has room for.
+constexpr float kMinCap = 9.5367432e-7f, kMaxCap = 1048576.f;        // 2^-20, 2^20
+constexpr float kMinScale = 5.9604645e-8f, kMaxScale = 16777216.f;  // 2^-24, 2^24
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct TileArgs {
+  MaskView m;
+  RingGeom g;
+  int S;
+  int64_t count;  // B * nblocks * ntile
+};
+
+// The ranges of query tile x (of B * nblocks * ntile), by a warp.
+__device__ __forceinline__ void sum_tile(const TileArgs& a, int64_t x) {
+  const int lane = threadIdx.x & 31;
+  const int per_seq = a.g.nblocks * a.g.ntile;
+  const int b = static_cast<int>(x / per_seq);
+  const int i = static_cast<int>(x - static_cast<int64_t>(b) * per_seq);
+  const int bq = i / a.g.ntile;
+  const int t0 = bq * a.g.blk + (i - bq * a.g.ntile) * kTile;
+  const int t1 = min(t0 + kTile, (bq + 1) * a.g.blk);
+  int first = 0x7fffffff, last = 0, all_from = 0, all_to = 0x7fffffff;
+#pragma unroll
+  for (int u = 0; u < kTile / 32; ++u) {
+    const int t = t0 + u * 32 + lane;
+    if (t < t1) {
+      const int2 r = mask_range(a.m, b, t, a.S, a.g.causal);
+      const bool some = r.x < r.y;
+      first = min(first, some ? r.x : 0x7fffffff);
+      last = max(last, r.y);
+      all_from = max(all_from, some ? r.x : 0x7fffffff);
+      all_to = min(all_to, r.y);
+    }
+  }
+  first = __reduce_min_sync(0xffffffffu, first);
+  last = __reduce_max_sync(0xffffffffu, last);
+  all_from = __reduce_max_sync(0xffffffffu, all_from);
+  all_to = __reduce_min_sync(0xffffffffu, all_to);
+  if (lane == 0) const_cast<int4*>(a.m.tiles)[x] = make_int4(first, last, all_from, all_to);
+}
+
+// Before the forward, in one launch: V's part of it (v16.cuh; its blocks come
+// first), then 8 tiles a block.
+__global__ void __launch_bounds__(kThreads) mask_fwd_prep_kernel(const __grid_constant__ TileArgs a,
+                                                                 const __grid_constant__ VArgs v) {
+  const int id = static_cast<int>(blockIdx.x) - max(v.max_blocks, 1);
+  if (id < 0) {
+    v16_first_launch<kThreads, true>(v, blockIdx.x);
+    return;
+  }
+  const int64_t x = static_cast<int64_t>(id) * (kThreads / 32) + threadIdx.x / 32;
+  if (x < a.count) sum_tile(a, x);
+}
+
+__global__ void __launch_bounds__(kThreads) mask_v16_kernel(const __grid_constant__ VArgs v) {
+  v16_copy<kThreads, true>(v);
+}
+
+// Before the backward, in one launch, a block for a query tile of a head: dQ's
+// accumulator cleared, the row statistics (rowstats.cuh), and whether the tile has
+// rows for the backward's producer to clear: those whose dO or LSE is not finite (so
+// is their LSE among the statistics: NaN, but -inf for a row that sees no key), and
+// with a cap, which leaves infinite scores finite, those whose Q is not; and,
+// where the tile ends inside the block of 128, any not finite among the rows behind
+// it, which the copies bring in as well.  Head 0's blocks sum the tile's ranges up.
+// Bound by memory: O, its residual and dO in, the accumulator out.
+struct BwdPrepArgs {
+  TileArgs tiles;
+  RowStatsArgs r;
+  const __nv_bfloat16* q;
+  float* dq_acc;
+  uint8_t* bad;
+};
+template <int D>
+__global__ void __launch_bounds__(kThreads) mask_bwd_prep_kernel(const __grid_constant__ BwdPrepArgs a) {
+  constexpr int TPR = D / 8, RPP = kThreads / TPR;  // threads of a row, rows of a pass
+  const RowStatsArgs& r = a.r;
+  const RingGeom& g = a.tiles.g;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int bq = blockIdx.x / g.ntile, qi = blockIdx.x - bq * g.ntile;
+  const int t0 = bq * g.blk + qi * kTile, len = min(kTile, (bq + 1) * g.blk - t0);
+  const int part = threadIdx.x % TPR;
+  int hc;
+  const int64_t row0 = r.lay.view_row(b, t0, h, r.hq, hc);
+  const int heads = r.lay.view_heads(r.hq);
+  const int64_t rows = r.lay.view_rows(gridDim.z), bh = static_cast<int64_t>(b) * r.hq + h;
+  const int64_t stat0 = bh * r.stat_len + static_cast<int64_t>(bq) * r.blk_pad + qi * kTile;
+  bool mark = false;
+#pragma unroll
+  for (int p = 0; p < kTile / RPP; ++p) {
+    const int row = p * RPP + threadIdx.x / TPR;
+    const int64_t at = ((row0 + row) * heads + hc) * D + part * 8;
+    const bool there = row0 + row < rows;
+    float acc = 0.f;
+    unsigned bad = 0;
+    if (row < len) {
+      if (in_bounds(there, r.err)) {
+        const uint4 ov = __ldg(reinterpret_cast<const uint4*>(r.o + at));
+        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(r.dout + at));
+        const uint4 rv = r.o_res ? __ldg(reinterpret_cast<const uint4*>(r.o_res + at)) : make_uint4(0, 0, 0, 0);
+        float4* dq = reinterpret_cast<float4*>(a.dq_acc + at);
+        dq[0] = dq[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        v16_finite(gv, bad);
+        if (a.tiles.m.cap_inv > 0.f) v16_finite(__ldg(reinterpret_cast<const uint4*>(a.q + at)), bad);
+        const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
+        const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&gv);
+        const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&rv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 fo = __bfloat1622float2(o2[e]);
+          const float2 fr = __bfloat1622float2(r2[e]);
+          const float2 fg = __bfloat1622float2(g2[e]);
+          acc = fmaf(fo.x + fr.x, fg.x, acc);
+          acc = fmaf(fo.y + fr.y, fg.y, acc);
+        }
+      }
+    } else if (there) {
+      v16_finite(__ldg(reinterpret_cast<const uint4*>(a.q + at)), bad);
+      v16_finite(__ldg(reinterpret_cast<const uint4*>(r.dout + at)), bad);
+    }
+    mark |= bad != 0;
+#pragma unroll
+    for (int off = TPR / 2; off > 0; off >>= 1) {
+      acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      bad |= __shfl_xor_sync(0xffffffffu, bad, off);
+    }
+    if (part == 0 && row < len) {
+      const int64_t pos = stat0 + row;
+      if (in_bounds(pos >= 0 && pos < (bh + 1) * r.stat_len, r.err)) {
+        float l = __ldg(r.lse + bh * r.S + t0 + row);
+        if (bad || !(l < INFINITY)) l = __int_as_float(0x7fffffff);
+        r.dstat[pos] = acc;
+        r.lse2[pos] = l * kRowStatsLog2e;
+        mark |= !(fabsf(l) < INFINITY);
+      }
+    }
+  }
+  const int any = __syncthreads_or(mark);
+  if (threadIdx.x == 0) a.bad[bh * g.nblocks * g.ntile + blockIdx.x] = any != 0;
+  if (h == 0 && threadIdx.x < 32) sum_tile(a.tiles, static_cast<int64_t>(b) * g.nblocks * g.ntile + blockIdx.x);
+}
+
+int check_mask(const loong_attn_desc* d, const loong_attn_mask* m) {
+  int st = loong_attn_check(d);
+  if (st != LOONG_OK) return st;
+  if (!m || !std::isfinite(m->score_cap) || m->score_cap < 0.f) return LOONG_ERR_INVALID_ARG;
+  if (d->seqlen > kMaxSeqlen || d->hq > 65535 || d->batch > 65535) return LOONG_ERR_UNSUPPORTED;
+  if (m->score_cap > 0.f) {
+    if (m->score_cap < kMinCap || m->score_cap > kMaxCap) return LOONG_ERR_UNSUPPORTED;
+    if (d->softmax_scale > 0.f && (d->softmax_scale < kMinScale || d->softmax_scale > kMaxScale))
+      return LOONG_ERR_UNSUPPORTED;
+  }
+  return LOONG_OK;
+}
+
+// The workspace: the plain pass's first, then the tiles' sums and, forward, the
+// shares of max |V|, backward, the marks of the query tiles.
+struct MaskWs {
+  size_t tiles, shares, bad, total;
+  int64_t count;
+};
+MaskWs mask_ws(const loong_attn_desc& d, int pass) {
+  const RingGeom g = ring_geom(d);
+  MaskWs w{};
+  w.count = d.batch * static_cast<int64_t>(g.nblocks) * g.ntile;
+  size_t at = up256(loong_attn_workspace_size(&d, pass));
+  w.tiles = at;
+  at += up256(static_cast<size_t>(w.count) * sizeof(int4));
+  if (pass == 0) {
+    w.shares = at;
+    at += up256(kMaxBlocks * 4);
+  } else {
+    w.bad = at;
+    at += up256(static_cast<size_t>(w.count) * d.hq);
+  }
+  w.total = at;
+  return w;
+}
+
+TileArgs tile_args(const loong_attn_desc& d, const loong_attn_mask& m, const MaskWs& w, uint8_t* base) {
+  TileArgs a;
+  a.m.range = reinterpret_cast<const int2*>(m.key_range);
+  a.m.tiles = reinterpret_cast<const int4*>(base + w.tiles);
+  const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.head_dim));
+  a.m.cap_inv = m.score_cap > 0.f ? scale / m.score_cap : 0.f;
+  a.g = ring_geom(d);
+  a.S = static_cast<int>(d.seqlen);
+  a.count = w.count;
+  return a;
+}
+
+}  // namespace
+
+}  // namespace loong
+
+using namespace loong;
+
+extern "C" {
+
+int loong_attn_mask_check(const loong_attn_desc* d, const loong_attn_mask* mask) { return check_mask(d, mask); }
+
+size_t loong_attn_mask_workspace_size(const loong_attn_desc* d, const loong_attn_mask* mask, int pass) {
+  if (check_mask(d, mask) != LOONG_OK || (pass != 0 && pass != 1)) return 0;
+  return mask_ws(*d, pass).total;
+}
+
+int loong_attn_mask_fwd(const loong_attn_desc* d, const loong_attn_mask* mask, const void* q, const void* k,
+                        const void* v, void* o, float* lse, void* o_res, void* ws, size_t ws_bytes,
+                        loong_stream_t stream_) {
+  NvtxRange range("loong_attn_mask_fwd");
+  int st = check_mask(d, mask);
+  if (st != LOONG_OK) return st;
+  const void* ptrs[] = {q, k, v, o, lse};
+  for (const void* p : ptrs)
+    if (!p || !aligned(p, 16)) return LOONG_ERR_INVALID_ARG;
+  if (!aligned(o_res, 16) || !aligned(mask->key_range, 8)) return LOONG_ERR_INVALID_ARG;
+  const MaskWs w = mask_ws(*d, 0);
+  if (!ws || ws_bytes < w.total || !aligned(ws, 16)) return LOONG_ERR_WORKSPACE;
+  if ((st = device_ready()) != LOONG_OK) return st;
+  for (const void* p : ptrs)
+    if (!on_device(p)) return LOONG_ERR_INVALID_ARG;
+  if (!on_device(ws) || (o_res && !on_device(o_res)) || (mask->key_range && !on_device(mask->key_range)))
+    return LOONG_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  TileArgs a = tile_args(*d, *mask, w, base);
+  a.m.v = static_cast<const __nv_bfloat16*>(v);
+  const FwdWsLayout L = fwd_ws_layout(*d);
+  VArgs va;
+  va.v = static_cast<const uint4*>(v);
+  va.v16 = reinterpret_cast<uint4*>(base + L.v16);
+  va.amax = reinterpret_cast<unsigned*>(base + L.amax);
+  va.shares = reinterpret_cast<unsigned*>(base + w.shares);
+  va.vecs = d->batch * d->seqlen * d->hkv * d->head_dim / 8;
+  auto blocks_for = [](int64_t n) {
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, kMaxBlocks)));
+  };
+  va.max_blocks = va.vecs <= kBlockV ? 0 : blocks_for(va.vecs / 2);
+  const int64_t tile_blocks = (w.count + kThreads / 32 - 1) / (kThreads / 32);
+  mask_fwd_prep_kernel<<<static_cast<unsigned>(std::max(va.max_blocks, 1) + tile_blocks), kThreads, 0, stream>>>(a, va);
+  if ((st = check_launch()) != LOONG_OK) return st;
+  if (va.max_blocks > 0) {
+    mask_v16_kernel<<<static_cast<unsigned>(blocks_for(va.vecs)), kThreads, 0, stream>>>(va);
+    if ((st = check_launch()) != LOONG_OK) return st;
+  }
+  return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, nullptr, &a.m);
+}
+
+int loong_attn_mask_bwd(const loong_attn_desc* d, const loong_attn_mask* mask, const void* q, const void* k,
+                        const void* v, const void* o, const void* o_res, const float* lse, const void* dout, void* dq,
+                        void* dk, void* dv, void* ws, size_t ws_bytes, loong_stream_t stream_) {
+  NvtxRange range("loong_attn_mask_bwd");
+  int st = check_mask(d, mask);
+  if (st != LOONG_OK) return st;
+  const void* ptrs[] = {q, k, v, o, lse, dout, dq, dk, dv};
+  for (const void* p : ptrs)
+    if (!p || !aligned(p, 16)) return LOONG_ERR_INVALID_ARG;
+  if (!aligned(o_res, 16) || !aligned(mask->key_range, 8)) return LOONG_ERR_INVALID_ARG;
+  const MaskWs w = mask_ws(*d, 1);
+  if (!ws || ws_bytes < w.total || !aligned(ws, 16)) return LOONG_ERR_WORKSPACE;
+  if ((st = device_ready()) != LOONG_OK) return st;
+  for (const void* p : ptrs)
+    if (!on_device(p)) return LOONG_ERR_INVALID_ARG;
+  if (!on_device(ws) || (o_res && !on_device(o_res)) || (mask->key_range && !on_device(mask->key_range)))
+    return LOONG_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const BwdWsLayout L = bwd_ws_layout(*d);
+  BwdPrepArgs a;
+  a.tiles = tile_args(*d, *mask, w, base);
+  int passes;
+  if ((st = rowstats_args(*d, o, o_res, dout, lse, reinterpret_cast<float*>(base + L.stats), &a.r, &passes)) !=
+      LOONG_OK)
+    return st;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.dq_acc = reinterpret_cast<float*>(base + L.dq_acc);
+  a.bad = base + w.bad;
+  const RingGeom& g = a.tiles.g;
+  const dim3 grid(static_cast<unsigned>(g.nblocks * g.ntile), static_cast<unsigned>(d->hq),
+                  static_cast<unsigned>(d->batch));
+  if (d->head_dim == 128)
+    mask_bwd_prep_kernel<128><<<grid, kThreads, 0, stream>>>(a);
+  else
+    mask_bwd_prep_kernel<64><<<grid, kThreads, 0, stream>>>(a);
+  if ((st = check_launch()) != LOONG_OK) return st;
+  a.tiles.m.bad = a.bad;
+  return run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, nullptr, nullptr, &a.tiles.m);
+}
+
+}  // extern "C"

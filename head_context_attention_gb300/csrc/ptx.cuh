@@ -373,6 +373,25 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// The lowest n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32));
+}
+
+// A 32 x 32 matrix of bits, a row in every lane's word, transposed: bit c of lane
+// r's result is bit r of lane c's word.  Blocks of 16, 8, .. 1 change places.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  uint32_t low = 0x0000ffffu;  // the columns whose bit j is 0
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    // rows with bit j of their number 0 keep their low columns and take the partner's low ones above them
+    x = lane & j ? (x & ~low) | ((y >> j) & low) : (x & low) | ((y & low) << j);
+    if (j > 1) low ^= low << (j >> 1);
+  }
+  return x;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

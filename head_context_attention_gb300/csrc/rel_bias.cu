@@ -38,11 +38,6 @@ constexpr float kMinScale = 5.9604645e-8f;        // 2^-24
 constexpr int64_t kMaxSeqlen = int64_t{1} << 29;  // places fit 32 bits
 constexpr int kSumSplits = 64;
 constexpr int kMaxBlocks = 1216;  // of a launch that strides over its data: 8 per SM
-// V of at most this many vectors of 8 is converted by one block, beside the
-// expansion, else by two launches.  The forward of heads of 64, one block and two
-// launches: 1,600 vectors 17.1 and 20.8 us, 4,096 21.0 and 23.0, 6,144 23.1 and
-// 24.7, 8,192 25.1 and 25.2, 12,288 29.2 and 27.1.
-constexpr int64_t kBlockV = 8192;
 
 struct BucketMap {
   int intervals;
@@ -107,68 +102,22 @@ __device__ __forceinline__ void expand_block(const ExpandArgs& a, int bx, int by
   }
 }
 
-// Maximum over the block of every thread's m, in every thread.
-__device__ __forceinline__ unsigned block_max(unsigned m) {
-  __shared__ unsigned warp_max[kThreads / 32];
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = max(m, warp_max[w]);
-  return m;
-}
-
 // Before the forward, in one launch: nx x ny blocks expand the bias, the rest
-// work on V.  One block brings a short V into its fp16 form (whole); else
+// work on V (v16.cuh): one block brings a short V into its fp16 form (whole); else
 // max_blocks blocks take the maximum of |V| of a share each, for v16_kernel.
-// 16K tokens of 32 + 8 heads of 128: 11.6 us for V's 34 MB, 11.8 us for the
-// copy (cold); memory's latency, in launches this short.
-struct VArgs {
-  const uint4* v;
-  uint4* v16;
-  unsigned* amax;
-  unsigned* shares;  // [max_blocks]
-  int64_t vecs;
-  int max_blocks;  // 0: one block converts V
-};
 __global__ void __launch_bounds__(kThreads) fwd_prep_kernel(const __grid_constant__ ExpandArgs a, int nx, int ny,
                                                             const __grid_constant__ VArgs v) {
   // V's blocks, the longer ones, come first
-  const int vb = max(v.max_blocks, 1), id = static_cast<int>(blockIdx.x) - vb;
+  const int id = static_cast<int>(blockIdx.x) - max(v.max_blocks, 1);
   if (id >= 0) {
     const int by = id / nx;
     expand_block(a, id - by * nx, by, ny);
     return;
   }
-  if (v.max_blocks == 0) {
-    block_v_to_f16<kThreads>(v.v, v.v16, v.amax, static_cast<int>(v.vecs));
-    return;
-  }
-  constexpr int U = 4;  // loads in flight per thread
-  const int64_t i1 = v.vecs * (blockIdx.x + 1) / vb;
-  unsigned m = 0;
-  for (int64_t i = v.vecs * blockIdx.x / vb + threadIdx.x; i < i1; i += kThreads * U) {
-    uint4 x[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) x[k] = i + k * kThreads < i1 ? __ldg(v.v + i + k * kThreads) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int k = 0; k < U; ++k) m = max(m, v16_absmax(x[k]));
-  }
-  m = block_max(m);
-  if (threadIdx.x == 0) v.shares[blockIdx.x] = m;
+  v16_first_launch<kThreads>(v, blockIdx.x);
 }
 
-// V's fp16 form from the shares' maxima, and max |V| for the attention kernel.
-__global__ void __launch_bounds__(kThreads) v16_kernel(const __grid_constant__ VArgs v) {
-  unsigned m = 0;
-  for (int i = threadIdx.x; i < v.max_blocks; i += kThreads) m = max(m, __ldg(v.shares + i));
-  m = block_max(m) << 16;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *v.amax = m;
-  const float f = v16_factor(m);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < v.vecs; i += stride)
-    v.v16[i] = v16_scaled(__ldg(v.v + i), f);
-}
+__global__ void __launch_bounds__(kThreads) v16_kernel(const __grid_constant__ VArgs v) { v16_copy<kThreads>(v); }
 
 // 16-byte words cleared by the whole grid.
 __device__ __forceinline__ void clear(uint4* p, int64_t n, int64_t id, int64_t threads) {

@@ -191,6 +191,80 @@ struct KvWalk {
   }
 };
 
+// Key tiles that a query tile of ring rank c meets where its rows see keys of
+// [kmin, kmax) only: over the whole ring (steps < 0) in natural order, from the
+// first block that holds one (most ring steps hold none), else the blocks of ring
+// step t's source rank.  Of every block the tiles from the one that holds the first
+// such key to the one that holds the last.
+struct RangeWalk {
+  RingGeom g;
+  int kmin, kmax;
+  int first, parts;  // the first block, or the source rank; blocks to visit
+  bool whole;
+  int p, kt, kt_n, bk;
+
+  __host__ __device__ void init(const RingGeom& geom, int c, int t0, int t1, int kmin_, int kmax_) {
+    g = geom;
+    kmin = kmin_;
+    kmax = kmax_;
+    whole = t0 == 0 && t1 == g.cp;
+    p = 0;
+    if (kmin >= kmax) {
+      first = parts = 0;
+    } else if (whole) {
+      first = kmin / g.blk;
+      parts = (kmax - 1) / g.blk - first + 1;
+    } else {
+      first = ring_src(c, t0, g.inner, g.outer);
+      parts = rank_parts(g);
+    }
+    settle();
+  }
+  __host__ __device__ int block(int part) const { return whole ? first + part : rank_block(g, first, part); }
+  __host__ __device__ int tile_begin(int b) const {
+    const int off = kmin - b * g.blk;
+    return off > 0 ? off / kTile : 0;
+  }
+  __host__ __device__ int tile_end(int b) const {
+    int off = kmax - b * g.blk;
+    if (off > g.blk) off = g.blk;
+    return off > 0 ? (off + kTile - 1) / kTile : 0;
+  }
+  __host__ __device__ void settle() {
+    for (; p < parts; ++p) {
+      bk = block(p);
+      kt = tile_begin(bk);
+      kt_n = tile_end(bk);
+      if (kt < kt_n) return;
+    }
+  }
+  __host__ __device__ int k0() const { return bk * g.blk + kt * kTile; }
+  __host__ __device__ int klen() const {
+    const int e = (bk + 1) * g.blk - k0();
+    return e < kTile ? e : kTile;
+  }
+  __host__ __device__ void advance() {
+    if (++kt < kt_n) return;
+    ++p;
+    settle();
+  }
+  // Number of tiles of the whole walk.  Over the whole ring in closed form: the
+  // tiles that begin before kmax less those that end before kmin.
+  __host__ __device__ int total() const {
+    if (parts == 0) return 0;
+    if (whole) {
+      const int last = first + parts - 1;
+      return last * g.ntile + tile_end(last) - first * g.ntile - tile_begin(first);
+    }
+    int n = 0;
+    for (int i = 0; i < parts; ++i) {
+      const int b = block(i), m = tile_end(b) - tile_begin(b);
+      n += m > 0 ? m : 0;
+    }
+    return n;
+  }
+};
+
 // Ring rank that holds source j's K/V at step t (inverse of ring_src in c).
 __host__ __device__ inline int ring_dst(int j, int t, int inner, int outer) {
   const int o = t / inner, i = t - (t / inner) * inner;

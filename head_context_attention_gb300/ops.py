@@ -38,6 +38,7 @@ EXPORTS = ("loong_version", "loong_status_string", "loong_last_cuda_error", "loo
            "loong_attn_bwd",
            "loong_attn_bwd_noalloc", "loong_lse_merge", "loong_headctx_pack", "loong_headctx_pack_n",
            "loong_rel_bias_check", "loong_attn_bias_workspace_size", "loong_attn_bias_fwd", "loong_attn_bias_bwd",
+           "loong_attn_mask_check", "loong_attn_mask_workspace_size", "loong_attn_mask_fwd", "loong_attn_mask_bwd",
            "loong_qk_norm_rope_fwd", "loong_qk_norm_rope_bwd_workspace_size", "loong_qk_norm_rope_bwd",
            "loong_attn_2d_host_workspace_size", "loong_attn_2d_host", "loong_host_alloc", "loong_host_free",
            "loong_set_timing_events", "loong_get_device_status", "loong_selftest_wait_timeout")
@@ -57,6 +58,10 @@ class LoongRelBias(ctypes.Structure):
     _fields_ = [("num_buckets", ctypes.c_int32), ("num_bounds", ctypes.c_int32),
                 ("bounds", ctypes.POINTER(ctypes.c_int32)), ("bucket_of", ctypes.POINTER(ctypes.c_int32)),
                 ("table", ctypes.c_void_p)]
+
+
+class LoongAttnMask(ctypes.Structure):
+    _fields_ = [("key_range", ctypes.c_void_p), ("score_cap", ctypes.c_float)]
 
 
 class LoongQkOpts(ctypes.Structure):
@@ -113,6 +118,12 @@ def lib():
         L.loong_attn_bias_workspace_size.argtypes = [D, RB, ctypes.c_int]
         L.loong_attn_bias_fwd.argtypes = [D, RB, P, P, P, P, P, P, P, SZ, P]
         L.loong_attn_bias_bwd.argtypes = [D, RB, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        MK = ctypes.POINTER(LoongAttnMask)
+        L.loong_attn_mask_check.argtypes = [D, MK]
+        L.loong_attn_mask_workspace_size.restype = SZ
+        L.loong_attn_mask_workspace_size.argtypes = [D, MK, ctypes.c_int]
+        L.loong_attn_mask_fwd.argtypes = [D, MK, P, P, P, P, P, P, P, SZ, P]
+        L.loong_attn_mask_bwd.argtypes = [D, MK, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         L.loong_qk_norm_rope_fwd.argtypes = [D, QO, P, P, P, P, P, P, P, P, P, P]
         L.loong_qk_norm_rope_bwd_workspace_size.restype = SZ
         L.loong_qk_norm_rope_bwd_workspace_size.argtypes = [D, QO]
@@ -332,6 +343,33 @@ def loong_attn_bias_bwd(desc, bias, q, k, v, o, o_res, lse, dout, dq, dk, dv, dt
     return _check("loong_attn_bias_bwd", lib().loong_attn_bias_bwd(
         ctypes.byref(desc), ctypes.byref(bias), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse),
         _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dtable), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def make_mask(key_range=None, score_cap=0.0):
+    """loong_attn_mask; keeps the tensor it points at."""
+    m = LoongAttnMask(None if key_range is None else key_range.data_ptr(), score_cap)
+    m.keep = key_range
+    return m
+
+
+def loong_attn_mask_check(desc, mask):
+    return lib().loong_attn_mask_check(ctypes.byref(desc), ctypes.byref(mask))
+
+
+def loong_attn_mask_workspace_size(desc, mask, pass_):
+    return lib().loong_attn_mask_workspace_size(ctypes.byref(desc), ctypes.byref(mask), pass_)
+
+
+def loong_attn_mask_fwd(desc, mask, q, k, v, o, lse, o_res, ws, stream=None):
+    return _check("loong_attn_mask_fwd", lib().loong_attn_mask_fwd(
+        ctypes.byref(desc), ctypes.byref(mask), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(o_res), _ptr(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def loong_attn_mask_bwd(desc, mask, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream=None):
+    return _check("loong_attn_mask_bwd", lib().loong_attn_mask_bwd(
+        ctypes.byref(desc), ctypes.byref(mask), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse),
+        _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def loong_qk_norm_rope_fwd(desc, opts, q, k, v, wq, wk, positions, q_out, k_out, v_out, stream=None):
@@ -565,6 +603,94 @@ def attn_bias_bwd(w, q, k, v, o, lse, do, table, buckets, o_res=None, mode=MODE_
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         loong_attn_bias_bwd(desc, buckets.struct(table), q, k, v, o, o_res, lse, do, dq, dk, dv, dtable, ws, stream)
     return dq, dk, dv, dtable
+
+
+def document_ranges(lengths, seqlen, prefix=None, window=0, causal=True, device=None):
+    """The key ranges (int32 [B, seqlen, 2]) of packed documents: ``lengths`` has,
+    for every sequence, the lengths of its documents in order; what they leave of
+    seqlen is padding, which sees nothing.  A token sees its own document:
+    itself and what is before it (causal), of that the last ``window`` tokens (0:
+    all), and the whole of the document's first part, where ``prefix`` gives that
+    part's length for every document; not causal: all of it, or the ``window``
+    tokens on both sides and itself.  With a prefix give the ranges to a workload
+    that is not causal."""
+    if window < 0 or (prefix is not None and (window or not causal)):
+        raise ValueError("window must not be negative, and a prefix goes with neither a window nor causal=False")
+    out = torch.zeros((len(lengths), seqlen, 2), dtype=torch.int32)
+    for b, docs in enumerate(lengths):
+        if any(n < 0 for n in docs) or sum(docs) > seqlen:
+            raise ValueError(f"sequence {b}: documents of {list(docs)} tokens do not fit {seqlen}")
+        if prefix is not None and (len(prefix[b]) != len(docs) or any(p < 0 for p in prefix[b])):
+            raise ValueError(f"sequence {b}: a prefix length for each of its documents")
+        at = 0
+        for i, n in enumerate(docs):
+            t = torch.arange(at, at + n, dtype=torch.int32)
+            first, last = torch.full_like(t, at), t + 1
+            if not causal:
+                last = torch.full_like(t, at + n) if not window else (t + window + 1).clamp(max=at + n)
+            elif prefix is not None:
+                last = last.clamp(min=at + min(prefix[b][i], n))
+            if window:
+                first = (t - window + (1 if causal else 0)).clamp(min=at)
+            out[b, at:at + n, 0], out[b, at:at + n, 1] = first, last
+            at += n
+    return out if device is None else out.to(device)
+
+
+def _mask_problem(w, score_cap, mode, layout):
+    """(descriptor, workspace bytes forward, backward), checked."""
+    desc, mask = make_desc(w, mode, layout=layout), make_mask(None, score_cap)
+    _check("loong_attn_mask_check", loong_attn_mask_check(desc, mask))
+    return desc, loong_attn_mask_workspace_size(desc, mask, 0), loong_attn_mask_workspace_size(desc, mask, 1)
+
+
+_kept_mask_problem = functools.lru_cache(maxsize=256)(_mask_problem)
+
+
+def _mask_problem_of(w, score_cap, mode, layout):
+    """Kept for a Workload, which cannot change."""
+    return (_kept_mask_problem if type(w) is Workload else _mask_problem)(w, float(score_cap), mode, layout)
+
+
+def attn_mask_fwd(w, q, k, v, key_range=None, score_cap=0.0, mode=MODE_FUSED, stream=None, layout=LAYOUT_NATURAL,
+                  res=True):
+    """attn_fwd in which query i sees the keys key_range[b, i, 0] <= j <
+    key_range[b, i, 1] (int32 [B, S, 2]; None: every key; causal workloads: of
+    those j <= i) and the scaled scores are capped, score_cap * tanh(x /
+    score_cap) (0: not).  Returns (o, lse, o_res); o_res is None when ``res`` is
+    false."""
+    desc, nbytes, _ = _mask_problem_of(w, score_cap, mode, layout)
+    for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv)):
+        _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, q.device)
+    if key_range is not None:
+        _contiguous("key_range", key_range, (w.batch, w.seqlen, 2), torch.int32, q.device)
+    where, stream = _on(q.device, stream)
+    with where:
+        o = torch.empty_like(q)
+        o_res = torch.empty_like(q) if res else None
+        lse = torch.empty((w.batch, w.hq, w.seqlen), dtype=torch.float32, device=q.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        loong_attn_mask_fwd(desc, make_mask(key_range, score_cap), q, k, v, o, lse, o_res, ws, stream)
+    return o, lse, o_res
+
+
+def attn_mask_bwd(w, q, k, v, o, lse, do, key_range=None, score_cap=0.0, o_res=None, mode=MODE_FUSED, stream=None,
+                  layout=LAYOUT_NATURAL):
+    """Gradient of attn_mask_fwd: (dq, dk, dv)."""
+    desc, _, nbytes = _mask_problem_of(w, score_cap, mode, layout)
+    for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv), ("o", o, w.hq), ("do", do, w.hq),
+                    ("o_res", o_res, w.hq)):
+        if t is not None or n != "o_res":
+            _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, q.device)
+    _contiguous("lse", lse, (w.batch, w.hq, w.seqlen), torch.float32, q.device)
+    if key_range is not None:
+        _contiguous("key_range", key_range, (w.batch, w.seqlen, 2), torch.int32, q.device)
+    where, stream = _on(q.device, stream)
+    with where:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        loong_attn_mask_bwd(desc, make_mask(key_range, score_cap), q, k, v, o, o_res, lse, do, dq, dk, dv, ws, stream)
+    return dq, dk, dv
 
 
 class QkOpts:

@@ -12,7 +12,7 @@
  *
  * Conventions shared by every entry point
  *   - Pointers named q, k, v, o, o_res, dout, dq, dk, dv, lse, ws, in, out,
- *     o_parts, lse_parts, o_out, lse_out, table, dtable, wq, wk, positions,
+ *     o_parts, lse_parts, o_out, lse_out, table, dtable, key_range, wq, wk, positions,
  *     q_out, k_out, v_out, dq_out, dk_out, dv_out, dwq, dwk are DEVICE pointers
  *     owned by the caller:
  *     memory of the current device, from cudaMalloc or managed.  A host
@@ -399,6 +399,66 @@ LOONG_API int loong_attn_bias_bwd(const loong_attn_desc* desc, const loong_rel_b
                                   const void* k, const void* v, const void* o, const void* o_res, const float* lse,
                                   const void* dout, void* dq, void* dk, void* dv, void* dtable, void* ws,
                                   size_t ws_bytes, loong_stream_t stream);
+
+/*
+ * Ring attention in which every query sees a range of keys of its own, with an
+ * optional cap of the scores: the logit of query i and key j is
+ * cap * tanh(softmax_scale * q_i.k_j / cap), over begin_i <= j < end_i.  Packed
+ * documents, prefixes that see themselves whole, windows and padding are all
+ * ranges.  The paper's attention is causal over one sequence; layers that train
+ * on packed sequences or cap their scores need these inside it.
+ *   key_range  DEVICE int32 [B][S][2], 8-byte aligned: begin and end of query i,
+ *              in natural token positions of its sequence, or NULL: every key.
+ *              Clipped to 0 .. S and, for causal descriptors, to keys j <= i.  A
+ *              query that this leaves no key gets O = 0 and LSE = -inf, adds
+ *              nothing to any gradient and gets dQ = 0.
+ *   score_cap  0: none; else 2^-20 .. 2^20 (and softmax_scale, where given,
+ *              2^-24 .. 2^24).
+ * What a key or a query holds does not matter to those that do not see each
+ * other: a value that is not finite reaches, as NaN, only what sees its row.
+ * FUSED descriptors visit the tiles that some query of a tile sees in natural
+ * order, the other modes those of every ring step.
+ */
+typedef struct {
+  const int32_t* key_range;
+  float score_cap;
+} loong_attn_mask;
+
+/*
+ * Check a descriptor and a mask without touching the GPU (key_range is not
+ * looked at): as loong_attn_check, and LOONG_ERR_INVALID_ARG for a negative or
+ * not finite cap, LOONG_ERR_UNSUPPORTED for one out of range, seqlen > 2^30 or
+ * more than 65535 sequences or query heads.
+ */
+LOONG_API int loong_attn_mask_check(const loong_attn_desc* desc, const loong_attn_mask* mask);
+
+/*
+ * Device workspace, in bytes, of loong_attn_mask_fwd (pass 0) or
+ * loong_attn_mask_bwd (pass 1); 0 for invalid arguments.  Host-only.
+ * loong_attn_workspace_size's, then 16 bytes for every 128-token query tile of a
+ * block; for the forward 1,216 words more, for the backward a byte for every
+ * query tile and head.  Each part starts on a 256-byte boundary.
+ */
+LOONG_API size_t loong_attn_mask_workspace_size(const loong_attn_desc* desc, const loong_attn_mask* mask, int pass);
+
+/*
+ * loong_attn_fwd with the mask: same arguments, layouts, modes and accuracy (a
+ * capped logit is off by at most 4e-7 of the cap more).  ws needs
+ * loong_attn_mask_workspace_size(desc, mask, 0) bytes.
+ */
+LOONG_API int loong_attn_mask_fwd(const loong_attn_desc* desc, const loong_attn_mask* mask, const void* q,
+                                  const void* k, const void* v, void* o, float* lse, void* o_res, void* ws,
+                                  size_t ws_bytes, loong_stream_t stream);
+
+/*
+ * loong_attn_bwd with the mask: dS takes the factor 1 - tanh^2 of its score.
+ * o, o_res and lse are loong_attn_mask_fwd's for the same mask.  ws needs
+ * loong_attn_mask_workspace_size(desc, mask, 1) bytes.
+ */
+LOONG_API int loong_attn_mask_bwd(const loong_attn_desc* desc, const loong_attn_mask* mask, const void* q,
+                                  const void* k, const void* v, const void* o, const void* o_res, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                  loong_stream_t stream);
 
 /*
  * What loong_qk_norm_rope_fwd does to Q and K.
