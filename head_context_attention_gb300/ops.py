@@ -40,6 +40,7 @@ EXPORTS = ("loong_version", "loong_status_string", "loong_last_cuda_error", "loo
            "loong_rel_bias_check", "loong_attn_bias_workspace_size", "loong_attn_bias_fwd", "loong_attn_bias_bwd",
            "loong_attn_mask_check", "loong_attn_mask_workspace_size", "loong_attn_mask_fwd", "loong_attn_mask_bwd",
            "loong_qk_norm_rope_fwd", "loong_qk_norm_rope_bwd_workspace_size", "loong_qk_norm_rope_bwd",
+           "loong_paged_check", "loong_paged_attn_workspace_size", "loong_paged_attn",
            "loong_attn_2d_host_workspace_size", "loong_attn_2d_host", "loong_host_alloc", "loong_host_free",
            "loong_set_timing_events", "loong_get_device_status", "loong_selftest_wait_timeout")
 NOALLOC_SCRATCH_BYTES = 32 << 20   # LOONG_NOALLOC_SCRATCH_BYTES
@@ -62,6 +63,14 @@ class LoongRelBias(ctypes.Structure):
 
 class LoongAttnMask(ctypes.Structure):
     _fields_ = [("key_range", ctypes.c_void_p), ("score_cap", ctypes.c_float)]
+
+
+class LoongPagedDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("score_cap", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
 
 
 class LoongQkOpts(ctypes.Structure):
@@ -128,6 +137,11 @@ def lib():
         L.loong_qk_norm_rope_bwd_workspace_size.restype = SZ
         L.loong_qk_norm_rope_bwd_workspace_size.argtypes = [D, QO]
         L.loong_qk_norm_rope_bwd.argtypes = [D, QO, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        PD = ctypes.POINTER(LoongPagedDesc)
+        L.loong_paged_check.argtypes = [PD]
+        L.loong_paged_attn_workspace_size.restype = SZ
+        L.loong_paged_attn_workspace_size.argtypes = [PD]
+        L.loong_paged_attn.argtypes = [PD, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         L.loong_attn_2d_host_workspace_size.restype = SZ
         L.loong_attn_2d_host_workspace_size.argtypes = [D, ctypes.c_int]
         L.loong_attn_2d_host.argtypes = [D, I32, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
@@ -388,6 +402,20 @@ def loong_qk_norm_rope_bwd(desc, opts, q, k, wq, wk, positions, dq_out, dk_out, 
         ctypes.byref(desc), ctypes.byref(opts), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(dq_out),
         _ptr(dk_out), _ptr(dv_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dwq), _ptr(dwk), _ptr(ws), _nbytes(ws),
         _stream(stream)))
+
+
+def loong_paged_check(desc):
+    return lib().loong_paged_check(ctypes.byref(desc))
+
+
+def loong_paged_attn_workspace_size(desc):
+    return lib().loong_paged_attn_workspace_size(ctypes.byref(desc))
+
+
+def loong_paged_attn(desc, q, k, v, k_pages, v_pages, table, lens, starts, o, lse, ws, stream=None):
+    return _check("loong_paged_attn", lib().loong_paged_attn(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens),
+        _ptr(starts), _ptr(o), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def loong_attn_2d_host_workspace_size(desc, pass_):
@@ -816,3 +844,69 @@ def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions
         ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n and (dwq is not None or dwk is not None) else None
         loong_qk_norm_rope_bwd(desc, o, q, k, wq, wk, positions, dq, dk, dv, *into, dwq, dwk, ws, stream)
     return (*into, dwq, dwk)
+
+
+def _row_stride(name, t, heads, d):
+    """Elements from row to row of [tokens, heads, d] with contiguous heads; an
+    expanded view repeats one row's memory and is not taken."""
+    ss, sh, sd = t.stride()
+    if t.shape[0] <= 1:
+        ss = heads * d
+    if (sd != 1 and d > 1) or (sh != d and heads > 1) or ss < heads * d:
+        raise ValueError(f"{name} must have contiguous heads and rows that do not overlap, not strides {t.stride()}")
+    return ss
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_problem(*fields):
+    """(descriptor, workspace bytes), checked."""
+    desc = LoongPagedDesc(*fields)
+    _check("loong_paged_check", loong_paged_check(desc))
+    return desc, loong_paged_attn_workspace_size(desc)
+
+
+def paged_attn(q, k_pages, v_pages, table, lens, starts, k=None, v=None, window=0, score_cap=0.0, scale=0.0, out=None,
+               stream=None):
+    """Attention of new tokens over a paged cache: q bf16 [tokens, hq, d], the
+    new tokens of sequence b in rows starts[b] .. starts[b + 1] - 1 (int32 [batch
+    + 1]); k_pages, v_pages bf16 [num_pages, page_size, hkv, d]; table int32
+    [batch, max_pages]; lens int32 [batch], lengths with the new tokens.  With k,
+    v (bf16 [tokens, hkv, d]) the new tokens' keys and values are written into
+    their pages first.  q, k and v may be slices of one fused projection.
+    ``window``: a token sees that many keys, itself included (0: all before it);
+    ``score_cap`` as in attn_mask_fwd.  ``out``: (o, lse) to write, whose rows
+    behind the last sequence stay as they are.  Returns (o, lse), lse fp32 [hq,
+    tokens]."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("q must be a tensor [tokens, hq, d], the pages [num_pages, page_size, hkv, d]")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a tensor [batch, max_pages]")
+    if (k is None) != (v is None):
+        raise ValueError("k and v belong together: give both or neither")
+    tokens, hq, d = q.shape
+    num_pages, page, hkv, _ = k_pages.shape
+    batch, max_pages = table.shape
+    dev, bf16 = q.device, torch.bfloat16
+    _same("q", q, (tokens, hq, d), bf16, dev)
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _contiguous(n, t, (num_pages, page, hkv, d), bf16, dev)
+    _contiguous("table", table, (batch, max_pages), torch.int32, dev)
+    _contiguous("lens", lens, (batch,), torch.int32, dev)
+    _contiguous("starts", starts, (batch + 1,), torch.int32, dev)
+    strides = [_row_stride("q", q, hq, d), 0, 0]
+    if k is not None:
+        for i, (n, t) in enumerate((("k", k), ("v", v))):
+            _same(n, t, (tokens, hkv, d), bf16, dev)
+            strides[1 + i] = _row_stride(n, t, hkv, d)
+    desc, nbytes = _paged_problem(batch, tokens, hq, hkv, d, page, num_pages, max_pages, int(window), float(scale),
+                                  float(score_cap), *strides)
+    if out is not None:
+        _contiguous("out[0]", out[0], (tokens, hq, d), bf16, dev)
+        _contiguous("out[1]", out[1], (hq, tokens), torch.float32, dev)
+    where, stream = _on(dev, stream)
+    with where:
+        if out is None:
+            out = torch.empty((tokens, hq, d), dtype=bf16, device=dev), torch.empty((hq, tokens), device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        loong_paged_attn(desc, q, k, v, k_pages, v_pages, table, lens, starts, out[0], out[1], ws, stream)
+    return tuple(out)

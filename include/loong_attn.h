@@ -540,6 +540,75 @@ LOONG_API int loong_qk_norm_rope_bwd(const loong_attn_desc* desc, const loong_qk
                                      loong_stream_t stream);
 
 /*
+ * Attention of new tokens over a cache of pages, after writing their keys and
+ * values into it: what a trained layer runs when it answers, from one new token
+ * of many sequences to a chunk of a long prompt.  The paper trains only; query
+ * heads, scores, cap and window are the attention's above.
+ *   batch       sequences, 1 .. 4096.
+ *   tokens      rows of q (and k, v): sequence b's new tokens are rows
+ *               starts[b] .. starts[b + 1] - 1.  Rows from starts[batch] on are
+ *               not looked at and their outputs left as they are.
+ *   hq, hkv     hq % hkv == 0, at most 128 query heads to a kv head.
+ *   head_dim    64 or 128.
+ *   page_size   tokens of a page, a power of two from 8 to 1024.
+ *   num_pages   pages of the pool; (num_pages + 1) * page_size <= 2^30.
+ *   max_pages   pages of a row of the table; max_pages * page_size <= 2^30.
+ *   window      0, or the number of keys that a token sees, itself included.
+ *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
+ *   score_cap   0: none; else as in loong_attn_mask.
+ *   q/k/v_stride  elements from one token's row to the next, 0 = contiguous
+ *               (heads * head_dim), else at least that, a multiple of 8 and at
+ *               most 2^31; a row's heads are contiguous.
+ */
+typedef struct {
+  int32_t batch, tokens, hq, hkv, head_dim;
+  int32_t page_size, num_pages, max_pages;
+  int32_t window;
+  float softmax_scale, score_cap;
+  int64_t q_stride, k_stride, v_stride;
+} loong_paged_desc;
+
+/*
+ * Check a paged descriptor without touching the GPU: LOONG_OK,
+ * LOONG_ERR_INVALID_ARG or LOONG_ERR_UNSUPPORTED (ranges above; work whose units
+ * of 128 rows by 128 keys may pass 2^31).
+ */
+LOONG_API int loong_paged_check(const loong_paged_desc* desc);
+
+/* Device workspace of loong_paged_attn, in bytes; 0 for an invalid descriptor.  Host-only. */
+LOONG_API size_t loong_paged_attn_workspace_size(const loong_paged_desc* desc);
+
+/*
+ *   q           bf16 [tokens][hq][head_dim], token-strided.
+ *   k, v        bf16 [tokens][hkv][head_dim], token-strided: written to the new
+ *               tokens' places before anything is read; both NULL: they are there
+ *               already.
+ *   k_pages,    bf16 [num_pages][page_size][hkv][head_dim], contiguous.  Places that
+ *   v_pages     no sequence uses may hold anything.
+ *   table       int32 [batch][max_pages]: sequence b's key j is row j % page_size of
+ *               page table[b][j / page_size].  Entries past a sequence's length, or
+ *               wholly before what its new tokens see, are not read.
+ *   lens        int32 [batch]: lengths with the new tokens.  New token t of a
+ *               sequence (t = 0 .. n - 1) stands at position lens[b] - n + t and sees
+ *               the keys up to its own.
+ *   starts      int32 [batch + 1], starting anywhere from 0, not falling.
+ *   o, lse      bf16 [tokens][hq][head_dim] and fp32 [hq][tokens] (natural log of
+ *               the softmax denominator), contiguous.
+ * The arrays are read on the device, so a captured call may be replayed on other
+ * lengths, tables and starts.  Pages that two new tokens share (the same place
+ * written twice) hold either's row.  A page outside the pool is read as zeros and
+ * not written, lengths and starts out of range are cut (tokens that stand before
+ * position 0 see nothing: O = 0, LSE = -inf), and loong_get_device_status then
+ * reports LOONG_ERR_DEVICE_CHECK.  No work with tokens == 0.
+ * Results do not depend on the order in which blocks run.  P enters the P V
+ * product as bf16, its sum takes the rounded values; all else is fp32.
+ */
+LOONG_API int loong_paged_attn(const loong_paged_desc* desc, const void* q, const void* k, const void* v,
+                               void* k_pages, void* v_pages, const int32_t* table, const int32_t* lens,
+                               const int32_t* starts, void* o, float* lse, void* ws, size_t ws_bytes,
+                               loong_stream_t stream);
+
+/*
  * Device workspace, in bytes, of loong_attn_2d_host for `desc`: pass 0 runs
  * the forward alone, pass 1 the forward and the backward; 0 for an invalid
  * descriptor.  Host-only.  It holds two sets of natural-layout inputs (the

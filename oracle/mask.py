@@ -54,7 +54,7 @@ def forward_backward(q, k, v, do, see, scale, cap=0.0, terms=False):
             t = np.tanh(x / cap)
             x, slope = cap * t, 1 - t * t
         x = np.where(see, x, -np.inf)
-        m = np.where(some, x.max(axis=1, keepdims=True), 0)
+        m = np.where(some, x.max(axis=1, keepdims=True, initial=-np.inf), 0)
         e = np.exp(x - m)
         l = e.sum(axis=1, keepdims=True)
         p = e / np.where(some, l, 1)
