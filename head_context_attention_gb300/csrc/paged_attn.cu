@@ -28,8 +28,9 @@
 // in attn_fwd.cu, S = Q K^T goes to one of NSB score buffers in tensor memory, P
 // overwrites it, O += P V; the softmax forms P against the running maximum and only
 // looks for a tile's maximum when a row's sum passes 2^8 of it.  P and V are bf16,
-// V being read where it lies; l is the sum of the rounded P, so that a row that one
-// key dominates has its V back to O's own rounding.
+// V being read where it lies; O is divided by the sum of the rounded P, so that a row
+// that one key dominates has its V back to O's own rounding, and the LSE comes from
+// the sum before rounding.
 // What a masked place of a tile holds (rows of the page behind the sequence, keys
 // that are yet to come) does not matter: its scores are replaced, and where a tile is
 // not seen whole, rows of V that are not finite are cleared in shared memory first
@@ -102,7 +103,7 @@ struct PagedArgs {
   int* count;          // groups
   unsigned* tickets;   // [max_groups * hkv * softmax warps]
   float* part_o;       // [blocks * 2][SLOTS * 128][D]
-  float2* part_ml;     // [blocks * 2][SLOTS * 128]: maximum (log2 units), sum
+  float4* part_ml;     // [blocks * 2][SLOTS * 128]: maximum (log2 units), sum, sum of the rounded P, -
   __nv_bfloat16* o;    // [tokens][hq][D]
   float* lse;          // [hq][tokens]
   unsigned* err;
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
         see = make_int2(a.window ? max(pos - a.window + 1, 0) : 0, max(pos + 1, 0));
       }
       const bool some = quarter * 32 < here;  // the warp has rows
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f, r_run = 0.f;  // r: the sum of the rounded P
       for (int j = 0; j < n; ++j) {
         const int i = J + SLOTS * j + h, buf = i % NSB;
         const uint32_t tS = tbase + t_lane + C::S_COL(buf);
@@ -612,28 +613,33 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
           };
           load_s();
           uint32_t pk[2][32];
-          // P = exp2(s * scale * log2e - ref), rounded; returns the row's sum of it
+          // P = exp2(s * scale * log2e - ref), rounded; returns the row's sums of it
           auto form_p = [&](float ref) {
             const float2 sl2v = make_float2(sl2, sl2), nref = make_float2(-ref, -ref);
-            float2 sum = make_float2(0.f, 0.f);
+            float2 sum = make_float2(0.f, 0.f), rsum = sum;
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 x = __ffma2_rn(
                     make_float2(__uint_as_float(sr[cb][e]), __uint_as_float(sr[cb][e + 1])), sl2v, nref);
-                const uint32_t p = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
-                sum = __fadd2_rn(sum, make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)));
+                const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                const uint32_t p = pack_bf16(y.x, y.y);
+                sum = __fadd2_rn(sum, y);
+                rsum = __fadd2_rn(rsum, make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)));
                 pk[cb >> 1][(cb & 1) * 16 + (e >> 1)] = p;
               }
-            return sum.x + sum.y;
+            return make_float2(sum.x + sum.y, rsum.x + rsum.y);
           };
           bool full = j == 0, over = false;
           if (!full) {
-            const float ts = form_p(m_run);
-            over = !(ts < kSumBound);
+            const float2 ts = form_p(m_run);
+            over = !(ts.x < kSumBound);
             full = __any_sync(0xffffffffu, over);
-            if (!full) l_run += ts;
+            if (!full) {
+              l_run += ts.x;
+              r_run += ts.y;
+            }
           }
           if (full) {
             if (j > 0) load_s();
@@ -655,6 +661,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
               tc_fence_after();
               const float f = rescale ? fast_exp2(m_run - m_new) : 1.f;
               l_run *= f;
+              r_run *= f;
 #pragma unroll 1
               for (int cb = 0; cb < D / 32; ++cb) {
                 uint32_t orow[32];
@@ -666,7 +673,9 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
               }
               if (rescale) m_run = m_new;
             }
-            l_run += form_p(m_run == -INFINITY ? 0.f : m_run);
+            const float2 ts = form_p(m_run == -INFINITY ? 0.f : m_run);
+            l_run += ts.x;
+            r_run += ts.y;
           }
           tmem_st32(tS, pk[0]);
           tmem_st32(tS + 32, pk[1]);
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
       // ------------------------------------------------------- the item's rows
       const int tok = sg.tok + h * a.per_slot + tl, head = sg.kvh * a.G + row - tl * a.G;
       if (sg.part < 0) {
-        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+        const float inv = r_run != 0.f ? 1.f / r_run : 0.f;
         __nv_bfloat16* orow = a.o + (static_cast<int64_t>(tok) * a.hq + head) * D;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -721,7 +730,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
             __stcg(dst + v4, make_uint4(ov[v4 * 4], ov[v4 * 4 + 1], ov[v4 * 4 + 2], ov[v4 * 4 + 3]));
         }
       }
-      if (valid) __stcg(a.part_ml + part_row, make_float2(m_run, l_run));
+      if (valid) __stcg(a.part_ml + part_row, make_float4(m_run, l_run, r_run, 0.f));
       tc_fence_before();
       __threadfence();
       __syncwarp();
@@ -748,16 +757,17 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
         for (int o = LANES / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (!live) continue;  // no lane exchanges anything from here on
         const float ref = mx == -INFINITY ? 0.f : mx;
-        float l = 0.f;
+        float l = 0.f, rl = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int p = 0; p < sg.parts; ++p) {
           const int64_t at = row_of(p, r);
-          const float2 ml = __ldcg(a.part_ml + at);
+          const float4 ml = __ldcg(a.part_ml + at);
           const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + part4);
           if (ml.y != 0.f) {  // a part without keys of the row adds nothing
             const float w = fast_exp2(ml.x - ref);
             l = fmaf(w, ml.y, l);
+            rl = fmaf(w, ml.z, rl);
             acc.x = fmaf(w, x.x, acc.x);
             acc.y = fmaf(w, x.y, acc.y);
             acc.z = fmaf(w, x.z, acc.z);
@@ -767,7 +777,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
         const int rr = quarter * 32 + r, t2 = rr / a.G;
         const int64_t tok2 = sg.tok + h * a.per_slot + t2;
         const int head2 = sg.kvh * a.G + rr - t2 * a.G;
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const float inv = rl != 0.f ? 1.f / rl : 0.f;
         reinterpret_cast<uint2*>(a.o + (tok2 * a.hq + head2) * D)[part4] =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
         if (part4 == 0) a.lse[static_cast<int64_t>(head2) * a.tokens + tok2] = l != 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
@@ -867,7 +877,7 @@ PagedWs paged_ws(const loong_paged_desc& d) {
   w.count = take(4);
   w.ticket = take(4 * static_cast<size_t>(w.tickets));
   const size_t rows = static_cast<size_t>(w.blocks) * 2 * w.slots * kTile;
-  w.part_ml = take(rows * sizeof(float2));
+  w.part_ml = take(rows * sizeof(float4));
   w.part_o = take(rows * d.head_dim * 4);
   w.total = at;
   return w;
@@ -976,7 +986,7 @@ int loong_paged_attn(const loong_paged_desc* d, const void* q, const void* k, co
   a.count = reinterpret_cast<int*>(base + w.count);
   a.tickets = reinterpret_cast<unsigned*>(base + w.ticket);
   a.part_o = reinterpret_cast<float*>(base + w.part_o);
-  a.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
+  a.part_ml = reinterpret_cast<float4*>(base + w.part_ml);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   if (!(a.err = device_error_word())) return LOONG_ERR_CUDA;

@@ -601,7 +601,8 @@ LOONG_API size_t loong_paged_attn_workspace_size(const loong_paged_desc* desc);
  * position 0 see nothing: O = 0, LSE = -inf), and loong_get_device_status then
  * reports LOONG_ERR_DEVICE_CHECK.  No work with tokens == 0.
  * Results do not depend on the order in which blocks run.  P enters the P V
- * product as bf16, its sum takes the rounded values; all else is fp32.
+ * product as bf16 and O is divided by the sum of the rounded values; all else is
+ * fp32.
  */
 LOONG_API int loong_paged_attn(const loong_paged_desc* desc, const void* q, const void* k, const void* v,
                                void* k_pages, void* v_pages, const int32_t* table, const int32_t* lens,

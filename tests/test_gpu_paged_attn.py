@@ -2,9 +2,10 @@
 
 Tolerances, per element (half steps: bf16 2^-8 of the value, fp32 2^-24): a
 logit's error dx and the factor 1 + e of every P as in test_gpu_mask_attn.  P is
-rounded to bf16 (2^-8), its sum takes the rounded values: O is off by at most
-2 (2^-8 + e) of A = P |V| (numerator and denominator), sums in fp32 2^-16, O's own
-rounding 2^-8 |O|; LSE: the sum's 2^-8, e, and 2^-22 |LSE|.
+rounded to bf16 (2^-8), and O divided by the sum of the rounded values: O is off by
+at most 2 (2^-8 + e) of A = P |V| (numerator and denominator), sums in fp32 2^-16,
+O's own rounding 2^-8 |O|; the LSE's sum is of the values before rounding: e + 2^-22
+(1 + |LSE|).
 """
 import numpy as np
 import pytest
@@ -97,7 +98,7 @@ class _Setup:
             _within(f"O of sequence {b}", o[at:at + new], t["o"],
                     2.0 ** -8 * np.abs(t["o"]) + (2 * (2.0 ** -8 + e) + 2.0 ** -16) * t["abs_o"])
             _within(f"LSE of sequence {b}", lse[:, at:at + new], t["lse"],
-                    2.0 ** -8 + e + 2.0 ** -22 * np.abs(t["lse"]))
+                    e + 2.0 ** -22 * (1 + np.abs(t["lse"])))
             at += new
 
 
