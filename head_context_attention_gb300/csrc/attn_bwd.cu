@@ -158,7 +158,7 @@ struct BwdPiece {
 // rows of K that are not are cleared in shared memory by the compute warps, rows of Q
 // and dO by the producer, in the tiles that the launch before marked.  Instead the
 // row's own P is NaN, for those that see it.
-enum BwdVariant { kBwdPlain, kBwdBias, kBwdMask };
+enum BwdVariant { kBwdPlain, kBwdBias, kBwdMask, kBwdCap };
 
 // The query tiles, in natural order, that see a block's keys [k0, k1), a word of 32
 // at a time, and the heads of the group for each.
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const __grid_constant__ CUtensorMap tmDQ, const BwdArgs a) {
   using C = BwdCfg<D>;
-  constexpr bool BIAS = VARIANT == kBwdBias, MASK = VARIANT == kBwdMask;
+  constexpr bool BIAS = VARIANT == kBwdBias, CAP = VARIANT == kBwdCap, MASK = VARIANT == kBwdMask || CAP;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // uniform over the CTA; the swizzled tiles need it
     if (threadIdx.x == 0) atomicOr(a.err, kErrSmemAlign);
@@ -785,11 +785,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           const int kq = k0 + quarter * 32;
           seen = transpose_bits(low_bits(min(r.y - kq, klen - quarter * 32)) & ~low_bits(r.x - kq), lane);
         }
-        if (a.mask.cap_inv > 0.f) {
+        if constexpr (CAP) {
           uint32_t sv[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[e] = __float_as_uint(pv[0][e]);
-          cap_scores(sv, a.mask.cap_inv);
+          cap_scores(sv, a.mask.cap);
 #pragma unroll
           for (int e = 0; e < 32; ++e) pv[0][e] = __uint_as_float(sv[e]);
         }
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         const int cbase = grp * C::GW + ch * 32;  // first query column of the chunk
         uint32_t pk[16];
         if constexpr (MASK) {
-          const bool capped = a.mask.cap_inv > 0.f;
+          const float inv = a.mask.cap.inv;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 l4 = *reinterpret_cast<const float4*>(lse_row + cbase + e);
@@ -819,8 +819,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
               }
               pk[(e + u) / 2] = pack_bf16(x, y);
               // from here on P with the cap's derivative, for dS
-              pv[0][e + u] = capped && x != 0.f ? x * fmaf(-t0, t0, 1.f) : x;
-              pv[0][e + u + 1] = capped && y != 0.f ? y * fmaf(-t1, t1, 1.f) : y;
+              auto slope = [&](float s) {
+                const float t = s * inv;
+                return fmaf(-t, t, 1.f);
+              };
+              pv[0][e + u] = CAP && x != 0.f ? x * slope(t0) : x;
+              pv[0][e + u + 1] = CAP && y != 0.f ? y * slope(t1) : y;
             }
           }
         } else if (unmasked) {
@@ -1158,8 +1162,8 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   a.G = d.hq / d.hkv;
   a.ring = ring_geom(d);
   a.scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
-  a.mask = VARIANT == kBwdMask ? *mask : MaskView{};
-  a.scale_log2 = (a.mask.cap_inv > 0.f ? a.scale / a.mask.cap_inv : a.scale) * kLog2e;
+  a.mask = VARIANT == kBwdMask || VARIANT == kBwdCap ? *mask : MaskView{};
+  a.scale_log2 = a.scale * kLog2e;
   a.lse2 = stats;
   a.blk_pad = stat_block_pad(a.ring.blk);
   a.stat_len = static_cast<int>(stat_row_len(a.ring));
@@ -1264,6 +1268,9 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
   if (!bias && !mask && (st = launch_bwd_rowstats(d, o, o_res, dout, lse, dvec, stream)) != LOONG_OK) return st;
   st = bias   ? launch_bwd_v<kBwdBias>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, bias,
                                        dbias_part, nullptr)
+       : mask && mask->cap.inv > 0.f
+           ? launch_bwd_v<kBwdCap>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv, nullptr,
+                                   nullptr, mask)
        : mask ? launch_bwd_v<kBwdMask>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv,
                                        nullptr, nullptr, mask)
               : launch_bwd_v<kBwdPlain>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv,

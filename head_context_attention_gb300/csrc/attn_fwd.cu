@@ -158,7 +158,7 @@ constexpr float kMaxMiddle = 32.0f;  // log2 units
 // there was such a value (v_amax[1]) the scores of its key become NaN for the rows
 // that see it.
 // Pairs of heads and of tiles are formed as with a bias.
-enum FwdVariant { kFwdPlain, kFwdBias, kFwdMask };
+enum FwdVariant { kFwdPlain, kFwdBias, kFwdMask, kFwdCap };
 
 struct FwdPiece {
   float lo, hi;  // the difference before and, kPieceStep, from the boundary on
@@ -166,6 +166,8 @@ struct FwdPiece {
   int step;      // kPieceStep: row r of the piece has passed the boundary up to column r + step
 };
 
+//
+// With a cap the softmax warps cap a tile where it lies in tensor memory first (softcap.cuh).
 //
 // SLOTS = 1 (with BIAS or MASK): one head's query tile per block, where even such blocks do
 // not fill the SMs.  The second slot's warps idle; the scores of the next tile, in
@@ -175,7 +177,8 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
     ring_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
   using C = FwdCfg<D>;
-  constexpr bool BIAS = VARIANT == kFwdBias, MASK = VARIANT == kFwdMask, PAIRS = VARIANT != kFwdPlain;
+  constexpr bool BIAS = VARIANT == kFwdBias, CAP = VARIANT == kFwdCap, MASK = VARIANT == kFwdMask || CAP;
+  constexpr bool PAIRS = VARIANT != kFwdPlain;
   constexpr int NSB = fwd_score_buffers(D, SLOTS);
   static_assert(NSB <= 2 * SLOTS, "a tile's scores prove P V of the tile two back");
   extern __shared__ uint8_t smem_raw[];
@@ -579,25 +582,32 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
           return BIAS ? g.causal && walk.bk == bq && walk.kt >= (h ? qi : qi0) : walk.diag();
       }();
       const int k0 = walk.k0();
-      // MASK: NaN for the keys whose V holds values that are not finite
-      auto poison = [&](uint32_t(&s)[4][32]) {
+      // MASK: the columns that this row sees, and whether the warp's rows see all
+      const int see_lo = MASK ? see.x - k0 : 0, see_hi = MASK ? min(see.y - k0, klen) : 0;
+      const bool masked = MASK && __any_sync(0xffffffffu, see_lo > 0 || see_hi < kTile);
+      // columns 32 cb .. of the tile: NaN for keys whose V holds values that are not finite
+      auto poison = [&](uint32_t(&s)[32], int cb) {
         if constexpr (MASK) {
-#pragma unroll
-          for (int cb = 0; cb < 4; ++cb) {
-            bool bad = false;  // of the lane's key
-            const int key = cb * 32 + lane;
-            if (key < klen) {
-              const uint4* vv = reinterpret_cast<const uint4*>(a.mask.v + a.lay.vec(b, k0 + key, kvh, a.hkv) * D);
-              unsigned m = 0;
-              for (int i = 0; i < D / 8; ++i) v16_finite(__ldg(vv + i), m);
-              bad = m != 0;
-            }
-            const unsigned keys = __ballot_sync(0xffffffffu, bad);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (keys >> i & 1) s[cb][i] = 0x7fffffffu;
+          bool bad = false;  // of the lane's key
+          const int key = cb * 32 + lane;
+          if (key < klen) {
+            const uint4* vv = reinterpret_cast<const uint4*>(a.mask.v + a.lay.vec(b, k0 + key, kvh, a.hkv) * D);
+            unsigned m = 0;
+            for (int i = 0; i < D / 8; ++i) v16_finite(__ldg(vv + i), m);
+            bad = m != 0;
           }
+          const unsigned keys = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (keys >> i & 1) s[i] = 0x7fffffffu;
         }
+      };
+      // and -inf for those that the row does not see
+      auto mask_columns = [&](uint32_t(&s)[32], int cb) {
+        const uint32_t bits = low_bits(see_hi - cb * 32) & ~low_bits(see_lo - cb * 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(bits >> i & 1)) s[i] = __float_as_uint(-INFINITY);
       };
       // the tile's scores, masked columns at -inf (read again by the full path)
       auto load_s = [&]() {
@@ -605,20 +615,13 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
         for (int cb = 0; cb < 4; ++cb) tmem_ld32(tS + cb * 32, sr[cb]);
         tmem_wait_ld();
         if constexpr (MASK) {
-          if (a.mask.cap_inv > 0.f) {
+          if (v_bad) {
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb) cap_scores(sr[cb], a.mask.cap_inv);
+            for (int cb = 0; cb < 4; ++cb) poison(sr[cb], cb);
           }
-          if (v_bad) poison(sr);
-          const int lo = see.x - k0, hi = min(see.y - k0, klen);  // columns that the row sees
-          if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
+          if (masked) {
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb) {
-              const uint32_t bits = low_bits(hi - cb * 32) & ~low_bits(lo - cb * 32);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(bits >> i & 1)) sr[cb][i] = __float_as_uint(-INFINITY);
-            }
+            for (int cb = 0; cb < 4; ++cb) mask_columns(sr[cb], cb);
           }
           return;
         }
@@ -632,6 +635,7 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
               if (cb * 32 + i > lim) sr[cb][i] = __float_as_uint(-INFINITY);
         }
       };
+      if constexpr (CAP) cap_tile(tS, a.mask.cap);
       load_s();
       // P = exp2(s*scale*log2e - ref + bias) for the whole tile, with the
       // columns in pairs on the paired fp32 pipe; returns this row's sum of P
@@ -832,7 +836,7 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
                  float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin, int rank_end,
                  const BiasView* bias, const MaskView* mask) {
   using C = FwdCfg<D>;
-  constexpr bool BIAS = VARIANT == kFwdBias, MASK = VARIANT == kFwdMask;
+  constexpr bool BIAS = VARIANT == kFwdBias, MASK = VARIANT == kFwdMask || VARIANT == kFwdCap;
   const Layout lay = layout_of(d);
   const int64_t rows = lay.view_rows(d.batch);
   CUtensorMap mq, mk, mv;
@@ -858,7 +862,7 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   a.kv_held = 0;
   const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
   a.mask = MASK ? *mask : MaskView{};
-  a.scale_log2 = (a.mask.cap_inv > 0.f ? scale / a.mask.cap_inv : scale) * kLog2e;
+  a.scale_log2 = scale * kLog2e;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_res = static_cast<__nv_bfloat16*>(sc.o_res);
   a.lse = lse;
@@ -957,6 +961,8 @@ int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const voi
                const BiasView* bias, const MaskView* mask) {
   if (rank_end < 0) rank_end = d.cp;
   if (bias) return launch_fwd_v<kFwdBias>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, nullptr);
+  if (mask && mask->cap.inv > 0.f)
+    return launch_fwd_v<kFwdCap>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr, mask);
   if (mask) return launch_fwd_v<kFwdMask>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, nullptr, mask);
   const int st = launch_v_to_f16(v, sc.v16, sc.v_amax, d.batch * d.seqlen * d.hkv * d.head_dim, stream);
   if (st != LOONG_OK) return st;

@@ -13,6 +13,7 @@
 
 #include "../../include/loong_attn.h"
 #include "ring.cuh"
+#include "softcap.cuh"
 
 namespace loong {
 
@@ -134,7 +135,7 @@ struct MaskView {
   const int4* tiles = nullptr;
   const uint8_t* bad = nullptr;  // backward: [B][hq][nblocks * ntile], tiles with rows to clear
   const __nv_bfloat16* v = nullptr;  // forward: V as given
-  float cap_inv = 0.f;           // softmax scale / cap, 0: no cap
+  ScoreCap cap;
 };
 
 // The keys [x, y) that query t of sequence b sees; (0, 0) where none.

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) mask_bwd_prep_kernel(const __grid_co
         float4* dq = reinterpret_cast<float4*>(a.dq_acc + at);
         dq[0] = dq[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         v16_finite(gv, bad);
-        if (a.tiles.m.cap_inv > 0.f) v16_finite(__ldg(reinterpret_cast<const uint4*>(a.q + at)), bad);
+        if (a.tiles.m.cap.inv > 0.f) v16_finite(__ldg(reinterpret_cast<const uint4*>(a.q + at)), bad);
         const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
         const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&gv);
         const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&rv);
@@ -213,7 +213,7 @@ TileArgs tile_args(const loong_attn_desc& d, const loong_attn_mask& m, const Mas
   a.m.range = reinterpret_cast<const int2*>(m.key_range);
   a.m.tiles = reinterpret_cast<const int4*>(base + w.tiles);
   const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.head_dim));
-  a.m.cap_inv = m.score_cap > 0.f ? scale / m.score_cap : 0.f;
+  a.m.cap = make_score_cap(scale, m.score_cap);
   a.g = ring_geom(d);
   a.S = static_cast<int>(d.seqlen);
   a.count = w.count;

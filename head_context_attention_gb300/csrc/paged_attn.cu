@@ -39,6 +39,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fwd_jobs.h"
 #include "internal.h"
@@ -94,7 +95,8 @@ struct PagedArgs {
   int batch, tokens, hq, hkv, G, per_slot;  // per_slot: tokens in 128 rows
   int page_log2, num_pages, max_pages, window;
   int max_groups;
-  float scale_log2, cap_inv;
+  float scale_log2;
+  ScoreCap cap;
   const int* table;    // [batch][max_pages]
   const int* lens;     // [batch]
   const int* starts;   // [batch + 1]
@@ -269,7 +271,7 @@ struct Segment {
   int parts, first_part, first_block, item;
 };
 
-template <int D, int SLOTS>
+template <int D, int SLOTS, bool CAP>
 __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedArgs a) {
@@ -589,60 +591,51 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) bad[cb] |= *reinterpret_cast<volatile unsigned*>(&bad_v[st][cb]);
           }
-          uint32_t sr[4][32];
+          // of columns 32 cb .. of the tile: -inf for keys that are not seen, NaN for
+          // those whose V holds values that are not finite
+          auto mask_columns = [&](uint32_t(&s)[32], int cb, uint32_t nan) {
+            const uint32_t bits = low_bits(hi - cb * 32) & ~low_bits(lo - cb * 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (nan >> e & 1) s[e] = 0x7fffffffu;
+              if (!(bits >> e & 1)) s[e] = __float_as_uint(-INFINITY);
+            }
+          };
+          uint32_t sr[4][32], pk[2][32];
           // the scores, masked columns at -inf
           auto load_s = [&]() {
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) tmem_ld32(tS + cb * 32, sr[cb]);
             tmem_wait_ld();
-            if (a.cap_inv > 0.f) {
-#pragma unroll
-              for (int cb = 0; cb < 4; ++cb) cap_scores(sr[cb], a.cap_inv);
-            }
             if (part) {
 #pragma unroll
-              for (int cb = 0; cb < 4; ++cb) {
-                const uint32_t bits = low_bits(hi - cb * 32) & ~low_bits(lo - cb * 32), nan = bad[cb];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  if (nan >> e & 1) sr[cb][e] = 0x7fffffffu;
-                  if (!(bits >> e & 1)) sr[cb][e] = __float_as_uint(-INFINITY);
-                }
-              }
+              for (int cb = 0; cb < 4; ++cb) mask_columns(sr[cb], cb, bad[cb]);
             }
           };
-          load_s();
-          uint32_t pk[2][32];
-          // P = exp2(s * scale * log2e - ref), rounded; returns the row's sums of it
+          // a pair of P rounded and packed, and added to the row's sums
+          float2 sum = make_float2(0.f, 0.f), rsum = sum;
+          auto pack = [&](float p0, float p1) {
+            const uint32_t p = pack_bf16(p0, p1);
+            sum = __fadd2_rn(sum, make_float2(p0, p1));
+            rsum = __fadd2_rn(rsum, make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)));
+            return p;
+          };
+          // P = exp2(s * scale * log2e - ref); the row's sums of it
           auto form_p = [&](float ref) {
             const float2 sl2v = make_float2(sl2, sl2), nref = make_float2(-ref, -ref);
-            float2 sum = make_float2(0.f, 0.f), rsum = sum;
+            sum = rsum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb)
+            for (int cb = 0; cb < 4; ++cb) {
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 x = __ffma2_rn(
                     make_float2(__uint_as_float(sr[cb][e]), __uint_as_float(sr[cb][e + 1])), sl2v, nref);
-                const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                const uint32_t p = pack_bf16(y.x, y.y);
-                sum = __fadd2_rn(sum, y);
-                rsum = __fadd2_rn(rsum, make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)));
-                pk[cb >> 1][(cb & 1) * 16 + (e >> 1)] = p;
+                pk[cb >> 1][(cb & 1) * 16 + (e >> 1)] = pack(fast_exp2(x.x), fast_exp2(x.y));
               }
+            }
             return make_float2(sum.x + sum.y, rsum.x + rsum.y);
           };
-          bool full = j == 0, over = false;
-          if (!full) {
-            const float2 ts = form_p(m_run);
-            over = !(ts.x < kSumBound);
-            full = __any_sync(0xffffffffu, over);
-            if (!full) {
-              l_run += ts.x;
-              r_run += ts.y;
-            }
-          }
-          if (full) {
-            if (j > 0) load_s();
+          auto tile_max = [&]() {  // log2 units
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb)
@@ -651,13 +644,17 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
                 mx0 = fmax3(mx0, __uint_as_float(sr[cb][e]), __uint_as_float(sr[cb][e + 1]));
                 mx1 = fmax3(mx1, __uint_as_float(sr[cb][e + 2]), __uint_as_float(sr[cb][e + 3]));
               }
-            const float m_new = fmaxf(m_run, fmaxf(mx0, mx1) * sl2);
+            return fmaxf(mx0, mx1) * sl2;
+          };
+          // the running maximum takes the tile's in; false: a wait gave up
+          auto new_reference = [&](float m_tile, bool over) {
+            const float m_new = fmaxf(m_run, m_tile);
             const bool rescale = j > 0 && m_new > m_run + (over ? 0.f : kRescaleThreshold);
             if (j == 0) m_run = m_new;
             if (__any_sync(0xffffffffu, rescale)) {
               // O_h holds the tile before's P V: with as many buffers as slots these scores
               // prove it, else its completion is waited for (fwd_jobs.h)
-              if (NSB > SLOTS && !(ok = warp_wait(&pv_done[h], (it + j - 1) & 1))) break;
+              if (NSB > SLOTS && !warp_wait(&pv_done[h], (it + j - 1) & 1)) return false;
               tc_fence_after();
               const float f = rescale ? fast_exp2(m_run - m_new) : 1.f;
               l_run *= f;
@@ -673,10 +670,26 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
               }
               if (rescale) m_run = m_new;
             }
-            const float2 ts = form_p(m_run == -INFINITY ? 0.f : m_run);
-            l_run += ts.x;
-            r_run += ts.y;
+            return true;
+          };
+          if constexpr (CAP) cap_tile(tS, a.cap);
+          // against the running maximum, and where some row's sum reaches the bound (or j is
+          // 0) with the tile's own: two turns of one loop, a copy of the code less
+          bool over = false;
+#pragma unroll 1
+          for (int turn = j == 0 ? 1 : 0; turn < 2; ++turn) {
+            load_s();
+            if (turn == 1 && !(ok = new_reference(tile_max(), over))) break;
+            // the first turn: against a row's -inf so far, NaN or more than the bound
+            const float2 ts = form_p(turn == 1 && m_run == -INFINITY ? 0.f : m_run);
+            over = !(ts.x < kSumBound);
+            if (turn == 1 || !__any_sync(0xffffffffu, over)) {
+              l_run += ts.x;
+              r_run += ts.y;
+              break;
+            }
           }
+          if (!ok) break;
           tmem_st32(tS, pk[0]);
           tmem_st32(tS + 32, pk[1]);
           tmem_wait_st();
@@ -891,7 +904,7 @@ bool paged_fits(const loong_paged_desc& d) {
   return groups * tiles < (int64_t{1} << 31) && groups * d.hkv * 8 < (int64_t{1} << 31);
 }
 
-template <int D, int SLOTS>
+template <int D, int SLOTS, bool CAP>
 int launch_paged(const loong_paged_desc& d, const PagedArgs& a, const AppendArgs& n, const void* q, const void* k_pages,
                  const void* v_pages, cudaStream_t stream) {
   using C = PagedCfg<D, SLOTS>;
@@ -908,7 +921,7 @@ int launch_paged(const loong_paged_desc& d, const PagedArgs& a, const AppendArgs
   const int copy_blocks = n.k ? std::min((d.tokens + kPrepThreads / 32 - 1) / (kPrepThreads / 32), 2 * sms) : 0;
   paged_prep_kernel<<<1 + copy_blocks, kPrepThreads, 0, stream>>>(a, n, SLOTS * a.per_slot);
   if ((st = check_launch()) != LOONG_OK) return st;
-  auto kern = paged_attn_kernel<D, SLOTS>;
+  auto kern = paged_attn_kernel<D, SLOTS, CAP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   if constexpr (C::SPLIT) {
@@ -976,8 +989,8 @@ int loong_paged_attn(const loong_paged_desc* d, const void* q, const void* k, co
   a.max_groups = w.max_groups;
   const float scale =
       d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt(static_cast<float>(d->head_dim));
-  a.cap_inv = d->score_cap > 0.f ? scale / d->score_cap : 0.f;
-  a.scale_log2 = (d->score_cap > 0.f ? d->score_cap : scale) * kLog2e;
+  a.cap = make_score_cap(scale, d->score_cap);
+  a.scale_log2 = scale * kLog2e;
   a.table = table;
   a.lens = lens;
   a.starts = starts;
@@ -1000,11 +1013,17 @@ int loong_paged_attn(const loong_paged_desc* d, const void* q, const void* k, co
   n.v_stride = d->v_stride ? d->v_stride / 8 : n.row_vecs;
   n.tickets = w.tickets;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  auto launch = [&](auto dim, auto slots) {
+    constexpr int D = decltype(dim)::value, SLOTS = decltype(slots)::value;
+    return d->score_cap > 0.f ? launch_paged<D, SLOTS, true>(*d, a, n, q, k_pages, v_pages, stream)
+                              : launch_paged<D, SLOTS, false>(*d, a, n, q, k_pages, v_pages, stream);
+  };
+  using std::integral_constant;
   if (d->head_dim == 128)
-    return w.slots == 2 ? launch_paged<128, 2>(*d, a, n, q, k_pages, v_pages, stream)
-                        : launch_paged<128, 1>(*d, a, n, q, k_pages, v_pages, stream);
-  return w.slots == 2 ? launch_paged<64, 2>(*d, a, n, q, k_pages, v_pages, stream)
-                      : launch_paged<64, 1>(*d, a, n, q, k_pages, v_pages, stream);
+    return w.slots == 2 ? launch(integral_constant<int, 128>{}, integral_constant<int, 2>{})
+                        : launch(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  return w.slots == 2 ? launch(integral_constant<int, 64>{}, integral_constant<int, 2>{})
+                      : launch(integral_constant<int, 64>{}, integral_constant<int, 1>{});
 }
 
 }  // extern "C"

@@ -1,25 +1,58 @@
 // softcap.cuh -- scores capped by a hyperbolic tangent: the attention kernels'
 // logit is cap * tanh(scale q.k / cap).
 //
-// A raw score s (the product of the matrix instructions) becomes t = tanh(x), x =
-// s * scale / cap, and the rest of a kernel goes on with t where it had s, its
-// factor cap * log2 e where it had scale * log2 e.  What counts is the absolute
-// error of t: times the cap it is the logit's.
+// A raw score s (the product of the matrix instructions) becomes s' = tanh(inv s) /
+// inv, inv = scale / cap, and the rest of a kernel goes on with s' where it had s.
+// What counts is the absolute error of the tangent: times the cap it is the logit's.
 //
-// |x| <= 1 takes an odd polynomial of degree 11, x (1 + y a(y)), y = x^2, a(y) fitted
-// on [0, 1] for the least greatest error of the whole (iterated weighted least
-// squares): 3.3e-7, below three half steps of fp32 next to 1.  Scores are formed in
-// pairs, so it costs four instructions a score, on the pipes that the exponentials
-// leave free.  A warp whose scores pass 1 takes 1 - 2 / (1 + e^2x), two more special
-// functions a score, off by at most 4e-7.
+// Up to |inv s| = 1 an odd polynomial of degree 11, s (1 + y a(y)), y = (inv s)^2, a(y)
+// fitted on [0, 1] for the least greatest error of the whole (iterated weighted least
+// squares): 3.3e-7, below three half steps of fp32 next to 1.  Up to 1/2, where most
+// scores are, one of degree 7 does (2.0e-7).  The powers of inv go into the
+// coefficients, and scores are formed in pairs: 7 and 5 paired operations for two
+// scores, which the fp32 pipe takes 14 and 10 cycles for; the matrix instructions take
+// 8 for them at head dimension 128, exponentials and sums 6 more.  A warp whose scores
+// pass 1 takes 1 - 2 / (1 + e^2x), two more special functions a score, off by at most
+// 4e-7.
 #pragma once
+
+#include <cmath>
 
 #include "ptx.cuh"
 
 namespace loong {
 
-constexpr float kTanhA1 = -0.33328669672829153f, kTanhA2 = 0.1327561340237302f, kTanhA3 = -0.05142530563209422f,
-                kTanhA4 = 0.01653276431015356f, kTanhA5 = -0.0029830620753639016f;
+struct ScoreCap {
+  float inv = 0.f;  // scale / cap; 0: no cap
+  float rinv = 0.f;
+  float limit = 0.f, near = 0.f;  // |s| up to which the polynomials hold
+  float c[5] = {}, n[3] = {};     // theirs: of s^2, s^4, ..
+};
+
+// scale and cap as the entry points let them through (2^-24 .. 2^24 and 2^-20 ..
+// 2^20).  The coefficients have to be normal numbers: the highest is about 2^-8
+// inv^10, so below inv = 2^-11 it may be lost, where it does not count up to a
+// quarter, below 2^-14 the next as well, and the polynomial is not used.
+inline ScoreCap make_score_cap(float scale, float cap) {
+  ScoreCap r;
+  if (!(cap > 0.f)) return r;
+  constexpr double a[5] = {-0.33328669672829153, 0.1327561340237302, -0.05142530563209422, 0.01653276431015356,
+                           -0.0029830620753639016};
+  constexpr double near[3] = {-0.33326460635391786, 0.1318586029707108, -0.04422924520882877};
+  const double inv = static_cast<double>(scale) / cap;
+  r.inv = static_cast<float>(inv);
+  r.rinv = static_cast<float>(1.0 / inv);
+  const double most = inv > 2048.0 ? 0.0 : inv > 0x1p-11 ? 1.0 : inv > 0x1p-14 ? 0.25 : 0.0;
+  r.limit = static_cast<float>(most / inv);
+  r.near = static_cast<float>(std::fmin(0.5, most) / inv);
+  double p = 1.0;
+  for (int i = 0; i < 5; ++i) {
+    p *= inv * inv;
+    r.c[i] = most > 0.0 ? static_cast<float>(a[i] * p) : 0.f;
+    if (i < 3) r.n[i] = most > 0.0 ? static_cast<float>(near[i] * p) : 0.f;
+  }
+  return r;
+}
 
 // max(|a|, |b|, |c|) in one instruction (sm_100 family).
 __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
@@ -28,38 +61,80 @@ __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
   return d;
 }
 
-// x[0 .. N) becomes tanh(x * inv), inv = scale / cap (32-bit words that hold
-// floats; N a multiple of 4).  The warp's lanes call it together.
-template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float inv) {
-  float m0 = 0.f, m1 = 0.f;
+// One score by the exponential.
+__device__ __forceinline__ float cap_score(float s, const ScoreCap& cap) {
+  return fmaf(__fdividef(-2.f, 1.f + fast_exp2(s * cap.inv * 2.8853900817779268f)), cap.rinv, cap.rinv);  // 2 log2 e
+}
+
+// s (1 + y (c[0] + y (c[1] + ..))), y = s^2, of s[0 .. N), N a multiple of 8.
+template <int N, int C>
+__device__ __forceinline__ void cap_polynomial(uint32_t (&s)[N], const float (&c)[C]) {
+  auto pair = [](float v) { return make_float2(v, v); };
+  constexpr int W = 4;  // pairs side by side (8 and 16: as fast)
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    m0 = fmax3_abs(m0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-    m1 = fmax3_abs(m1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-  }
-  if (__all_sync(0xffffffffu, fmaxf(m0, m1) * inv <= 1.f)) {
-    const float2 iv = make_float2(inv, inv);
-    auto pair = [](float c) { return make_float2(c, c); };
+  for (int i = 0; i < N; i += 2 * W) {
+    float2 x[W], y[W], p[W];
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), iv);
-      const float2 y = __fmul2_rn(x, x);
-      float2 p = __ffma2_rn(y, pair(kTanhA5), pair(kTanhA4));
-      p = __ffma2_rn(y, p, pair(kTanhA3));
-      p = __ffma2_rn(y, p, pair(kTanhA2));
-      p = __ffma2_rn(y, p, pair(kTanhA1));
-      p = __ffma2_rn(y, p, pair(1.f));
-      p = __fmul2_rn(x, p);
-      s[i] = __float_as_uint(p.x);
-      s[i + 1] = __float_as_uint(p.y);
+    for (int u = 0; u < W; ++u) {
+      x[u] = make_float2(__uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+      y[u] = __fmul2_rn(x[u], x[u]);
     }
-  } else {
-    const float k = inv * 2.8853900817779268f;  // 2 log2 e
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      s[i] = __float_as_uint(1.f - __fdividef(2.f, 1.f + fast_exp2(__uint_as_float(s[i]) * k)));
+    for (int u = 0; u < W; ++u) p[u] = __ffma2_rn(y[u], pair(c[C - 1]), pair(c[C - 2]));
+#pragma unroll
+    for (int k = C - 3; k >= 0; --k)
+#pragma unroll
+      for (int u = 0; u < W; ++u) p[u] = __ffma2_rn(y[u], p[u], pair(c[k]));
+#pragma unroll
+    for (int u = 0; u < W; ++u) p[u] = __fmul2_rn(y[u], p[u]);
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      x[u] = __ffma2_rn(x[u], p[u], x[u]);
+      s[i + 2 * u] = __float_as_uint(x[u].x);
+      s[i + 2 * u + 1] = __float_as_uint(x[u].y);
+    }
   }
+}
+
+// Scores s[0 .. N) (32-bit words that hold floats; N a multiple of 8) capped.  The
+// warp's lanes call it together.
+template <int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap) {
+  float m[4] = {};
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      m[u] = fmax3_abs(m[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+  const float most = fmaxf(fmax3_abs(m[0], m[1], m[2]), m[3]);
+  if (__all_sync(0xffffffffu, most <= cap.near)) {
+    cap_polynomial(s, cap.n);
+  } else if (__all_sync(0xffffffffu, most <= cap.limit)) {
+    cap_polynomial(s, cap.c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(cap_score(__uint_as_float(s[i]), cap));
+  }
+}
+
+// The 128 scores of a lane's row in tensor memory, from column address t on, capped
+// where they are, before the softmax reads them.  A loop, because the code of a tile
+// in one piece, the polynomial of 64 pairs and the other form of the tangent beside it
+// in front of the exponentials, did not fit the instruction cache: forward of 32 + 8
+// heads of 128, 16K tokens, 3.03-3.81 ms by how it was arranged, as a loop 2.56, with the shorter
+// polynomial beside the longer 2.33 (without a cap 1.37).  Bound by the instructions'
+// latencies: two softmax warps a scheduler, 0.42 instructions a cycle, the fp32 pipe
+// busy 41 % of the time, the tensor cores 34 %.
+__device__ __forceinline__ void cap_tile(uint32_t t, const ScoreCap& cap) {
+#pragma unroll 1
+  for (int cb = 0; cb < 4; ++cb) {
+    uint32_t s[32];
+    tmem_ld32(t + cb * 32, s);
+    tmem_wait_ld();
+    cap_scores(s, cap);
+    tmem_st32(t + cb * 32, s);
+  }
+  tmem_wait_st();
 }
 
 }  // namespace loong

@@ -259,7 +259,13 @@ def test_values_that_are_not_finite(cuda_device, name, value):
         t0 = sum(m for _, m in s.seqs[:b])
         hit[t0:t0 + new] = sees
         g = s.hq // s.hkv
-        assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(o[:, g:], clean[0][:, g:])
+        # An infinite K's score is beyond the cap's polynomial, so the rows of its warp take the other form of tanh:
+        # both are within their bound of the exact value (see the top; A <= |V|max, e < 2^-12 here), so within twice
+        # 2^-8 |O| + 2 (2^-8 + 2^-12) |V|max of each other.  Everything else is the same bits.
+        capped = s.cap and kind == "k"
+        far = 2.0 ** -7 * clean[0].float().abs() + 4 * (2.0 ** -8 + 2.0 ** -12) * s.v[torch.isfinite(s.v)].abs().max()
+        same = (o.float() - clean[0].float()).abs() <= far if capped else o == clean[0]
+        assert bool(same[~hit].all()) and bool(same[:, g:].all())
         if kind == "v" or not (s.cap and value == float("inf")):
             bad = ~torch.isfinite(o[hit][:, :g].float()).all(-1)
             assert bool(bad.all()) if kind == "v" or value != value else bool(bad.any())
