@@ -55,6 +55,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kSumBound = 256.0f;        // 2^threshold: the largest P let through without a new maximum
+// What an item costs a block beside its tiles, in tiles: its first scores wait for Q and
+// its rows for the last product.  Counted out of the division it left blocks that drew
+// many short items behind: 61 sequences of 64 to 16,000 keys, 64 + 8 heads of 128, 226 us
+// for 0, 167 for 2, 134 for 4; 13 sequences of up to 300 new tokens in a window 74, 46, 45.
+constexpr int kItemUnits = 4;
 constexpr int kMaxSequences = 4096;
 constexpr int kPrepThreads = 1024;
 constexpr float kMinCap = 9.5367432e-7f, kMaxCap = 1048576.f;        // 2^-20, 2^20
@@ -101,7 +106,7 @@ struct PagedArgs {
   const int* lens;     // [batch]
   const int* starts;   // [batch + 1]
   Group* groups;       // [max_groups]
-  int* prefix;         // [max_groups + 1]: tiles before a group (of one kv head)
+  int* prefix;         // [max_groups + 1]: units before a group (of one kv head)
   int* count;          // groups
   unsigned* tickets;   // [max_groups * hkv * softmax warps]
   float* part_o;       // [blocks * 2][SLOTS * 128][D]
@@ -154,7 +159,7 @@ __device__ __forceinline__ bool sequence(const PagedArgs& a, int b, int& tok, in
   return tok == s0 && count == s1 - s0 && len == l && count <= len;
 }
 
-// The groups and the tiles before each.
+// The groups and the units before each: an item's tiles, and kItemUnits.
 __device__ __forceinline__ void plan(const PagedArgs& a, int per_group) {
   __shared__ int first[kMaxSequences + 1];  // the sequences' first groups
   int base = 0, total;
@@ -175,7 +180,7 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int per_group) {
   if (!fine) atomicOr(a.err, kErrBounds);
   if (threadIdx.x == 0) first[a.batch] = base;
   __syncthreads();
-  int tiles_before = 0;
+  int units_before = 0;
   for (int g0 = 0; g0 < base; g0 += kPrepThreads) {
     const int g = g0 + threadIdx.x;
     int n = 0;
@@ -198,16 +203,17 @@ __device__ __forceinline__ void plan(const PagedArgs& a, int per_group) {
       r.pos = len - count + off;
       const int to = max(r.pos + r.count, 0), from = a.window ? max(r.pos - a.window + 1, 0) : 0;
       r.tile = from / kTile;
-      r.tiles = n = max((to + kTile - 1) / kTile - r.tile, 1);  // where nothing is seen that has to be stored
+      r.tiles = max((to + kTile - 1) / kTile - r.tile, 1);  // where nothing is seen that has to be stored
+      n = r.tiles + kItemUnits;
       r.pad0 = r.pad1 = 0;
       a.groups[g] = r;
     }
     const int end = block_scan(n, &total);
-    if (g < base) a.prefix[g] = tiles_before + end - n;
-    tiles_before += total;
+    if (g < base) a.prefix[g] = units_before + end - n;
+    units_before += total;
   }
   if (threadIdx.x == 0) {
-    a.prefix[base] = tiles_before;
+    a.prefix[base] = units_before;
     *a.count = base;
   }
 }
@@ -363,12 +369,18 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
     const int box = min(page_rows, kTile), boxes = kTile / box;
     int it = 0, seg = 0;
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int group = gi;
       const Group g = a.groups[gi];
       const int64_t base = static_cast<int64_t>(a.prefix[gi]) * a.hkv;
-      const int kvh = static_cast<int>((u - base) / g.tiles), skip = static_cast<int>((u - base) % g.tiles);
-      const int64_t begin = u - skip;  // the item's units
-      const int n = static_cast<int>(min(static_cast<int64_t>(g.tiles - skip), u1 - u));
+      const int units = g.tiles + kItemUnits;
+      const int kvh = static_cast<int>((u - base) / units), off = static_cast<int>((u - base) % units);
+      const int64_t begin = u - off, end = begin + units;  // the item's units, kItemUnits and then its tiles
+      const int skip = max(off - kItemUnits, 0);
+      u = min(end, u1);
+      const int n = max(static_cast<int>(u - begin) - kItemUnits, 0) - skip;
+      if (u == end && kvh == a.hkv - 1) ++gi;
+      if (n == 0) continue;
       Segment sg;
       sg.tok = g.tok;
       sg.count = g.count;
@@ -377,26 +389,16 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
       sg.seq = g.seq;
       sg.tile = g.tile + skip;
       sg.tiles = n;
-      sg.item = gi * a.hkv + kvh;
+      sg.item = group * a.hkv + kvh;
       sg.part = -1;
       sg.parts = 1;
       sg.first_part = sg.first_block = 0;
       if (n < g.tiles) {
-        sg.part = 2 * c + (u == u0 ? 0 : 1);
-        sg.first_block = block_of(begin);
-        sg.parts = block_of(begin + g.tiles - 1) - sg.first_block + 1;
-        sg.first_part = begin == U * sg.first_block / blocks ? 0 : 1;
+        sg.part = 2 * c + (seg == 0 ? 0 : 1);
+        sg.first_block = block_of(begin + kItemUnits);
+        sg.parts = block_of(end - 1) - sg.first_block + 1;
+        sg.first_part = U * sg.first_block / blocks >= begin ? 0 : 1;  // a block's first share or its last
       }
-      // Q, once the segment before has been multiplied with it
-      if (seg > 0 && !warp_wait(q_empty, (seg - 1) & 1)) break;
-      uint64_t* full = &seg_full[seg % C::SEGS];
-      if (leader) segs[seg % C::SEGS] = sg;
-      const int slots = SLOTS == 2 && g.count > a.per_slot ? 2 : 1;
-      mbar_expect_tx_p(leader, full, slots * C::ATOMS * a.per_slot * a.G * 128);
-      for (int h = 0; h < slots; ++h)
-        for (int at = 0; at < C::ATOMS; ++at)
-          tma_load_3d_p(leader, sQ + h * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, full, at * 64, kvh * a.G,
-                        g.tok + h * a.per_slot);
       // keys [from, to) are seen by some row: only their boxes are loaded
       const int to = g.pos + g.count, from = a.window ? max(g.pos - a.window + 1, 0) : 0;
       const int* pages = a.table + static_cast<int64_t>(g.seq) * a.max_pages;
@@ -406,6 +408,20 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
         page = lane < boxes && key < to && key + box > from ? __ldg(pages + (key >> a.page_log2)) : -1;
       };
       look_up(sg.tile);
+      // Q, once the segment before has been multiplied with it: after the first tile of K
+      auto load_q = [&]() {
+        if (seg > 0 && !warp_wait(q_empty, (seg - 1) & 1)) return false;
+        uint64_t* full = &seg_full[seg % C::SEGS];
+        if (leader) segs[seg % C::SEGS] = sg;
+        const int slots = SLOTS == 2 && g.count > a.per_slot ? 2 : 1;
+        mbar_expect_tx_p(leader, full, slots * C::ATOMS * a.per_slot * a.G * 128);
+        for (int h = 0; h < slots; ++h)
+          for (int at = 0; at < C::ATOMS; ++at)
+            tma_load_3d_p(leader, sQ + h * C::TILE_BYTES + at * C::ATOM_BYTES, &tmQ, full, at * 64, kvh * a.G,
+                          g.tok + h * a.per_slot);
+        return true;
+      };
+      bool q_loaded = false;
       for (int j = 0; j < n; ++j, ++it) {
         const int s = it % NS;
         const int key = (sg.tile + j) * kTile + lane * box;
@@ -430,7 +446,8 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
             tma_load_3d(sK + s * C::TILE_BYTES + at * C::ATOM_BYTES + lane * box * 128, &tmK, &k_full[s], at * 64, kvh,
                         row);
         }
-        if (it >= NS && !warp_wait(&v_empty[s], (it / NS - 1) & 1)) {
+        if (j == 0) q_loaded = load_q();
+        if (!q_loaded || (it >= NS && !warp_wait(&v_empty[s], (it / NS - 1) & 1))) {
           mbar_drain(&k_full[s], (it / NS) & 1, a.err);
           ok = false;
           break;
@@ -445,8 +462,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
                         row);
         }
       }
-      u += n;
-      if (begin + g.tiles == u && kvh == a.hkv - 1) ++gi;
+      if (q_loaded) ++seg;
     }
     if (ok) {  // the end (it needs no Q, but its place among the descriptions)
       if (seg == 0 || warp_wait(q_empty, (seg - 1) & 1)) {
@@ -565,13 +581,18 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
               const int key = cb * 32 + lane;
-              unsigned m = 0;
+              // 0 times a value that is not finite is NaN, which the sum keeps
+              __nv_bfloat162 nan = __float2bfloat162_rn(0.f);
+              const __nv_bfloat162 zero = nan;
 #pragma unroll 4
-              for (int p = 0; p < D / 8; ++p)
-                v16_finite(*reinterpret_cast<const uint4*>(tile + (p >> 3) * C::ATOM_BYTES + key * 128 +
-                                                           (((p & 7) ^ (key & 7)) << 4)),
-                           m);
-              bad[cb] = __ballot_sync(0xffffffffu, m != 0);
+              for (int p = 0; p < D / 8; ++p) {
+                const uint4 x = *reinterpret_cast<const uint4*>(tile + (p >> 3) * C::ATOM_BYTES + key * 128 +
+                                                                (((p & 7) ^ (key & 7)) << 4));
+                const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) nan = __hfma2(v[e], zero, nan);
+              }
+              bad[cb] = __ballot_sync(0xffffffffu, __hisnan(nan.x) || __hisnan(nan.y));
             }
             // noted before they are cleared: another warp that finds them cleared
             // finds them noted
@@ -900,7 +921,7 @@ PagedWs paged_ws(const loong_paged_desc& d) {
 bool paged_fits(const loong_paged_desc& d) {
   const int64_t per_group = static_cast<int64_t>(paged_slots(d)) * (kTile / (d.hq / d.hkv));
   const int64_t groups = d.tokens / per_group + d.batch;
-  const int64_t tiles = (static_cast<int64_t>(d.max_pages) * d.page_size + kTile - 1) / kTile + 1;
+  const int64_t tiles = (static_cast<int64_t>(d.max_pages) * d.page_size + kTile - 1) / kTile + 1 + kItemUnits;
   return groups * tiles < (int64_t{1} << 31) && groups * d.hkv * 8 < (int64_t{1} << 31);
 }
 
