@@ -111,8 +111,8 @@ struct BwdArgs {
   int t_begin, t_end;
   float scale, scale_log2;
   // Row statistics, [B*Hq][stat_len] each, block b's rows at b*blk_pad:
-  const float* lse2;   // LSE * log2(e); with a bias its negative
-  const float* dstat;  // D = rowsum(dO * O)
+  const float* lse2;   // LSE * log2(e); with a bias or a mask its negative
+  const float* dstat;  // D = rowsum(dO * O); with a mask its negative
   int blk_pad, stat_len;
   float* dq_acc;      // fp32, the layout of Q
   __nv_bfloat16* dk;  // FUSED outputs
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   std::conditional_t<MASK, RangeQWalk, QWalk> walk;
   int n;
   if constexpr (MASK) {
+    previous_launch_wait();
     const int nq = g.nblocks * g.ntile;
     walk.tiles = a.mask.tiles + static_cast<int64_t>(b) * nq;
     walk.g = &g;
@@ -803,28 +804,33 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         const int cbase = grp * C::GW + ch * 32;  // first query column of the chunk
         uint32_t pk[16];
         if constexpr (MASK) {
-          const float inv = a.mask.cap.inv;
+          // in pairs; the statistics hold -LSE and -D.  After P has been packed for dV it
+          // takes the cap's derivative, 1 - (inv s)^2 of the capped score s, for dS.
+          const float inv2 = -a.mask.cap.inv * a.mask.cap.inv;
+          const float2 sl2 = make_float2(a.scale_log2, a.scale_log2), i2 = make_float2(inv2, inv2),
+                       one = make_float2(1.f, 1.f);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 l4 = *reinterpret_cast<const float4*>(lse_row + cbase + e);
-            const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+            const float2 lv[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
 #pragma unroll
-            for (int u = 0; u < 4; u += 2) {
-              const float t0 = pv[0][e + u], t1 = pv[0][e + u + 1];
-              float x, y;
-              form_p(t0, t1, lv[u], lv[u + 1], x, y);
+            for (int u = 0; u < 2; ++u) {
+              const int c = e + 2 * u;
+              const float2 s = make_float2(pv[0][c], pv[0][c + 1]);
+              const float2 x = __ffma2_rn(s, sl2, lv[u]);
+              float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
               if (!unmasked) {
-                x = seen >> (e + u) & 1 ? x : 0.f;
-                y = seen >> (e + u + 1) & 1 ? y : 0.f;
+                p.x = seen >> c & 1 ? p.x : 0.f;
+                p.y = seen >> (c + 1) & 1 ? p.y : 0.f;
               }
-              pk[(e + u) / 2] = pack_bf16(x, y);
-              // from here on P with the cap's derivative, for dS
-              auto slope = [&](float s) {
-                const float t = s * inv;
-                return fmaf(-t, t, 1.f);
-              };
-              pv[0][e + u] = CAP && x != 0.f ? x * slope(t0) : x;
-              pv[0][e + u + 1] = CAP && y != 0.f ? y * slope(t1) : y;
+              pk[c / 2] = pack_bf16(p.x, p.y);
+              if constexpr (CAP) {
+                const float2 q = __fmul2_rn(p, __ffma2_rn(__fmul2_rn(s, i2), s, one));
+                // a masked score may be NaN
+                p = unmasked ? q : make_float2(p.x != 0.f ? q.x : 0.f, p.y != 0.f ? q.y : 0.f);
+              }
+              pv[0][c] = p.x;
+              pv[0][c + 1] = p.y;
             }
           }
         } else if (unmasked) {
@@ -890,8 +896,19 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           const float4 d4 = *reinterpret_cast<const float4*>(d_row + cbase + e);
           const float dv4[4] = {d4.x, d4.y, d4.z, d4.w};
           float ds[4];
+          if constexpr (MASK) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 4; u += 2) {
+              const float2 p = make_float2(pv[0][e + u], pv[0][e + u + 1]);
+              const float2 x = __fmul2_rn(
+                  p, __fadd2_rn(make_float2(__uint_as_float(dpv[e + u]), __uint_as_float(dpv[e + u + 1])),
+                                make_float2(dv4[u], dv4[u + 1])));
+              ds[u] = unmasked || p.x != 0.f ? x.x : 0.f;
+              ds[u + 1] = unmasked || p.y != 0.f ? x.y : 0.f;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < (MASK ? 0 : 4); ++u) {
             const float p = pv[ch][e + u];
             const float x = p * (__uint_as_float(dpv[e + u]) - dv4[u]);
             // masked columns: p is 0 and D may be another row's or padding
@@ -1062,9 +1079,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           tmem_wait_ld();
           if (key_ok) {
             float4* dst = reinterpret_cast<float4*>(acc_glob + cb * 32);
+            // MASK, FUSED: the first flush finds an accumulator that was not cleared
+            const bool fresh = MASK && !STEP && i + 1 == kFlush;
 #pragma unroll
             for (int v4 = 0; v4 < 8; ++v4) {
-              float4 x = dst[v4];
+              float4 x = fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : dst[v4];
               x.x += __uint_as_float(v[v4 * 4 + 0]) * acc_mul;
               x.y += __uint_as_float(v[v4 * 4 + 1]) * acc_mul;
               x.z += __uint_as_float(v[v4 * 4 + 2]) * acc_mul;
@@ -1187,9 +1206,13 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
     a.t_begin = t_first;
     a.t_end = t_last;
     record_start(stream);
-    kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, mo, mdq, a);
+    if constexpr (VARIANT == kBwdMask || VARIANT == kBwdCap)
+      st = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::THREADS, C::SMEM_BYTES, stream, mq, mk, mv, mo,
+                            mdq, a);
+    else
+      kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, mo, mdq, a);
     record_stop(stream);
-    return check_launch();
+    return st == LOONG_OK ? check_launch() : st;
   }
   if (is_copy_mode(d)) {
     // receive buffers K0, K1, V0, V1, each the size of K (exchange.h); dK, dV
@@ -1258,10 +1281,11 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
   int st;
   cudaError_t e = bias || mask ? cudaSuccess : cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  // FUSED walks of at most kFlush (tile, head) pairs never touch the dK, dV accumulators
+  // FUSED walks of at most kFlush (tile, head) pairs never touch the dK, dV accumulators;
+  // with a mask longer ones write them first
   const RingGeom g = ring_geom(d);
   const int64_t longest = static_cast<int64_t>(d.hq / d.hkv) * g.nblocks * g.ntile;
-  if ((step || longest > kFlush) &&
+  if ((step || (longest > kFlush && !mask)) &&
       ((e = cudaMemsetAsync(dk_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess ||
        (e = cudaMemsetAsync(dv_acc, 0, static_cast<size_t>(kv_elems) * 4, stream)) != cudaSuccess))
     return cuda_fail(e);

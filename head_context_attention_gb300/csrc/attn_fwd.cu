@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
 
   std::conditional_t<MASK, RangeWalk, KvWalk> walk;
   if constexpr (MASK) {
+    previous_launch_wait();
     const int4* tiles = a.mask.tiles + (static_cast<int64_t>(b) * g.nblocks + bq) * g.ntile;
     const int4 t0 = tiles[qi0], t1 = tiles[qi];
     walk.init(g, block_owner(g, bq), a.t_begin, a.t_end, min(t0.x, t1.x), max(t0.y, t1.y));
@@ -892,9 +893,12 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
     a.t_begin = 0;
     a.t_end = d.cp;
     record_start(stream);
-    kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
+    if constexpr (MASK)
+      st = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, C::SMEM_BYTES, stream, mq, mk, mv, a);
+    else
+      kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
     record_stop(stream);
-    return check_launch();
+    return st == LOONG_OK ? check_launch() : st;
   }
   if (is_copy_mode(d)) {
     // receive buffers K0, K1, V0, V1, each the size of K

@@ -149,6 +149,25 @@ __device__ __forceinline__ int2 mask_range(const MaskView& m, int b, int t, int 
 // SMs of the current device.
 int num_sms();
 
+// A launch whose blocks may start, up to previous_launch_wait, while the kernel
+// before it in the stream still runs (next_launch_go there).
+template <typename... Params, typename... Args>
+int launch_dependent(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                     const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e == cudaSuccess ? LOONG_OK : cuda_fail(e);
+}
+
 // Kernel launchers (asynchronous on `stream`).
 // Query rows of ring ranks [rank_begin, rank_end) only (all of them: 0, cp).
 // The forward first writes V's fp16 copy into sc.v16 (with a bias or a mask it is there already).

@@ -74,6 +74,7 @@ __device__ __forceinline__ void sum_tile(const TileArgs& a, int64_t x) {
 // first), then 8 tiles a block.
 __global__ void __launch_bounds__(kThreads) mask_fwd_prep_kernel(const __grid_constant__ TileArgs a,
                                                                  const __grid_constant__ VArgs v) {
+  next_launch_go();
   const int id = static_cast<int>(blockIdx.x) - max(v.max_blocks, 1);
   if (id < 0) {
     v16_first_launch<kThreads, true>(v, blockIdx.x);
@@ -84,13 +85,16 @@ __global__ void __launch_bounds__(kThreads) mask_fwd_prep_kernel(const __grid_co
 }
 
 __global__ void __launch_bounds__(kThreads) mask_v16_kernel(const __grid_constant__ VArgs v) {
+  next_launch_go();
+  previous_launch_wait();
   v16_copy<kThreads, true>(v);
 }
 
 // Before the backward, in one launch, a block for a query tile of a head: dQ's
 // accumulator cleared, the row statistics (rowstats.cuh), and whether the tile has
 // rows for the backward's producer to clear: those whose dO or LSE is not finite (so
-// is their LSE among the statistics: NaN, but -inf for a row that sees no key), and
+// is their LSE among the statistics, which hold -LSE and -D: NaN, but infinite for a
+// row that sees no key), and
 // with a cap, which leaves infinite scores finite, those whose Q is not; and,
 // where the tile ends inside the block of 128, any not finite among the rows behind
 // it, which the copies bring in as well.  Head 0's blocks sum the tile's ranges up.
@@ -104,6 +108,7 @@ struct BwdPrepArgs {
 };
 template <int D>
 __global__ void __launch_bounds__(kThreads) mask_bwd_prep_kernel(const __grid_constant__ BwdPrepArgs a) {
+  next_launch_go();
   constexpr int TPR = D / 8, RPP = kThreads / TPR;  // threads of a row, rows of a pass
   const RowStatsArgs& r = a.r;
   const RingGeom& g = a.tiles.g;
@@ -160,8 +165,8 @@ __global__ void __launch_bounds__(kThreads) mask_bwd_prep_kernel(const __grid_co
       if (in_bounds(pos >= 0 && pos < (bh + 1) * r.stat_len, r.err)) {
         float l = __ldg(r.lse + bh * r.S + t0 + row);
         if (bad || !(l < INFINITY)) l = __int_as_float(0x7fffffff);
-        r.dstat[pos] = acc;
-        r.lse2[pos] = l * kRowStatsLog2e;
+        r.dstat[pos] = -acc;
+        r.lse2[pos] = -l * kRowStatsLog2e;
         mark |= !(fabsf(l) < INFINITY);
       }
     }
@@ -271,8 +276,8 @@ int loong_attn_mask_fwd(const loong_attn_desc* d, const loong_attn_mask* mask, c
   mask_fwd_prep_kernel<<<static_cast<unsigned>(std::max(va.max_blocks, 1) + tile_blocks), kThreads, 0, stream>>>(a, va);
   if ((st = check_launch()) != LOONG_OK) return st;
   if (va.max_blocks > 0) {
-    mask_v16_kernel<<<static_cast<unsigned>(blocks_for(va.vecs)), kThreads, 0, stream>>>(va);
-    if ((st = check_launch()) != LOONG_OK) return st;
+    st = launch_dependent(mask_v16_kernel, dim3(blocks_for(va.vecs)), kThreads, 0, stream, va);
+    if (st != LOONG_OK) return st;
   }
   return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, nullptr, &a.m);
 }

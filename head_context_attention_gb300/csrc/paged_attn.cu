@@ -6,7 +6,7 @@
 //   O_i = sum_j softmax_j(z_ij) v_j over j <= i (and j > i - window), j a position of
 //   i's sequence, its K and V at row j mod page of page table[sequence][j / page]
 //
-// Two launches.  paged_prep_kernel writes the new keys and values into their pages
+// Two launches, the second's blocks starting while the first runs.  paged_prep_kernel writes the new keys and values into their pages
 // and lays the work out (block 0): a group is up to SLOTS * (128 / G) new tokens of a
 // sequence, G query heads to a kv head; with a kv head it makes an item, whose rows
 // (token by token, the kv head's G query heads each) fill SLOTS blocks of 128 rows of
@@ -239,6 +239,7 @@ __device__ __forceinline__ int sequence_of(const PagedArgs& a, int t) {
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_constant__ PagedArgs a,
                                                                   const __grid_constant__ AppendArgs n,
                                                                   int per_group) {
+  next_launch_go();
   const int id = blockIdx.x * kPrepThreads + threadIdx.x, threads = gridDim.x * kPrepThreads;
   for (int i = id; i < n.tickets; i += threads) a.tickets[i] = 0;
   if (blockIdx.x == 0) {
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = tmem_base_sh;
+  previous_launch_wait();
   if constexpr (C::SPLIT) {
     if (warp >= C::SOFTMAX_WARPS) regs_dec<C::OTHER_REGS>();
   }
@@ -951,8 +953,7 @@ int launch_paged(const loong_paged_desc& d, const PagedArgs& a, const AppendArgs
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return cuda_fail(e);
     if (at.numRegs < C::SPLIT_REGS) return LOONG_ERR_UNSUPPORTED;
   }
-  kern<<<sms, C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
-  return check_launch();
+  return launch_dependent(kern, dim3(sms), C::THREADS, C::SMEM_BYTES, stream, mq, mk, mv, a);
 }
 
 }  // namespace

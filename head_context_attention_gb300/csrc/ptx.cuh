@@ -359,6 +359,14 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ------------------------------------------------- a launch after another
+// The kernel before this one in the stream has completed and what it wrote is seen
+// (a kernel that launch_dependent started early waits here; else nothing to wait for).
+__device__ __forceinline__ void previous_launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel after this one, where launch_dependent launches it, may start and come as far
+// as its wait.
+__device__ __forceinline__ void next_launch_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- math
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
