@@ -119,21 +119,31 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap
 }
 
 // The 128 scores of a lane's row in tensor memory, from column address t on, capped
-// where they are, before the softmax reads them.  A loop, because the code of a tile
-// in one piece, the polynomial of 64 pairs and the other form of the tangent beside it
-// in front of the exponentials, did not fit the instruction cache: forward of 32 + 8
-// heads of 128, 16K tokens, 3.03-3.81 ms by how it was arranged, as a loop 2.56, with the shorter
-// polynomial beside the longer 2.33 (without a cap 1.37).  Bound by the instructions'
-// latencies: two softmax warps a scheduler, 0.42 instructions a cycle, the fp32 pipe
-// busy 41 % of the time, the tensor cores 34 %.
+// where they are, before the softmax reads them, N at a time.  A loop, because the
+// code of a tile in one piece, the polynomial of 64 pairs and the other form of the
+// tangent beside it in front of the exponentials, did not fit the instruction cache:
+// forward of 32 + 8 heads of 128, 16K tokens, scores of deviation 3, 3.03-3.81 ms by how
+// it was arranged, as a loop 2.56, with the shorter polynomial beside the longer 2.32
+// (without a cap, on the same scores, 1.57).  The difference is the fp32 pipe's 1,280
+// cycles for two slots' polynomials, which no other work of the chain from scores to
+// scores covers (0.58 ms), and the way through tensor memory (0.24).  Four more warps for
+// the cap alone, 2.63: the softmax warps then have 176 registers for 216, and every tile
+// one more barrier on its way.
+template <int N>
 __device__ __forceinline__ void cap_tile(uint32_t t, const ScoreCap& cap) {
 #pragma unroll 1
-  for (int cb = 0; cb < 4; ++cb) {
-    uint32_t s[32];
-    tmem_ld32(t + cb * 32, s);
+  for (int cb = 0; cb < 128; cb += N) {
+    uint32_t s[N / 32][32], x[N];
+#pragma unroll
+    for (int u = 0; u < N / 32; ++u) tmem_ld32(t + cb + u * 32, s[u]);
     tmem_wait_ld();
-    cap_scores(s, cap);
-    tmem_st32(t + cb * 32, s);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = s[i / 32][i % 32];
+    cap_scores(x, cap);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i / 32][i % 32] = x[i];
+#pragma unroll
+    for (int u = 0; u < N / 32; ++u) tmem_st32(t + cb + u * 32, s[u]);
   }
   tmem_wait_st();
 }

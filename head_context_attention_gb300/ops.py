@@ -680,6 +680,19 @@ def _mask_problem_of(w, score_cap, mode, layout):
     return (_kept_mask_problem if type(w) is Workload else _mask_problem)(w, float(score_cap), mode, layout)
 
 
+def _mask_tensors(w, layout, key_range, lse, **bf16):
+    """Refuse what the C entry cannot see of the tensors below; ``bf16`` by name, k
+    and v of the key heads, the others of the query heads, o_res may be None."""
+    device = bf16["q"].device
+    for n, t in bf16.items():
+        if t is not None or n != "o_res":
+            _contiguous(n, t, _attn_shape(w, w.hkv if n in ("k", "v") else w.hq, layout), torch.bfloat16, device)
+    if lse is not None:
+        _contiguous("lse", lse, (w.batch, w.hq, w.seqlen), torch.float32, device)
+    if key_range is not None:
+        _contiguous("key_range", key_range, (w.batch, w.seqlen, 2), torch.int32, device)
+
+
 def attn_mask_fwd(w, q, k, v, key_range=None, score_cap=0.0, mode=MODE_FUSED, stream=None, layout=LAYOUT_NATURAL,
                   res=True):
     """attn_fwd in which query i sees the keys key_range[b, i, 0] <= j <
@@ -688,16 +701,14 @@ def attn_mask_fwd(w, q, k, v, key_range=None, score_cap=0.0, mode=MODE_FUSED, st
     score_cap) (0: not).  Returns (o, lse, o_res); o_res is None when ``res`` is
     false."""
     desc, nbytes, _ = _mask_problem_of(w, score_cap, mode, layout)
-    for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv)):
-        _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, q.device)
-    if key_range is not None:
-        _contiguous("key_range", key_range, (w.batch, w.seqlen, 2), torch.int32, q.device)
-    where, stream = _on(q.device, stream)
+    _mask_tensors(w, layout, key_range, None, q=q, k=k, v=v)
+    device = q.device
+    where, stream = _on(device, stream)
     with where:
         o = torch.empty_like(q)
         o_res = torch.empty_like(q) if res else None
-        lse = torch.empty((w.batch, w.hq, w.seqlen), dtype=torch.float32, device=q.device)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        lse = torch.empty((w.batch, w.hq, w.seqlen), dtype=torch.float32, device=device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         loong_attn_mask_fwd(desc, make_mask(key_range, score_cap), q, k, v, o, lse, o_res, ws, stream)
     return o, lse, o_res
 
@@ -706,13 +717,9 @@ def attn_mask_bwd(w, q, k, v, o, lse, do, key_range=None, score_cap=0.0, o_res=N
                   layout=LAYOUT_NATURAL):
     """Gradient of attn_mask_fwd: (dq, dk, dv)."""
     desc, _, nbytes = _mask_problem_of(w, score_cap, mode, layout)
-    for n, t, h in (("q", q, w.hq), ("k", k, w.hkv), ("v", v, w.hkv), ("o", o, w.hq), ("do", do, w.hq),
-                    ("o_res", o_res, w.hq)):
-        if t is not None or n != "o_res":
-            _contiguous(n, t, _attn_shape(w, h, layout), torch.bfloat16, q.device)
-    _contiguous("lse", lse, (w.batch, w.hq, w.seqlen), torch.float32, q.device)
-    if key_range is not None:
-        _contiguous("key_range", key_range, (w.batch, w.seqlen, 2), torch.int32, q.device)
+    if not isinstance(lse, torch.Tensor):
+        raise TypeError("lse must be a tensor")
+    _mask_tensors(w, layout, key_range, lse, q=q, k=k, v=v, o=o, do=do, o_res=o_res)
     where, stream = _on(q.device, stream)
     with where:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -849,6 +856,8 @@ def qk_norm_rope_bwd(w, opts, q, k, dq, dk, dv=None, wq=None, wk=None, positions
 def _row_stride(name, t, heads, d):
     """Elements from row to row of [tokens, heads, d] with contiguous heads; an
     expanded view repeats one row's memory and is not taken."""
+    if t.is_contiguous():
+        return heads * d
     ss, sh, sd = t.stride()
     if t.shape[0] <= 1:
         ss = heads * d
@@ -877,29 +886,35 @@ def paged_attn(q, k_pages, v_pages, table, lens, starts, k=None, v=None, window=
     ``score_cap`` as in attn_mask_fwd.  ``out``: (o, lse) to write, whose rows
     behind the last sequence stay as they are.  Returns (o, lse), lse fp32 [hq,
     tokens]."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("q must be a tensor [tokens, hq, d], the pages [num_pages, page_size, hkv, d]")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a tensor [batch, max_pages]")
-    if (k is None) != (v is None):
-        raise ValueError("k and v belong together: give both or neither")
+    if q.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError("q must be [tokens, hq, d], k_pages [num_pages, page_size, hkv, d], table [batch, max_pages]")
     tokens, hq, d = q.shape
     num_pages, page, hkv, _ = k_pages.shape
     batch, max_pages = table.shape
-    dev, bf16 = q.device, torch.bfloat16
-    _same("q", q, (tokens, hq, d), bf16, dev)
-    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _contiguous(n, t, (num_pages, page, hkv, d), bf16, dev)
-    _contiguous("table", table, (batch, max_pages), torch.int32, dev)
-    _contiguous("lens", lens, (batch,), torch.int32, dev)
-    _contiguous("starts", starts, (batch + 1,), torch.int32, dev)
-    strides = [_row_stride("q", q, hq, d), 0, 0]
+    dev, bf16, i32 = q.device, torch.bfloat16, torch.int32
+    if (k is None) != (v is None):
+        raise ValueError("k and v belong together: give both or neither")
+    # a token at a time the checks' own time counts: in one go, one after the other only to say which
+    if not (q.dtype is bf16 and k_pages.dtype is bf16 and v_pages.dtype is bf16 and table.dtype is i32 and
+            lens.dtype is i32 and starts.dtype is i32 and k_pages.shape[3] == d and v_pages.shape == k_pages.shape and
+            lens.shape == (batch,) and starts.shape == (batch + 1,) and k_pages.is_contiguous() and
+            v_pages.is_contiguous() and table.is_contiguous() and lens.is_contiguous() and starts.is_contiguous() and
+            k_pages.device == v_pages.device == table.device == lens.device == starts.device == dev):
+        _same("q", q, (tokens, hq, d), bf16, dev)
+        for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            _contiguous(n, t, (num_pages, page, hkv, d), bf16, dev)
+        _contiguous("table", table, (batch, max_pages), i32, dev)
+        _contiguous("lens", lens, (batch,), i32, dev)
+        _contiguous("starts", starts, (batch + 1,), i32, dev)
+    q_stride, k_stride, v_stride = _row_stride("q", q, hq, d), 0, 0
     if k is not None:
-        for i, (n, t) in enumerate((("k", k), ("v", v))):
-            _same(n, t, (tokens, hkv, d), bf16, dev)
-            strides[1 + i] = _row_stride(n, t, hkv, d)
-    desc, nbytes = _paged_problem(batch, tokens, hq, hkv, d, page, num_pages, max_pages, int(window), float(scale),
-                                  float(score_cap), *strides)
+        if not (k.dtype is bf16 and v.dtype is bf16 and k.shape == v.shape == (tokens, hkv, d) and
+                k.device == v.device == dev):
+            _same("k", k, (tokens, hkv, d), bf16, dev)
+            _same("v", v, (tokens, hkv, d), bf16, dev)
+        k_stride, v_stride = _row_stride("k", k, hkv, d), _row_stride("v", v, hkv, d)
+    desc, nbytes = _paged_problem(batch, tokens, hq, hkv, d, page, num_pages, max_pages, window, scale, score_cap,
+                                  q_stride, k_stride, v_stride)
     if out is not None:
         _contiguous("out[0]", out[0], (tokens, hq, d), bf16, dev)
         _contiguous("out[1]", out[1], (hq, tokens), torch.float32, dev)
