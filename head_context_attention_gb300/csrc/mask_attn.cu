@@ -189,6 +189,18 @@ int check_mask(const loong_attn_desc* d, const loong_attn_mask* m) {
   return LOONG_OK;
 }
 
+// In FUSED mode the walks do not follow the ring, so where the layout does not either
+// the sequence is one block: its tiles are of 128 tokens but for the last one, whatever
+// the ring's blocks (2 x 1990 tokens in 10 blocks of 199, 6 + 3 heads of 64: 16 tiles a
+// sequence for 20; 320 tokens in 16 blocks: 3 for 16).
+loong_attn_desc one_block(loong_attn_desc d) {
+  if (d.mode == LOONG_MODE_FUSED && d.layout == LOONG_LAYOUT_NATURAL) {
+    d.hp = d.cp = d.ring_inner = d.ring_outer = 1;
+    d.placement = LOONG_PLACEMENT_CONTIGUOUS;
+  }
+  return d;
+}
+
 // The workspace: the plain pass's first, then the tiles' sums and, forward, the
 // shares of max |V|, backward, the marks of the query tiles.
 struct MaskWs {
@@ -237,15 +249,16 @@ int loong_attn_mask_check(const loong_attn_desc* d, const loong_attn_mask* mask)
 
 size_t loong_attn_mask_workspace_size(const loong_attn_desc* d, const loong_attn_mask* mask, int pass) {
   if (check_mask(d, mask) != LOONG_OK || (pass != 0 && pass != 1)) return 0;
-  return mask_ws(*d, pass).total;
+  return mask_ws(one_block(*d), pass).total;
 }
 
-int loong_attn_mask_fwd(const loong_attn_desc* d, const loong_attn_mask* mask, const void* q, const void* k,
+int loong_attn_mask_fwd(const loong_attn_desc* desc, const loong_attn_mask* mask, const void* q, const void* k,
                         const void* v, void* o, float* lse, void* o_res, void* ws, size_t ws_bytes,
                         loong_stream_t stream_) {
   NvtxRange range("loong_attn_mask_fwd");
-  int st = check_mask(d, mask);
+  int st = check_mask(desc, mask);
   if (st != LOONG_OK) return st;
+  const loong_attn_desc one = one_block(*desc), *d = &one;
   const void* ptrs[] = {q, k, v, o, lse};
   for (const void* p : ptrs)
     if (!p || !aligned(p, 16)) return LOONG_ERR_INVALID_ARG;
@@ -282,12 +295,13 @@ int loong_attn_mask_fwd(const loong_attn_desc* d, const loong_attn_mask* mask, c
   return run_attn_fwd(*d, q, k, v, o, lse, o_res, ws, stream, nullptr, &a.m);
 }
 
-int loong_attn_mask_bwd(const loong_attn_desc* d, const loong_attn_mask* mask, const void* q, const void* k,
+int loong_attn_mask_bwd(const loong_attn_desc* desc, const loong_attn_mask* mask, const void* q, const void* k,
                         const void* v, const void* o, const void* o_res, const float* lse, const void* dout, void* dq,
                         void* dk, void* dv, void* ws, size_t ws_bytes, loong_stream_t stream_) {
   NvtxRange range("loong_attn_mask_bwd");
-  int st = check_mask(d, mask);
+  int st = check_mask(desc, mask);
   if (st != LOONG_OK) return st;
+  const loong_attn_desc one = one_block(*desc), *d = &one;
   const void* ptrs[] = {q, k, v, o, lse, dout, dq, dk, dv};
   for (const void* p : ptrs)
     if (!p || !aligned(p, 16)) return LOONG_ERR_INVALID_ARG;

@@ -223,7 +223,7 @@ struct RangeWalk {
   __host__ __device__ int block(int part) const { return whole ? first + part : rank_block(g, first, part); }
   __host__ __device__ int tile_begin(int b) const {
     const int off = kmin - b * g.blk;
-    return off > 0 ? off / kTile : 0;
+    return off <= 0 ? 0 : off < g.blk ? off / kTile : g.ntile;  // the last tile may end inside 128
   }
   __host__ __device__ int tile_end(int b) const {
     int off = kmax - b * g.blk;

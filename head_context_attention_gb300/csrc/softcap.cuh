@@ -5,55 +5,19 @@
 // inv, inv = scale / cap, and the rest of a kernel goes on with s' where it had s.
 // What counts is the absolute error of the tangent: times the cap it is the logit's.
 //
-// Up to |inv s| = 1 an odd polynomial of degree 11, s (1 + y a(y)), y = (inv s)^2, a(y)
-// fitted on [0, 1] for the least greatest error of the whole (iterated weighted least
-// squares): 3.3e-7, below three half steps of fp32 next to 1.  Up to 1/2, where most
-// scores are, one of degree 7 does (2.0e-7).  (Up to 1/4 one of degree 5 as well: 4 %
-// for the forward where scores stay there, 3 % against it elsewhere and in the backward.)  The powers of inv go into the
-// coefficients, and scores are formed in pairs: 7 and 5 paired operations for two
-// scores, which the fp32 pipe takes 14 and 10 cycles for; the matrix instructions take
-// 8 for them at head dimension 128, exponentials and sums 6 more.  A warp whose scores
+// Scores within the polynomials' reach (score_cap.h) are formed in pairs: 7 paired
+// operations for two scores up to |inv s| = 1, 5 up to 1/2, where most are; the fp32 pipe
+// takes 14 and 10 cycles for them, the matrix instructions 8 at head dimension 128,
+// exponentials and sums 6.  (A third polynomial up to 1/4: 4 % for the forward where
+// scores stay there, 3 % against it elsewhere and in the backward.)  A warp whose scores
 // pass 1 takes 1 - 2 / (1 + e^2x), two more special functions a score, off by at most
 // 4e-7.
 #pragma once
 
-#include <cmath>
-
 #include "ptx.cuh"
+#include "score_cap.h"
 
 namespace loong {
-
-struct ScoreCap {
-  float inv = 0.f;  // scale / cap; 0: no cap
-  float rinv = 0.f;
-  float limit = 0.f, half = 0.f;  // |s| up to which the polynomials hold
-  float c[5] = {}, h[3] = {};     // theirs: of s^2, s^4, ..
-};
-
-// scale and cap as the entry points let them through (2^-24 .. 2^24 and 2^-20 ..
-// 2^20).  The coefficients have to be normal numbers: the highest is about 2^-8
-// inv^10, so below inv = 2^-11 it may be lost, where it does not count up to a
-// quarter, below 2^-14 the next as well, and the polynomial is not used.
-inline ScoreCap make_score_cap(float scale, float cap) {
-  ScoreCap r;
-  if (!(cap > 0.f)) return r;
-  constexpr double a[5] = {-0.33328669672829153, 0.1327561340237302, -0.05142530563209422, 0.01653276431015356,
-                           -0.0029830620753639016};
-  constexpr double half[3] = {-0.33326460635391786, 0.1318586029707108, -0.04422924520882877};
-  const double inv = static_cast<double>(scale) / cap;
-  r.inv = static_cast<float>(inv);
-  r.rinv = static_cast<float>(1.0 / inv);
-  const double most = inv > 2048.0 ? 0.0 : inv > 0x1p-11 ? 1.0 : inv > 0x1p-14 ? 0.25 : 0.0;
-  r.limit = static_cast<float>(most / inv);
-  r.half = static_cast<float>(std::fmin(0.5, most) / inv);
-  double p = 1.0;
-  for (int i = 0; i < 5; ++i) {
-    p *= inv * inv;
-    r.c[i] = most > 0.0 ? static_cast<float>(a[i] * p) : 0.f;
-    if (i < 3) r.h[i] = most > 0.0 ? static_cast<float>(half[i] * p) : 0.f;
-  }
-  return r;
-}
 
 // max(|a|, |b|, |c|) in one instruction (sm_100 family).
 __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {

@@ -437,7 +437,8 @@ LOONG_API int loong_attn_mask_check(const loong_attn_desc* desc, const loong_att
  * loong_attn_mask_bwd (pass 1); 0 for invalid arguments.  Host-only.
  * loong_attn_workspace_size's, then 16 bytes for every 128-token query tile of a
  * block; for the forward 1,216 words more, for the backward a byte for every
- * query tile and head.  Each part starts on a 256-byte boundary.
+ * query tile and head.  Each part starts on a 256-byte boundary.  A FUSED
+ * descriptor with the NATURAL layout counts as one of cp = hp = 1, one block.
  */
 LOONG_API size_t loong_attn_mask_workspace_size(const loong_attn_desc* desc, const loong_attn_mask* mask, int pass);
 
