@@ -158,6 +158,7 @@ struct BwdPiece {
 // rows of K that are not are cleared in shared memory by the compute warps, rows of Q
 // and dO by the producer, in the tiles that the launch before marked.  Instead the
 // row's own P is NaN, for those that see it.
+// Where key tiles do not fill the SMs, the query heads of a group go to several blocks.
 enum BwdVariant { kBwdPlain, kBwdBias, kBwdMask, kBwdCap };
 
 // The query tiles, in natural order, that see a block's keys [k0, k1), a word of 32
@@ -262,6 +263,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   // ---- work item: (batch, kv head, key tile); early (heavy) key tiles first
   const RingGeom& g = a.ring;
   int idx = blockIdx.x;
+  int split = 0;
+  if constexpr (MASK) {
+    split = idx % a.mask.splits;
+    idx /= a.mask.splits;
+  }
   const int nkt = g.nblocks * g.ntile;
   const int r = idx % nkt;
   idx /= nkt;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     walk.g = &g;
     walk.k0 = k0;
     walk.k1 = k0 + klen;
-    walk.G = a.G;
+    walk.G = min(a.mask.per_split, a.G - split * a.mask.per_split);
     walk.rank = STEP ? ring_dst(block_owner(g, bk), a.t_begin, g.inner, g.outer) : -1;
     if (threadIdx.x == 0) {
       sWalk[0] = 0;
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       atomicMax(sWalk + 2, last);
     }
     __syncthreads();
-    n = sWalk[0] * a.G;
+    n = sWalk[0] * walk.G;
     walk.base = sWalk[1];
     walk.last = sWalk[2];
     if (n == 0) {
@@ -315,8 +321,16 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         for (int i = threadIdx.x; i < klen * (D / 8); i += C::THREADS) {
           const int64_t kv = a.lay.vec(b, k0 + i / (D / 8), kvh, a.hkv);
           if (!in_bounds(kv >= 0 && kv < static_cast<int64_t>(a.batch) * a.S * a.hkv, a.err)) continue;
-          reinterpret_cast<uint4*>(a.dk + kv * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
-          reinterpret_cast<uint4*>(a.dv + kv * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+          if (a.mask.splits > 1) {
+            const int64_t at = (static_cast<int64_t>(a.batch) * a.S * a.hkv * split + kv) * D;
+            for (int u = 0; u < 2; ++u) {
+              reinterpret_cast<float4*>(a.dk_acc + at)[2 * (i % (D / 8)) + u] = make_float4(0.f, 0.f, 0.f, 0.f);
+              reinterpret_cast<float4*>(a.dv_acc + at)[2 * (i % (D / 8)) + u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          } else {
+            reinterpret_cast<uint4*>(a.dk + kv * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(a.dv + kv * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+          }
         }
       }
       return;
@@ -421,9 +435,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       look_up();
       // MASK: whether the tile the walk stands at has rows to clear (for the next trip)
       unsigned marked = 0, patches = 0;
+      const int head0 = kvh * a.G + (MASK ? split * a.mask.per_split : 0);
       auto look_up_mark = [&]() {
         if constexpr (MASK)
-          marked = __ldg(a.mask.bad + (static_cast<int64_t>(b) * a.hq + kvh * a.G + walk.hk) * g.nblocks * g.ntile +
+          marked = __ldg(a.mask.bad + (static_cast<int64_t>(b) * a.hq + head0 + walk.hk) * g.nblocks * g.ntile +
                          walk.x);
       };
       if constexpr (MASK) {
@@ -437,7 +452,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // coordinates first, off the wait's critical path
         int head, q0, qlen, bq, qi, flags;
         if constexpr (MASK) {
-          head = kvh * a.G + walk.hk;
+          head = head0 + walk.hk;
           bq = walk.x / g.ntile;
           qi = walk.x - bq * g.ntile;
           q0 = bq * g.blk + qi * kTile;
@@ -667,7 +682,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     const bool owns_dv = grp < C::GROUPS / 2;
     const int acc_part = C::GROUPS == 2 ? 0 : (owns_dv ? grp : grp - C::GROUPS / 2) * C::ACC_COLS;
     const uint32_t acc_col = (owns_dv ? C::RV : C::RK) + acc_part;
-    float* acc_glob = (owns_dv ? a.dv_acc : a.dk_acc) + krow * D + acc_part;
+    const int64_t slice = MASK ? static_cast<int64_t>(a.batch) * a.S * a.hkv * split : 0;
+    float* acc_glob = (owns_dv ? a.dv_acc : a.dk_acc) + (slice + krow) * D + acc_part;
     const float acc_mul = owns_dv ? 1.f : a.scale;
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
@@ -1124,7 +1140,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
               x[v4 * 4 + 3] += y.w;
             }
           }
-          if constexpr (!STEP) {
+          if (!STEP && !(MASK && a.mask.splits > 1)) {
             __nv_bfloat16* dst = (owns_dv ? a.dv : a.dk) + krow * D + acc_part + cb * 32;
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4) {
@@ -1199,7 +1215,7 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   auto kern = ring_bwd_kernel<D, STEP, VARIANT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
-  const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(a.ring.nblocks) * a.ring.ntile;
+  const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(a.ring.nblocks) * a.ring.ntile * a.mask.splits;
   if (grid <= 0 || grid > 0x7fffffff) return LOONG_ERR_INVALID_ARG;
   const int t_first = 0, t_last = d.cp;
   if (!STEP) {
@@ -1278,6 +1294,10 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
   const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
   const int64_t kv_elems = d.batch * d.seqlen * d.hkv * d.head_dim;
   const bool step = d.mode != LOONG_MODE_FUSED;
+  if (mask && mask->splits > 1) {
+    dk_acc = mask->dk_parts;
+    dv_acc = mask->dv_parts;
+  }
   int st;
   cudaError_t e = bias || mask ? cudaSuccess : cudaMemsetAsync(dq_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -1300,7 +1320,8 @@ int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const voi
               : launch_bwd_v<kBwdPlain>(d, q, k, v, dout, dvec, dq_acc, dk, dv, dk_acc, dv_acc, stream, kv_recv,
                                         nullptr, nullptr, nullptr);
   if (st != LOONG_OK) return st;
-  if (!bias && (st = launch_f32_to_bf16(dq_acc, dq, q_elems, stream)) != LOONG_OK) return st;
+  const bool parts = mask && mask->splits > 1;
+  if (!bias && !parts && (st = launch_f32_to_bf16(dq_acc, dq, q_elems, stream)) != LOONG_OK) return st;
   if (step) {
     if ((st = launch_f32_to_bf16(dk_acc, dk, kv_elems, stream)) != LOONG_OK) return st;
     if ((st = launch_f32_to_bf16(dv_acc, dv, kv_elems, stream)) != LOONG_OK) return st;

@@ -136,6 +136,11 @@ struct MaskView {
   const uint8_t* bad = nullptr;  // backward: [B][hq][nblocks * ntile], tiles with rows to clear
   const __nv_bfloat16* v = nullptr;  // forward: V as given
   ScoreCap cap;
+  // Backward: blocks that share a key tile of a kv head, per_split query heads each.
+  // More than one: each leaves its fp32 dK and dV in a part of its own, [splits][the
+  // layout of K], and the caller adds them up and converts dq_acc.
+  int splits = 1, per_split = 0;
+  float *dk_parts = nullptr, *dv_parts = nullptr;
 };
 
 // The keys [x, y) that query t of sequence b sees; (0, 0) where none.

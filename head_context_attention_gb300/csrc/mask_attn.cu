@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 1216;                  // of a launch that strides over its data: 8 per SM
+constexpr int kSms = 152;                         // workspace sizes do not ask the device
 constexpr int64_t kMaxSeqlen = int64_t{1} << 30;  // a tile past the last token still has a 32-bit number
 // A capped logit is at most the cap; up to 2^20 the softmax's reference, rounded to
 // 24 bits, is off by at most 2^-3 in log2 units, which fp16 P has room for.
@@ -33,6 +34,11 @@ constexpr float kMinScale = 5.9604645e-8f, kMaxScale = 16777216.f;  // 2^-24, 2^
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Blocks of a launch that strides over n threads' work.
+unsigned blocks_for(int64_t n) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, kMaxBlocks)));
+}
 
 struct TileArgs {
   MaskView m;
@@ -176,6 +182,39 @@ __global__ void __launch_bounds__(kThreads) mask_bwd_prep_kernel(const __grid_co
   if (h == 0 && threadIdx.x < 32) sum_tile(a.tiles, static_cast<int64_t>(b) * g.nblocks * g.ntile + blockIdx.x);
 }
 
+// After the backward, where the query heads of a group went to several blocks: dQ
+// rounded, and the blocks' parts of dK and dV added up, in the order of the heads, and
+// rounded.
+struct FinishArgs {
+  const float4 *dq_acc, *dk_parts, *dv_parts;
+  uint4 *dq, *dk, *dv;
+  int64_t q_vecs, kv_vecs;  // of 8 elements
+  int splits;
+};
+__global__ void __launch_bounds__(kThreads) mask_finish_kernel(const __grid_constant__ FinishArgs a) {
+  auto pack = [](float4 x, float4 y) {
+    return make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+  };
+  auto add = [](float4 x, float4 y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < a.q_vecs + 2 * a.kv_vecs;
+       i += stride) {
+    if (i < a.q_vecs) {
+      a.dq[i] = pack(a.dq_acc[2 * i], a.dq_acc[2 * i + 1]);
+      continue;
+    }
+    const bool v = i >= a.q_vecs + a.kv_vecs;
+    const int64_t j = i - a.q_vecs - (v ? a.kv_vecs : 0);
+    const float4* parts = v ? a.dv_parts : a.dk_parts;
+    float4 x = parts[2 * j], y = parts[2 * j + 1];
+    for (int s = 1; s < a.splits; ++s) {
+      x = add(x, parts[2 * (s * a.kv_vecs + j)]);
+      y = add(y, parts[2 * (s * a.kv_vecs + j) + 1]);
+    }
+    (v ? a.dv : a.dk)[j] = pack(x, y);
+  }
+}
+
 int check_mask(const loong_attn_desc* d, const loong_attn_mask* m) {
   int st = loong_attn_check(d);
   if (st != LOONG_OK) return st;
@@ -204,8 +243,9 @@ loong_attn_desc one_block(loong_attn_desc d) {
 // The workspace: the plain pass's first, then the tiles' sums and, forward, the
 // shares of max |V|, backward, the marks of the query tiles.
 struct MaskWs {
-  size_t tiles, shares, bad, total;
+  size_t tiles, shares, bad, dk_parts, dv_parts, total;
   int64_t count;
+  int splits, per_split;
 };
 MaskWs mask_ws(const loong_attn_desc& d, int pass) {
   const RingGeom g = ring_geom(d);
@@ -220,6 +260,21 @@ MaskWs mask_ws(const loong_attn_desc& d, int pass) {
   } else {
     w.bad = at;
     at += up256(static_cast<size_t>(w.count) * d.hq);
+    // Query heads of a group per block: as many blocks as SMs, where key tiles are fewer.
+    // Training passes on the device, one block a key tile and several: 1K tokens of 4 + 2
+    // heads of 64 59 and 49 us, 858 of 30 + 5 of 128 123 and 82, 162 in six ring blocks of
+    // 56 + 7 of 64 173 and 101, twice 1990 of 6 + 3 of 64 139 and 116.
+    const int group = d.hq / d.hkv;
+    const int64_t blocks = w.count * d.hkv;
+    const int most = d.mode == LOONG_MODE_FUSED ? static_cast<int>(std::max<int64_t>(1, kSms / blocks)) : 1;
+    w.per_split = (group + std::min(most, group) - 1) / std::min(most, group);
+    w.splits = (group + w.per_split - 1) / w.per_split;
+    if (w.splits > 1) {
+      const size_t part = up256(static_cast<size_t>(w.splits) * d.batch * d.seqlen * d.hkv * d.head_dim * 4);
+      w.dk_parts = at;
+      w.dv_parts = at + part;
+      at += 2 * part;
+    }
   }
   w.total = at;
   return w;
@@ -281,10 +336,7 @@ int loong_attn_mask_fwd(const loong_attn_desc* desc, const loong_attn_mask* mask
   va.amax = reinterpret_cast<unsigned*>(base + L.amax);
   va.shares = reinterpret_cast<unsigned*>(base + w.shares);
   va.vecs = d->batch * d->seqlen * d->hkv * d->head_dim / 8;
-  auto blocks_for = [](int64_t n) {
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, kMaxBlocks)));
-  };
-  va.max_blocks = va.vecs <= kBlockV ? 0 : blocks_for(va.vecs / 2);
+  va.max_blocks = va.vecs <= kBlockV ? 0 : static_cast<int>(blocks_for(va.vecs / 2));
   const int64_t tile_blocks = (w.count + kThreads / 32 - 1) / (kThreads / 32);
   mask_fwd_prep_kernel<<<static_cast<unsigned>(std::max(va.max_blocks, 1) + tile_blocks), kThreads, 0, stream>>>(a, va);
   if ((st = check_launch()) != LOONG_OK) return st;
@@ -333,8 +385,26 @@ int loong_attn_mask_bwd(const loong_attn_desc* desc, const loong_attn_mask* mask
   else
     mask_bwd_prep_kernel<64><<<grid, kThreads, 0, stream>>>(a);
   if ((st = check_launch()) != LOONG_OK) return st;
-  a.tiles.m.bad = a.bad;
-  return run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, nullptr, nullptr, &a.tiles.m);
+  MaskView& m = a.tiles.m;
+  m.bad = a.bad;
+  m.splits = w.splits;
+  m.per_split = w.per_split;
+  m.dk_parts = reinterpret_cast<float*>(base + w.dk_parts);
+  m.dv_parts = reinterpret_cast<float*>(base + w.dv_parts);
+  st = run_attn_bwd(*d, q, k, v, o, o_res, lse, dout, dq, dk, dv, ws, stream, nullptr, nullptr, &m);
+  if (st != LOONG_OK || w.splits == 1) return st;
+  FinishArgs f;
+  f.dq_acc = reinterpret_cast<const float4*>(a.dq_acc);
+  f.dk_parts = reinterpret_cast<const float4*>(m.dk_parts);
+  f.dv_parts = reinterpret_cast<const float4*>(m.dv_parts);
+  f.dq = static_cast<uint4*>(dq);
+  f.dk = static_cast<uint4*>(dk);
+  f.dv = static_cast<uint4*>(dv);
+  f.q_vecs = d->batch * d->seqlen * d->hq * d->head_dim / 8;
+  f.kv_vecs = d->batch * d->seqlen * d->hkv * d->head_dim / 8;
+  f.splits = w.splits;
+  mask_finish_kernel<<<blocks_for(f.q_vecs + 2 * f.kv_vecs), kThreads, 0, stream>>>(f);
+  return check_launch();
 }
 
 }  // extern "C"

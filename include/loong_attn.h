@@ -439,6 +439,9 @@ LOONG_API int loong_attn_mask_check(const loong_attn_desc* desc, const loong_att
  * block; for the forward 1,216 words more, for the backward a byte for every
  * query tile and head.  Each part starts on a 256-byte boundary.  A FUSED
  * descriptor with the NATURAL layout counts as one of cp = hp = 1, one block.
+ * Where a FUSED backward's key tiles of 128 (of all blocks, kv heads and sequences)
+ * are 76 or fewer, the query heads of a group go to up to 152 / tiles blocks, each
+ * with fp32 values for the whole of dK and dV.
  */
 LOONG_API size_t loong_attn_mask_workspace_size(const loong_attn_desc* desc, const loong_attn_mask* mask, int pass);
 
