@@ -806,6 +806,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           uint32_t sv[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[e] = __float_as_uint(pv[0][e]);
+          if (!unmasked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen >> e & 1)) sv[e] = 0;
+          }
           cap_scores(sv, a.mask.cap);
 #pragma unroll
           for (int e = 0; e < 32; ++e) pv[0][e] = __uint_as_float(sv[e]);

@@ -503,10 +503,11 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
     bool ok = true;
     // MASK: the keys of this row (rows past the block see all, they are not stored)
     int2 see = make_int2(0, 0);
-    bool v_bad = false;
+    bool v_bad = false, stored = true;
     if constexpr (MASK) {
       const int tok = (h ? q1 : q0) + row;
-      see = tok < (bq + 1) * g.blk ? mask_range(a.mask, b, tok, a.S, g.causal) : make_int2(0, 0x7fffffff);
+      stored = tok < (bq + 1) * g.blk;
+      see = stored ? mask_range(a.mask, b, tok, a.S, g.causal) : make_int2(0, 0x7fffffff);
       v_bad = a.v_amax[1] != 0;
     }
     for (int j = 0; j < n; ++j, walk.advance()) {
@@ -604,8 +605,9 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
         }
       };
       // and -inf for those that the row does not see
+      auto seen = [&](int c) { return low_bits(see_hi - c) & ~low_bits(see_lo - c); };
       auto mask_columns = [&](uint32_t(&s)[32], int cb) {
-        const uint32_t bits = low_bits(see_hi - cb * 32) & ~low_bits(see_lo - cb * 32);
+        const uint32_t bits = seen(cb * 32);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (!(bits >> i & 1)) s[i] = __float_as_uint(-INFINITY);
@@ -636,7 +638,8 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
               if (cb * 32 + i > lim) sr[cb][i] = __float_as_uint(-INFINITY);
         }
       };
-      if constexpr (CAP) cap_tile<32>(tS, a.mask.cap);  // 64: 2.60 ms for 2.55 (softcap.cuh's case)
+      if constexpr (CAP)  // 64 columns at a time: 2.60 ms for 2.55 (softcap.cuh's case)
+        cap_tile<32>(tS, a.mask.cap, stored, masked, seen);
       load_s();
       // P = exp2(s*scale*log2e - ref + bias) for the whole tile, with the
       // columns in pairs on the paired fp32 pipe; returns this row's sum of P

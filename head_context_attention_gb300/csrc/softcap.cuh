@@ -62,16 +62,17 @@ __device__ __forceinline__ void cap_polynomial(uint32_t (&s)[N], const float (&c
 }
 
 // Scores s[0 .. N) (32-bit words that hold floats; N a multiple of 8) capped.  The
-// warp's lanes call it together.
+// warp's lanes call it together; which form they take goes by the lanes that count
+// and all of their scores, so those that are not seen are 0.
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap) {
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap, bool counts = true) {
   float m[4] = {};
 #pragma unroll
   for (int i = 0; i < N; i += 8)
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       m[u] = fmax3_abs(m[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
-  const float most = fmaxf(fmax3_abs(m[0], m[1], m[2]), m[3]);
+  const float most = counts ? fmaxf(fmax3_abs(m[0], m[1], m[2]), m[3]) : 0.f;
   if (__all_sync(0xffffffffu, most <= cap.half)) {
     cap_polynomial(s, cap.h);
   } else if (__all_sync(0xffffffffu, most <= cap.limit)) {
@@ -93,8 +94,9 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap
 // scores covers (0.58 ms), and the way through tensor memory (0.24).  Four more warps for
 // the cap alone, 2.63: the softmax warps then have 176 registers for 216, and every tile
 // one more barrier on its way.
-template <int N>
-__device__ __forceinline__ void cap_tile(uint32_t t, const ScoreCap& cap) {
+// masked: seen(c) has a bit for each of columns c .. c + 31.
+template <int N, typename Seen>
+__device__ __forceinline__ void cap_tile(uint32_t t, const ScoreCap& cap, bool counts, bool masked, Seen&& seen) {
 #pragma unroll 1
   for (int cb = 0; cb < 128; cb += N) {
     uint32_t s[N / 32][32], x[N];
@@ -103,7 +105,16 @@ __device__ __forceinline__ void cap_tile(uint32_t t, const ScoreCap& cap) {
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = s[i / 32][i % 32];
-    cap_scores(x, cap);
+    if (masked) {
+#pragma unroll
+      for (int u = 0; u < N / 32; ++u) {
+        const uint32_t bits = seen(cb + u * 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(bits >> i & 1)) x[u * 32 + i] = 0;
+      }
+    }
+    cap_scores(x, cap, counts);
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i / 32][i % 32] = x[i];
 #pragma unroll

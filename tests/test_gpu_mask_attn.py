@@ -204,18 +204,20 @@ def _poisoned(x, names, where, value):
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("seqlen,cp,docs", [(300, 1, (100, 120)), (398, 1, (150, 90)), (398, 2, (140, 90))])
-def test_padding_holds_anything(cuda_device, value, d, seqlen, cp, docs):
+@pytest.mark.parametrize("seqlen,cp,docs,cap", [(300, 1, (100, 120), 0.0), (398, 1, (150, 90), 20.0),
+                                                (398, 2, (140, 90), 0.0)])
+def test_padding_holds_anything(cuda_device, value, d, seqlen, cp, docs, cap):
     """Tokens behind the last document may hold anything: outputs and gradients of the others are the same bits (dQ,
     which is added up in any order, to rounding), their own are 0."""
     w = inputs.Workload("pad", seqlen, 4, 2, d, 1, cp, cp, 1, True, placement=0)
     x = inputs.make_inputs(w, device="cuda")
+    x["q"] = x["q"] * 8  # with the cap, in reach of every form of it
     r = ops.document_ranges([list(docs)], seqlen)
     end = sum(docs)
-    clean = _run(w, x, r, 0.0)
+    clean = _run(w, x, r, cap)
     y = _poisoned(x, ("q", "k", "v", "do"), (slice(None), slice(end, None)), value)
-    got = _run(w, y, r, 0.0)
-    _check(w, x, r, 0.0, got)
+    got = _run(w, y, r, cap)
+    _check(w, x, r, cap, got)
     for i, (a, b) in enumerate(zip(clean, got)):
         if i != 2:
             assert torch.equal(a.view(torch.int16 if a.dtype == torch.bfloat16 else torch.int32),
