@@ -159,6 +159,8 @@ struct BwdPiece {
 // and dO by the producer, in the tiles that the launch before marked.  Instead the
 // row's own P is NaN, for those that see it.
 // Where key tiles do not fill the SMs, the query heads of a group go to several blocks.
+// 32 + 8 heads of 128: 16K tokens in one piece 4.98 ms (K2's rate), capped 5.9; 64K in
+// documents of about 8K 14.7 ms.
 enum BwdVariant { kBwdPlain, kBwdBias, kBwdMask, kBwdCap };
 
 // The query tiles, in natural order, that see a block's keys [k0, k1), a word of 32

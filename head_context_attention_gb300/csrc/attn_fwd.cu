@@ -158,6 +158,9 @@ constexpr float kMaxMiddle = 32.0f;  // log2 units
 // there was such a value (v_amax[1]) the scores of its key become NaN for the rows
 // that see it.
 // Pairs of heads and of tiles are formed as with a bias.
+// 32 + 8 heads of 128: 32K tokens in one piece 5.1-5.4 ms (1.6-1.7 PFLOP/s, as without a
+// mask), in documents of about 4K 1.34 ms, where a block has 8 to 16 tiles and its start
+// and end, about 10 us, weigh.
 enum FwdVariant { kFwdPlain, kFwdBias, kFwdMask, kFwdCap };
 
 struct FwdPiece {

