@@ -1219,9 +1219,8 @@ int launch_bwd_t(const loong_attn_desc& d, const void* q, const void* k, const v
   a.dbias_part = dbias_part;
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
-  auto kern = ring_bwd_kernel<D, STEP, VARIANT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return cuda_fail(e);
+  constexpr auto kern = ring_bwd_kernel<D, STEP, VARIANT>;
+  if ((st = kernel_ready<kern>(C::SMEM_BYTES, 0)) != LOONG_OK) return st;
   const int64_t grid = d.batch * d.hkv * static_cast<int64_t>(a.ring.nblocks) * a.ring.ntile * a.mask.splits;
   if (grid <= 0 || grid > 0x7fffffff) return LOONG_ERR_INVALID_ARG;
   const int t_first = 0, t_last = d.cp;

@@ -879,16 +879,9 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
   a.err = device_error_word();
   if (!a.err) return LOONG_ERR_CUDA;
 
-  auto kern = ring_fwd_kernel<D, STEP, VARIANT, SLOTS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return cuda_fail(e);
+  constexpr auto kern = ring_fwd_kernel<D, STEP, VARIANT, SLOTS>;
   constexpr int threads = VARIANT != kFwdPlain ? C::SPLIT_THREADS : C::THREADS;
-  if constexpr (VARIANT != kFwdPlain) {
-    // the register split draws on what the block starts with: less would wait for ever
-    cudaFuncAttributes at;
-    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return cuda_fail(e);
-    if (at.numRegs < C::SPLIT_REGS) return LOONG_ERR_UNSUPPORTED;
-  }
+  if ((st = kernel_ready<kern>(C::SMEM_BYTES, VARIANT != kFwdPlain ? C::SPLIT_REGS : 0)) != LOONG_OK) return st;
   const int64_t blocks = static_cast<int64_t>(rank_end - rank_begin) * rank_parts(a.ring);
   const int64_t per_kvh = SLOTS == 1 ? blocks * a.ring.ntile * a.G
                           : BIAS || MASK ? blocks * (a.ring.ntile * (a.G / 2) + (a.G & 1) * ((a.ring.ntile + 1) / 2))

@@ -9,6 +9,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <cstdio>
 
 #include "../../include/loong_attn.h"
@@ -153,6 +154,26 @@ __device__ __forceinline__ int2 mask_range(const MaskView& m, int b, int t, int 
 
 // SMs of the current device.
 int num_sms();
+
+// A kernel's dynamic shared memory allowed and its registers per thread checked
+// (a register split draws on what the block starts with: less would wait for ever), once
+// a device.
+template <auto Kern>
+int kernel_ready(int smem, int min_regs) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64) return LOONG_ERR_UNSUPPORTED;
+  if (done[dev].load(std::memory_order_acquire)) return LOONG_OK;
+  if ((e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+    return cuda_fail(e);
+  cudaFuncAttributes at;
+  if ((e = cudaFuncGetAttributes(&at, Kern)) != cudaSuccess) return cuda_fail(e);
+  if (at.numRegs < min_regs) return LOONG_ERR_UNSUPPORTED;
+  done[dev].store(true, std::memory_order_release);
+  return LOONG_OK;
+}
 
 // A launch whose blocks may start, up to previous_launch_wait, while the kernel
 // before it in the stream still runs (next_launch_go there).

@@ -950,15 +950,8 @@ int launch_paged(const loong_paged_desc& d, const PagedArgs& a, const AppendArgs
   const int copy_blocks = n.k ? std::min((d.tokens + kPrepThreads / 32 - 1) / (kPrepThreads / 32), 2 * sms) : 0;
   paged_prep_kernel<<<1 + copy_blocks, kPrepThreads, 0, stream>>>(a, n, SLOTS * a.per_slot);
   if ((st = check_launch()) != LOONG_OK) return st;
-  auto kern = paged_attn_kernel<D, SLOTS, CAP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if constexpr (C::SPLIT) {
-    // the register split draws on what the block starts with: less would wait for ever
-    cudaFuncAttributes at;
-    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return cuda_fail(e);
-    if (at.numRegs < C::SPLIT_REGS) return LOONG_ERR_UNSUPPORTED;
-  }
+  constexpr auto kern = paged_attn_kernel<D, SLOTS, CAP>;
+  if ((st = kernel_ready<kern>(C::SMEM_BYTES, C::SPLIT ? C::SPLIT_REGS : 0)) != LOONG_OK) return st;
   return launch_dependent(kern, dim3(sms), C::THREADS, C::SMEM_BYTES, stream, mq, mk, mv, a);
 }
 

@@ -680,17 +680,25 @@ def _mask_problem_of(w, score_cap, mode, layout):
     return (_kept_mask_problem if type(w) is Workload else _mask_problem)(w, float(score_cap), mode, layout)
 
 
-def _mask_tensors(w, layout, key_range, lse, **bf16):
-    """Refuse what the C entry cannot see of the tensors below; ``bf16`` by name, k
-    and v of the key heads, the others of the query heads, o_res may be None."""
-    device = bf16["q"].device
-    for n, t in bf16.items():
+def _mask_tensors(w, layout, key_range, lse, q, k, v, **more):
+    """Refuse what the C entry cannot see of the tensors: k and v of the key heads, q
+    and the others (by name, o_res may be None) of the query heads."""
+    device, bf16 = q.device, torch.bfloat16
+    queries, keys = _attn_shape(w, w.hq, layout), _attn_shape(w, w.hkv, layout)
+    # short sequences feel the checks' own time: in one go, one after the other only to say which
+    if not (q.dtype is k.dtype is v.dtype is bf16 and q.shape == queries and k.shape == v.shape == keys and
+            q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and k.device == v.device == device):
+        _contiguous("q", q, queries, bf16, device)
+        _contiguous("k", k, keys, bf16, device)
+        _contiguous("v", v, keys, bf16, device)
+    for n, t in more.items():
         if t is not None or n != "o_res":
-            _contiguous(n, t, _attn_shape(w, w.hkv if n in ("k", "v") else w.hq, layout), torch.bfloat16, device)
+            _contiguous(n, t, queries, bf16, device)
     if lse is not None:
         _contiguous("lse", lse, (w.batch, w.hq, w.seqlen), torch.float32, device)
     if key_range is not None:
         _contiguous("key_range", key_range, (w.batch, w.seqlen, 2), torch.int32, device)
+    return device
 
 
 def attn_mask_fwd(w, q, k, v, key_range=None, score_cap=0.0, mode=MODE_FUSED, stream=None, layout=LAYOUT_NATURAL,
@@ -701,8 +709,7 @@ def attn_mask_fwd(w, q, k, v, key_range=None, score_cap=0.0, mode=MODE_FUSED, st
     score_cap) (0: not).  Returns (o, lse, o_res); o_res is None when ``res`` is
     false."""
     desc, nbytes, _ = _mask_problem_of(w, score_cap, mode, layout)
-    _mask_tensors(w, layout, key_range, None, q=q, k=k, v=v)
-    device = q.device
+    device = _mask_tensors(w, layout, key_range, None, q, k, v)
     where, stream = _on(device, stream)
     with where:
         o = torch.empty_like(q)
@@ -719,11 +726,11 @@ def attn_mask_bwd(w, q, k, v, o, lse, do, key_range=None, score_cap=0.0, o_res=N
     desc, _, nbytes = _mask_problem_of(w, score_cap, mode, layout)
     if not isinstance(lse, torch.Tensor):
         raise TypeError("lse must be a tensor")
-    _mask_tensors(w, layout, key_range, lse, q=q, k=k, v=v, o=o, do=do, o_res=o_res)
-    where, stream = _on(q.device, stream)
+    device = _mask_tensors(w, layout, key_range, lse, q, k, v, o=o, do=do, o_res=o_res)
+    where, stream = _on(device, stream)
     with where:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         loong_attn_mask_bwd(desc, make_mask(key_range, score_cap), q, k, v, o, o_res, lse, do, dq, dk, dv, ws, stream)
     return dq, dk, dv
 
