@@ -241,7 +241,9 @@ static FwdScratch fwd_scratch(const loong_attn_desc& d, void* ws, void* o_res) {
 int run_attn_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
                  void* o_res, void* ws, cudaStream_t stream, const BiasView* bias, const MaskView* mask) {
   const FwdScratch sc = fwd_scratch(d, ws, o_res);
-  if (d.mode == LOONG_MODE_FUSED) return launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias, mask);
+  if (d.mode == LOONG_MODE_FUSED)
+    return mask ? launch_mask_fwd(d, q, k, o, lse, sc, *mask, stream)
+                : launch_fwd(d, q, k, v, o, lse, sc, stream, 0, -1, bias);
   const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
   cudaError_t e = cudaMemsetAsync(sc.o_acc, 0, static_cast<size_t>(q_elems) * 4, stream);
   if (e != cudaSuccess) return cuda_fail(e);

@@ -148,19 +148,16 @@ static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bou
 // logit is off by at most 2^-24 * 22, as one of that size is anyway.
 constexpr float kMaxMiddle = 32.0f;  // log2 units
 
-// MASK gives every query a range of keys and may cap the scores (softcap.cuh;
-// scale_log2 is then the cap's).  A block walks the tiles between the first and the
+// MASK (only where STEP; mask_fwd.cu is the rest) gives every query a range of keys and may
+// cap the scores (softcap.cuh; scale_log2 is then the cap's).  A block walks the tiles between the first and the
 // last key that any of its rows sees (RangeWalk), which the launch before summed up
-// for it; a block whose rows see nothing only writes that.  A softmax warp some of
+// for it; a block whose rows see nothing in a step leaves it out.  A softmax warp some of
 // whose rows do not see a whole tile masks it by four words of bits a row.  Columns of
 // masked keys are replaced, so what the keys hold does not matter; V, whose rows a
 // product adds up with P = 0, is 0 in its copy where it is not finite, and where
 // there was such a value (v_amax[1]) the scores of its key become NaN for the rows
 // that see it.
 // Pairs of heads and of tiles are formed as with a bias.
-// 32 + 8 heads of 128: 32K tokens in one piece 5.1-5.4 ms (1.6-1.7 PFLOP/s, as without a
-// mask), in documents of about 4K 1.34 ms, where a block has 8 to 16 tiles and its start
-// and end, about 10 us, weigh.
 enum FwdVariant { kFwdPlain, kFwdBias, kFwdMask, kFwdCap };
 
 struct FwdPiece {
@@ -172,7 +169,7 @@ struct FwdPiece {
 //
 // With a cap the softmax warps cap a tile where it lies in tensor memory first (softcap.cuh).
 //
-// SLOTS = 1 (with BIAS or MASK): one head's query tile per block, where even such blocks do
+// SLOTS = 1 (with BIAS): one head's query tile per block, where even such blocks do
 // not fill the SMs.  The second slot's warps idle; the scores of the next tile, in
 // the other buffer, are computed while the softmax works.
 template <int D, bool STEP, int VARIANT, int SLOTS = 2>
@@ -263,7 +260,6 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
 
   std::conditional_t<MASK, RangeWalk, KvWalk> walk;
   if constexpr (MASK) {
-    previous_launch_wait();
     const int4* tiles = a.mask.tiles + (static_cast<int64_t>(b) * g.nblocks + bq) * g.ntile;
     const int4 t0 = tiles[qi0], t1 = tiles[qi];
     walk.init(g, block_owner(g, bq), a.t_begin, a.t_end, min(t0.x, t1.x), max(t0.y, t1.y));
@@ -271,21 +267,7 @@ __global__ void __launch_bounds__(VARIANT != kFwdPlain ? FwdCfg<D>::SPLIT_THREAD
     walk.init(g, bq, qi, a.t_begin, a.t_end);
   }
   const int n = walk.total();
-  if (n == 0) {  // uniform over the CTA: nothing of this tile in these steps
-    if constexpr (MASK && !STEP) {  // no row sees a key
-      for (int i = threadIdx.x; i < SLOTS * kTile * (D / 8); i += C::SPLIT_THREADS) {
-        const int h = i / (kTile * (D / 8)), row = i / (D / 8) % kTile, part = i % (D / 8);
-        const int qh = h ? q1 : q0, head = h ? head1 : head0;
-        if (row >= min(kTile, (bq + 1) * g.blk - qh)) continue;
-        const int64_t qv = a.lay.vec(b, qh + row, head, a.hq);
-        if (!in_bounds(qv >= 0 && qv < static_cast<int64_t>(a.batch) * a.S * a.hq, a.err)) continue;
-        reinterpret_cast<uint4*>(a.o + qv * D)[part] = make_uint4(0, 0, 0, 0);
-        if (a.o_res) reinterpret_cast<uint4*>(a.o_res + qv * D)[part] = make_uint4(0, 0, 0, 0);
-        if (part == 0) a.lse[(static_cast<int64_t>(b) * a.hq + head) * a.S + qh + row] = -INFINITY;
-      }
-    }
-    return;
-  }
+  if (n == 0) return;  // uniform over the CTA: nothing of this tile in these steps
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -892,12 +874,9 @@ int launch_fwd_t(const loong_attn_desc& d, const void* q, const void* k, void* o
     a.t_begin = 0;
     a.t_end = d.cp;
     record_start(stream);
-    if constexpr (MASK)
-      st = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, C::SMEM_BYTES, stream, mq, mk, mv, a);
-    else
-      kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
+    kern<<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(mq, mk, mv, a);
     record_stop(stream);
-    return st == LOONG_OK ? check_launch() : st;
+    return check_launch();
   }
   if (is_copy_mode(d)) {
     // receive buffers K0, K1, V0, V1, each the size of K
@@ -939,7 +918,7 @@ template <int VARIANT>
 int launch_fwd_v(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
                  cudaStream_t stream, int rank_begin, int rank_end, const BiasView* bias, const MaskView* mask) {
   const bool step = d.mode != LOONG_MODE_FUSED;
-  if constexpr (VARIANT != kFwdPlain) {
+  if constexpr (VARIANT == kFwdBias) {
     const RingGeom g = ring_geom(d);
     if (!step && fwd_one_slot(d.batch * d.hq * g.nblocks * g.ntile, num_sms())) {
       if (d.head_dim == 128)
@@ -948,12 +927,16 @@ int launch_fwd_v(const loong_attn_desc& d, const void* q, const void* k, void* o
         return launch_fwd_t<64, false, VARIANT, 1>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
     }
   }
-  if (d.head_dim == 128)
-    return step ? launch_fwd_t<128, true, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask)
-                : launch_fwd_t<128, false, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
-  if (d.head_dim == 64)
-    return step ? launch_fwd_t<64, true, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask)
-                : launch_fwd_t<64, false, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
+  if (step && d.head_dim == 128)
+    return launch_fwd_t<128, true, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
+  if (step && d.head_dim == 64)
+    return launch_fwd_t<64, true, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
+  if constexpr (VARIANT != kFwdMask && VARIANT != kFwdCap) {  // these have a kernel of their own (mask_fwd.cu)
+    if (d.head_dim == 128)
+      return launch_fwd_t<128, false, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
+    if (d.head_dim == 64)
+      return launch_fwd_t<64, false, VARIANT>(d, q, k, o, lse, sc, stream, rank_begin, rank_end, bias, mask);
+  }
   return LOONG_ERR_UNSUPPORTED;
 }
 

@@ -26,7 +26,7 @@ constexpr int fwd_score_buffers(int head_dim, int slots) {
   return room < 2 * slots ? room : 2 * slots;
 }
 
-// With a bias, blocks of one slot where `tiles` query tiles of single heads find an
+// With a bias or a mask, blocks of one slot where `tiles` query tiles of single heads find an
 // SM each: a block takes two thirds of a two-slot block's time, so they pay in one
 // round only.  One and two slots, 4K tokens of 4 heads of 128 (128 and 64 blocks)
 // 43.0 and 65.5 us, of 64 38.9 and 49.0, 2K of 8 + 2 heads of 64 26.6 and 31.0, 512

@@ -136,6 +136,7 @@ struct MaskView {
   const int4* tiles = nullptr;
   const uint8_t* bad = nullptr;  // backward: [B][hq][nblocks * ntile], tiles with rows to clear
   const __nv_bfloat16* v = nullptr;  // forward: V as given
+  int* counter = nullptr;            // FUSED forward: items taken, cleared
   ScoreCap cap;
   // Backward: blocks that share a key tile of a kv head, per_split query heads each.
   // More than one: each leaves its fp32 dK and dV in a part of its own, [splits][the
@@ -200,6 +201,9 @@ int launch_dependent(void (*kern)(Params...), dim3 grid, unsigned threads, size_
 int launch_fwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, void* o,
                float* lse, const FwdScratch& sc, cudaStream_t stream, int rank_begin = 0, int rank_end = -1,
                const BiasView* bias = nullptr, const MaskView* mask = nullptr);
+// The masked forward in FUSED mode; V's fp16 copy and the tiles' sums are there already.
+int launch_mask_fwd(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
+                    const MaskView& mask, cudaStream_t stream);
 // o_res: the forward's residual of O, or null (D from O alone).  With a bias the
 // row statistics are in dvec and dq_acc is zeroed already, and dq_acc is left to
 // the caller to convert; with a mask the former two.

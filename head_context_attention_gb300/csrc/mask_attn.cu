@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kThreads) mask_fwd_prep_kernel(const __grid_co
     v16_first_launch<kThreads, true>(v, blockIdx.x);
     return;
   }
+  if (id == 0 && threadIdx.x == 0) *a.m.counter = 0;
   const int64_t x = static_cast<int64_t>(id) * (kThreads / 32) + threadIdx.x / 32;
   if (x < a.count) sum_tile(a, x);
 }
@@ -244,7 +245,7 @@ loong_attn_desc one_block(loong_attn_desc d) {
 // The workspace: the plain pass's first, then the tiles' sums and, forward, the
 // shares of max |V|, backward, the marks of the query tiles.
 struct MaskWs {
-  size_t tiles, shares, bad, dk_parts, dv_parts, total;
+  size_t tiles, shares, counter, bad, dk_parts, dv_parts, total;
   int64_t count;
   int splits, per_split;
 };
@@ -258,6 +259,8 @@ MaskWs mask_ws(const loong_attn_desc& d, int pass) {
   if (pass == 0) {
     w.shares = at;
     at += up256(kMaxBlocks * 4);
+    w.counter = at;
+    at += up256(4);
   } else {
     w.bad = at;
     at += up256(static_cast<size_t>(w.count) * d.hq);
@@ -330,6 +333,7 @@ int loong_attn_mask_fwd(const loong_attn_desc* desc, const loong_attn_mask* mask
   uint8_t* base = static_cast<uint8_t*>(ws);
   TileArgs a = tile_args(*d, *mask, w, base);
   a.m.v = static_cast<const __nv_bfloat16*>(v);
+  a.m.counter = reinterpret_cast<int*>(base + w.counter);
   const FwdWsLayout L = fwd_ws_layout(*d);
   VArgs va;
   va.v = static_cast<const uint4*>(v);

@@ -12,7 +12,7 @@ from oracle import mask as omask
 from tests.helpers import to64
 from tests.test_gpu_checked import _library
 from tests.test_gpu_layout import _within_one_bf16_spacing
-from tests.test_gpu_mask_attn import _make, _pack, _run
+from tests.test_gpu_mask_attn import _check, _make, _pack, _run
 from tests.test_gpu_paged_attn import _Setup
 
 pytestmark = pytest.mark.gpu
@@ -76,6 +76,29 @@ def test_long_sequence_of_documents(cuda_device):
     pad = int(starts[-1])
     assert bool((out[0][0, pad:] == 0).all()) and bool(torch.isneginf(out[1][0, :, pad:]).all())
     assert all(bool((g[0, pad:] == 0).all()) for g in out[2:])
+
+
+@pytest.mark.parametrize("B,S,hq,hkv,d,cp,causal,cap", [
+    (14, 900, 6, 2, 64, 1, True, 0.0), (14, 900, 6, 2, 128, 1, True, 15.0), (20, 500, 8, 4, 128, 2, False, 0.0),
+    (9, 700, 16, 2, 64, 1, False, 30.0), (40, 130, 5, 5, 128, 1, True, 0.0)])
+def test_more_tiles_than_multiprocessors(cuda_device, B, S, hq, hkv, d, cp, causal, cap):
+    """Several query tiles a block one after the other, some of which see nothing in between."""
+    w = inputs.Workload("many", S, hq, hkv, d, 1, cp, cp, 1, True, placement=0, batch=B, causal=causal)
+    x = inputs.make_inputs(w, device="cuda")
+    rng = np.random.default_rng(S)
+    docs = [[] if b % 3 == 1 else [int(n) for n in rng.integers(1, S // 3, 2 + b % 2)] for b in range(B)]
+    r = ops.document_ranges(docs, S, causal=causal)
+    out = _run(w, x, r, cap)
+    _check(w, x, r, cap, out)
+    # another order of the blocks, and padding that is not finite, change no bit
+    pad = torch.zeros((B, S), dtype=torch.bool)
+    for b, lengths in enumerate(docs):
+        pad[b, sum(lengths):] = True
+    x = {n: t.masked_fill(pad.cuda()[..., None, None], float("nan")) for n, t in x.items()}
+    for _ in range(3):
+        again = _run(w, x, r, cap)
+        for i in (0, 1, 3, 4):
+            assert torch.equal(_bits(again[i]), _bits(out[i])), i
 
 
 def test_pool_past_32_bits(cuda_device):
