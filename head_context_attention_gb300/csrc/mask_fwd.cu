@@ -17,7 +17,7 @@
 // the light ones come last; a kv head after the other took 1.25 ms, prefixes of 2 x 4K
 // with 16 heads 275 us for 228.  What bounds an item is the softmax's exponentials
 // (1.70 PFLOP/s at 32K in one piece, as without a mask) and, short, its ends: first scores
-// and last rows, some 3 us that nothing else of the SM's covers.
+// and last rows, some 4 us that nothing else of the SM's covers.
 // SLOTS = 1: one head's tile an item, where even those do not fill the SMs.
 //
 // An item walks the key tiles between the first and the last key that any of its rows

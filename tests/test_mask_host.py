@@ -57,7 +57,7 @@ def test_mask_workspace_sizes(loong_lib, mode, seqlen):
         base = _desc(mode=mode, seqlen=seqlen, **one) if whole else d
         tiles = -(-seqlen // 128) if whole else 8 * -(-(seqlen // 8) // 128)
         assert ops.loong_attn_mask_workspace_size(d, m, 0) == \
-            up(ops.loong_attn_workspace_size(base, 0)) + up(16 * tiles) + up(4 * 1216)
+            up(ops.loong_attn_workspace_size(base, 0)) + up(16 * tiles) + up(4 * 1216) + up(4)
         # 16 key tiles' blocks for 152 SMs: the two query heads of a group go to two, each with a part of dK and dV
         parts = 2 * up(2 * 4 * seqlen * W.hkv * W.head_dim) if mode == ops.MODE_FUSED else 0
         assert ops.loong_attn_mask_workspace_size(d, m, 1) == \
