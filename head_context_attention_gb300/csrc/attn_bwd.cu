@@ -271,8 +271,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     idx /= a.mask.splits;
   }
   const int nkt = g.nblocks * g.ntile;
-  const int r = idx % nkt;
-  idx /= nkt;
+  // MASK: all kv heads of all sequences at one key tile, so that the light ones come last (a training
+  // pass of 16K tokens of 32 + 8 heads of 128 with a cap 8.26 -> 7.84 ms, prefixes of 2 x 4K 790 -> 720 us)
+  const int heads = MASK ? a.batch * a.hkv : nkt;
+  const int r = MASK ? idx / heads : idx % nkt;
+  idx = MASK ? idx % heads : idx / nkt;
   const int kvh = idx % a.hkv;
   const int b = idx / a.hkv;
   const int bk = r / g.ntile;
