@@ -608,7 +608,13 @@ int launch_t(const loong_attn_desc& d, const void* q, const void* k, void* o, fl
 int launch_mask_fwd(const loong_attn_desc& d, const void* q, const void* k, void* o, float* lse, const FwdScratch& sc,
                     const MaskView& mask, cudaStream_t stream) {
   const RingGeom g = ring_geom(d);
-  const bool one = fwd_one_slot(d.batch * d.hq * g.nblocks * g.ntile, num_sms());
+  // One slot where single tiles find an SM each (fwd_jobs.h), and up to two tiles an SM where
+  // they are uneven, the light ones filling up: causal rows of 2K and 4K tokens without ranges,
+  // two slots and one, 192 tiles of 64 with a cap 47.5 and 36.4 us, 288 48.7 and 48.0, of 128 57.3
+  // and 50.0, 256 of 32 tiles a row without one 63 and 52.  Ranges may make every tile short, and the ends of
+  // twice the items weigh more (documents of about 128, 192 tiles, 21.5 and 23.5 us).
+  const int rounds = !mask.range && d.causal ? 2 : 1;
+  const bool one = fwd_one_slot(d.batch * d.hq * g.nblocks * g.ntile, rounds * num_sms());
   auto launch = [&](auto dim, auto slots) {
     constexpr int D = decltype(dim)::value, SLOTS = decltype(slots)::value;
     return mask.cap.inv > 0.f ? launch_t<D, SLOTS, true>(d, q, k, o, lse, sc, mask, stream)

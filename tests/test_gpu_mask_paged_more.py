@@ -101,6 +101,17 @@ def test_more_tiles_than_multiprocessors(cuda_device, B, S, hq, hkv, d, cp, caus
             assert torch.equal(_bits(again[i]), _bits(out[i])), i
 
 
+@pytest.mark.parametrize("B,S,hq,hkv,d,cap", [(4, 900, 6, 2, 64, 20.0), (2, 1500, 9, 3, 128, 5.0), (5, 777, 8, 8, 64, 0.0)])
+def test_two_uneven_tiles_a_multiprocessor(cuda_device, B, S, hq, hkv, d, cap):
+    w = inputs.Workload("uneven", S, hq, hkv, d, 1, 1, 1, 1, True, placement=0, batch=B)
+    x = inputs.make_inputs(w, device="cuda")
+    out = _run(w, x, None, cap)
+    _check(w, x, None, cap, out)
+    again = _run(w, x, None, cap)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(_bits(again[i]), _bits(out[i])), i
+
+
 def test_pool_past_32_bits(cuda_device):
     """A pool of more than 2^32 bytes and 2^31 elements, the sequences' pages at its end."""
     hkv, d, page = 8, 128, 256
