@@ -387,7 +387,12 @@ __global__ void __launch_bounds__(MaskFwdCfg<D, SLOTS>::THREADS, 1)
         }
         continue;
       }
-      const int2 see = stored ? mask_range(a.mask, x.b, tok, a.S, g.causal) : make_int2(0, 0x7fffffff);
+      int2 see = stored ? mask_range(a.mask, x.b, tok, a.S, g.causal) : make_int2(0, 0);
+      // a row that sees nothing (padding) goes along as if it saw all, so that its warp does not
+      // mask for its sake, and its result is dropped: 2 x 1990 tokens less some padding, every key,
+      // 6 + 3 heads of 64, 48.4 -> 30.7 us, with a cap 78 -> 53 (documents without: 1 % slower)
+      constexpr int kAll = 0x7fffffff;
+      if (see.x >= see.y) see = make_int2(0, kAll);
       RangeWalk walk;
       walk.init(g, 0, 0, g.cp, x.kmin, x.kmax);
       float m_run = -INFINITY, l_run = 0.f;
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(MaskFwdCfg<D, SLOTS>::THREADS, 1)
             }
           }
         };
-        if constexpr (CAP) cap_tile<32>(tS, a.mask.cap, stored, masked, seen);
+        if constexpr (CAP) cap_tile<32>(tS, a.mask.cap, see.y != kAll, masked, seen);
         load_s();
         // P = exp2(s*scale*log2e - ref + bias) for the whole tile; returns this row's sum of
         // P (l carries the factor 2^bias as well)
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(MaskFwdCfg<D, SLOTS>::THREADS, 1)
       // ---------------------------------------------------------- the item's rows
       // l_run and O carry 2^kPBias; O also carries V's 2^-e.  A row without keys has l_run
       // = 0, and one that met a NaN keeps it (in its LSE for the gradient as well)
-      const bool any = l_run != 0.f;
+      const bool any = see.y != kAll && l_run != 0.f;
       const float inv = any ? __int_as_float((127 + v16_shift(*a.v_amax)) << 23) / l_run : 0.f;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
@@ -524,6 +529,10 @@ __global__ void __launch_bounds__(MaskFwdCfg<D, SLOTS>::THREADS, 1)
           float y[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(ov[e]) * inv;
+          if (!any) {  // whatever its Q held
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = 0.f;
+          }
 #pragma unroll
           for (int v4 = 0; v4 < 4; ++v4) {
             uint32_t w[4];
