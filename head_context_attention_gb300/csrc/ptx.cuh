@@ -374,6 +374,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// 1 / x to a step of fp32; 0 for infinity.
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // max(a, b, c) in one instruction (sm_100 family); exact, like fmaxf twice.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;

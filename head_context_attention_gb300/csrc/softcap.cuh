@@ -3,15 +3,18 @@
 //
 // A raw score s (the product of the matrix instructions) becomes s' = tanh(inv s) /
 // inv, inv = scale / cap, and the rest of a kernel goes on with s' where it had s.
-// What counts is the absolute error of the tangent: times the cap it is the logit's.
+// It is within 2^-19 of itself, or 2^-21 of a cap of up to 64 (score_cap.h): the cap may be
+// far above the scores.
 //
 // Scores within the polynomials' reach (score_cap.h) are formed in pairs: 7 paired
 // operations for two scores up to |inv s| = 1, 5 up to 1/2, where most are; the fp32 pipe
 // takes 14 and 10 cycles for them, the matrix instructions 8 at head dimension 128,
 // exponentials and sums 6.  (A third polynomial up to 1/4: 4 % for the forward where
 // scores stay there, 3 % against it elsewhere and in the backward.)  A warp whose scores
-// pass 1 takes 1 - 2 / (1 + e^2x), two more special functions a score, off by at most
-// 4e-7.
+// pass 1 takes 1 - 2 / (1 + e^2x), two more special functions a score, and under caps above
+// 64 the shorter polynomial for those of them below 1/2.  (For every cap: 12 % for the
+// forward where scores pass it, 20 % for a chunk over pages, and 2 to 3 % for the backward
+// everywhere.)
 #pragma once
 
 #include "ptx.cuh"
@@ -26,9 +29,10 @@ __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
   return d;
 }
 
-// One score by the exponential.
+// One score where the polynomials do not reach (score_cap.h).
+template <bool NEAR>
 __device__ __forceinline__ float cap_score(float s, const ScoreCap& cap) {
-  return fmaf(__fdividef(-2.f, 1.f + fast_exp2(s * cap.inv * 2.8853900817779268f)), cap.rinv, cap.rinv);  // 2 log2 e
+  return cap_far_score<NEAR>(s, cap, [](float a) { return fast_exp2(a); }, [](float a) { return fast_rcp(a); });
 }
 
 // s (1 + y (c[0] + y (c[1] + ..))), y = s^2, of s[0 .. N), N a multiple of 8.
@@ -77,9 +81,12 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap
     cap_polynomial(s, cap.h);
   } else if (__all_sync(0xffffffffu, most <= cap.limit)) {
     cap_polynomial(s, cap.c);
+  } else if (!cap.near) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(cap_score<false>(__uint_as_float(s[i]), cap));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(cap_score(__uint_as_float(s[i]), cap));
+    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(cap_score<true>(__uint_as_float(s[i]), cap));
   }
 }
 

@@ -447,8 +447,8 @@ LOONG_API size_t loong_attn_mask_workspace_size(const loong_attn_desc* desc, con
 
 /*
  * loong_attn_fwd with the mask: same arguments, layouts, modes and accuracy (a
- * capped logit is off by at most 4e-7 of the cap more).  ws needs
- * loong_attn_mask_workspace_size(desc, mask, 0) bytes.
+ * capped logit is off by at most 2^-19 of itself more, or 2^-21 of a cap of up to 64).
+ * ws needs loong_attn_mask_workspace_size(desc, mask, 0) bytes.
  */
 LOONG_API int loong_attn_mask_fwd(const loong_attn_desc* desc, const loong_attn_mask* mask, const void* q,
                                   const void* k, const void* v, void* o, float* lse, void* o_res, void* ws,

@@ -1,0 +1,27 @@
+"""Host-side checks of the masked and the paged attention where they once went wrong."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(HERE, "..", "head_context_attention_gb300", "csrc")
+
+
+def _native(tmp_path, name):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    exe = tmp_path / name
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-I", CSRC, os.path.join(HERE, "native", name + ".cpp"), "-o",
+                        str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    return r.stdout
+
+
+def test_capped_scores_keep_their_own_precision(tmp_path):
+    """A capped score is off by a part of itself, not of a large cap."""
+    _native(tmp_path, "score_cap_relative")
