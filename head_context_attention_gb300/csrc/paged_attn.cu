@@ -47,6 +47,7 @@
 
 #include "fwd_jobs.h"
 #include "internal.h"
+#include "paged_plan.h"
 #include "ptx.cuh"
 #include "softcap.cuh"
 #include "v16.cuh"
@@ -94,12 +95,6 @@ struct PagedCfg {
   static_assert(NSB * 128 + SLOTS * D <= 512 && SMEM_BYTES <= 232448, "tensor and shared memory");
 };
 
-// New tokens [tok, tok + count) of sequence `seq`, the first at position pos; key
-// tiles [tile, tile + tiles) hold what they see.
-struct Group {
-  int seq, tok, count, pos, tile, tiles, pad0, pad1;
-};
-
 struct PagedArgs {
   int batch, tokens, hq, hkv, G, per_slot;  // per_slot: tokens in 128 rows
   int page_log2, num_pages, max_pages, window;
@@ -130,86 +125,62 @@ struct AppendArgs {
 };
 
 // Inclusive sum over the block's threads; *total their whole.
-__device__ __forceinline__ int block_scan(int x, int* total) {
-  __shared__ int sums[kPrepThreads / 32];
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* total) {
+  __shared__ T sums[kPrepThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // the sums of an earlier call have been read
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  int s = sums[lane];
+  T s = sums[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
   *total = __shfl_sync(0xffffffffu, s, 31);
-  const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  const T before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
   return warp ? x + before : x;
 }
 
-// Sequence b's new tokens and its length with them, in the arrays' bounds; false
-// where they had to be cut.
-__device__ __forceinline__ bool sequence(const PagedArgs& a, int b, int& tok, int& count, int& len) {
-  const int s0 = a.starts[b], s1 = a.starts[b + 1], l = a.lens[b];
-  tok = min(max(s0, 0), a.tokens);
-  count = max(min(max(s1, 0), a.tokens) - tok, 0);
-  const int64_t room = static_cast<int64_t>(a.max_pages) << a.page_log2;
-  len = static_cast<int>(min(static_cast<int64_t>(max(l, 0)), room));
-  return tok == s0 && count == s1 - s0 && len == l && count <= len;
+__device__ __forceinline__ SequenceCut sequence(const PagedArgs& a, int b) {
+  return cut_sequence(a.starts[b], a.starts[b + 1], a.lens[b], a.tokens, static_cast<int64_t>(a.max_pages) << a.page_log2);
 }
 
 // The groups and the units before each: an item's tiles, and kItemUnits.
 __device__ __forceinline__ void plan(const PagedArgs& a, int per_group) {
-  __shared__ int first[kMaxSequences + 1];  // the sequences' first groups
-  int base = 0, total;
+  __shared__ int first[kMaxSequences];  // the sequences' first groups
+  GroupSum sum = 0, part;
   bool fine = true;
   for (int b0 = 0; b0 < a.batch; b0 += kPrepThreads) {
     const int b = b0 + threadIdx.x;
-    int tok, count = 0, len;
-    if (b < a.batch) fine &= sequence(a, b, tok, count, len);
-    const int n = (count + per_group - 1) / per_group;
-    const int end = block_scan(n, &total);
-    if (b < a.batch) first[b] = base + end - n;
-    base += total;
+    GroupSum n = 0;
+    if (b < a.batch) {
+      const SequenceCut c = sequence(a, b);
+      fine &= c.fine;
+      n = groups_of(c.count, per_group);
+    }
+    const GroupSum end = block_scan(n, &part);
+    if (b < a.batch) first[b] = cut_groups(sum + end - n, a.max_groups);
+    sum += part;
   }
-  if (base > a.max_groups) {  // sequences that share tokens: more work than there is room for
-    base = a.max_groups;
-    fine = false;
-  }
+  fine &= sum <= a.max_groups;  // else sequences share tokens: more work than there is room for
+  const int base = cut_groups(sum, a.max_groups);
   if (!fine) atomicOr(a.err, kErrBounds);
-  if (threadIdx.x == 0) first[a.batch] = base;
   __syncthreads();
-  int units_before = 0;
+  int units_before = 0, total;
   for (int g0 = 0; g0 < base; g0 += kPrepThreads) {
     const int g = g0 + threadIdx.x;
     int n = 0;
     if (g < base) {
-      int lo = 0, hi = a.batch - 1;  // the last sequence that begins at or before group g
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (first[mid] <= g)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      int tok, count, len;
-      sequence(a, lo, tok, count, len);
-      const int off = (g - first[lo]) * per_group;
-      Group r;
-      r.seq = lo;
-      r.tok = tok + off;
-      r.count = min(count - off, per_group);
-      r.pos = len - count + off;
-      const int to = max(r.pos + r.count, 0), from = a.window ? max(r.pos - a.window + 1, 0) : 0;
-      r.tile = from / kTile;
-      r.tiles = max((to + kTile - 1) / kTile - r.tile, 1);  // where nothing is seen that has to be stored
+      const int b = sequence_of_group(first, a.batch, g);
+      const Group r = make_group(sequence(a, b), b, (g - first[b]) * per_group, per_group, a.window);
       n = r.tiles + kItemUnits;
-      r.pad0 = r.pad1 = 0;
       a.groups[g] = r;
     }
     const int end = block_scan(n, &total);
@@ -255,9 +226,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
   for (int t = (blockIdx.x - 1) * (kPrepThreads / 32) + threadIdx.x / 32; t < a.tokens; t += warps) {
     const int b = sequence_of(a, t);
     if (b < 0) continue;
-    int tok, count, len;
-    sequence(a, b, tok, count, len);
-    const int pos = len - count + t - tok;
+    const SequenceCut c = sequence(a, b);
+    const int pos = c.len - c.count + t - c.tok;
     if (pos < 0) continue;  // reported by the plan
     const int page = a.table[static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_log2)];
     if (page < 0 || page >= a.num_pages) {

@@ -25,3 +25,8 @@ def _native(tmp_path, name):
 def test_capped_scores_keep_their_own_precision(tmp_path):
     """A capped score is off by a part of itself, not of a large cap."""
     _native(tmp_path, "score_cap_relative")
+
+
+def test_plan_stays_within_its_bounds(tmp_path):
+    """Starts that fall by so much that the groups' sum passes 32 bits, and anything else."""
+    _native(tmp_path, "paged_plan")
