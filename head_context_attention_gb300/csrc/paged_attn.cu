@@ -97,7 +97,8 @@ struct PagedCfg {
 
 struct PagedArgs {
   int batch, tokens, hq, hkv, G, per_slot;  // per_slot: tokens in 128 rows
-  int page_log2, num_pages, max_pages, window;
+  int page_log2, num_pages, max_pages;
+  int window;  // 0 (none), or less than a row of the table holds
   int max_groups;
   float scale_log2;
   ScoreCap cap;
@@ -976,7 +977,7 @@ int loong_paged_attn(const loong_paged_desc* d, const void* q, const void* k, co
   a.page_log2 = log2_of(d->page_size);
   a.num_pages = d->num_pages;
   a.max_pages = d->max_pages;
-  a.window = d->window;
+  a.window = window_within(d->window, static_cast<int64_t>(d->max_pages) * d->page_size);
   a.max_groups = w.max_groups;
   const float scale =
       d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt(static_cast<float>(d->head_dim));

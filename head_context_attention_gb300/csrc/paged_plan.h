@@ -54,6 +54,10 @@ __host__ __device__ inline int sequence_of_group(const int* first, int batch, in
   return lo;
 }
 
+// A window as wide as a sequence may be leaves every key, like none (0), and positions less
+// such a window stay within 32 bits.
+__host__ __device__ inline int window_within(int window, int64_t room) { return window < room ? window : 0; }
+
 // The group that begins `off` tokens into the sequence's new ones.
 __host__ __device__ inline Group make_group(const SequenceCut& c, int seq, int off, int per_group, int window) {
   Group r;
@@ -62,7 +66,7 @@ __host__ __device__ inline Group make_group(const SequenceCut& c, int seq, int o
   r.count = c.count - off < per_group ? c.count - off : per_group;
   r.pos = c.len - c.count + off;
   const int to = r.pos + r.count > 0 ? r.pos + r.count : 0;
-  const int from = window && r.pos - window + 1 > 0 ? r.pos - window + 1 : 0;
+  const int from = window && r.pos - window + 1 > 0 ? r.pos - window + 1 : 0;  // window: of window_within
   r.tile = from / kTile;
   const int tiles = (to + kTile - 1) / kTile - r.tile;
   r.tiles = tiles > 1 ? tiles : 1;  // where nothing is seen that has to be stored

@@ -100,6 +100,20 @@ int main() {
     const int per_group = 2, max_groups = tokens / per_group + 4096;
     hold(!plan(starts, lens, tokens, 1 << 20, per_group, max_groups, 0, groups, 1000));
   }
+  // a window of any size, up to the largest number, where tokens stand before position 0
+  for (const int64_t wide : {int64_t{300}, int64_t{1} << 30, (int64_t{1} << 31) - 6, (int64_t{1} << 31) - 1})
+    for (int len = 0; len < 300; len += 7) {
+      const int64_t room = 4096;
+      const std::vector<int> starts{0, 200}, lens{len};
+      plan(starts, lens, 200, room, 32, 8, window_within(static_cast<int>(wide), room), groups, ~size_t{0});
+      hold(groups.size() == 7);
+      for (const Group& r : groups)
+        for (int i = 0; i < r.count; ++i) {
+          const int64_t pos = r.pos + i, from = pos - wide + 1 > 0 ? pos - wide + 1 : 0;
+          hold(pos == len - 200 + r.tok + i);
+          if (pos >= 0) hold(int64_t{r.tile} * kTile <= from && pos < int64_t{r.tile + r.tiles} * kTile);
+        }
+    }
   std::printf("%ld checks, %ld failed\n", checked, bad);
   return bad ? 1 : 0;
 }

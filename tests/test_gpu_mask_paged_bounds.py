@@ -86,3 +86,27 @@ def test_caps_far_above_the_scores_paged(cuda_device, name, cap):
                 2.0 ** -8 * np.abs(t["o"]) + (2 * (2.0 ** -8 + e) + 2.0 ** -16) * t["abs_o"])
         _within(f"LSE of sequence {b}", lse[:, at:at + new], t["lse"], e + 2.0 ** -22 * (1 + np.abs(t["lse"])))
         at += new
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30, 900])
+def test_wide_windows_before_the_first_position(cuda_device, window):
+    """More new tokens than a sequence's length holds: those that stand before position 0 see nothing, the others what
+    they see without a window."""
+    s = _Setup("whole-prompts")
+    want = s.run()
+    s.window = window
+    assert all(torch.equal(a, b) for a, b in zip(s.run(append=False), want))
+    s.check(*want)
+    short = 40   # the last sequence has 300 new tokens and now a length of 40
+    s.lens[2] = short
+    o, lse = s.run(append=False)
+    assert ops.loong_get_device_status() == ops.LOONG_ERR_DEVICE_CHECK
+    at = int(s.starts[3])
+    assert bool((o[at - 300:at - short] == 0).all()) and bool(torch.isneginf(lse[:, at - 300:at - short]).all())
+    i = np.arange(short)
+    t = omask.forward_backward(to64(s.q[at - short:at]), to64(s.ks[2][:short]), to64(s.vs[2][:short]), None,
+                               omask.sees(np.stack([0 * i, i + 1], 1), short, False), ops.default_scale(s.d), 0.0,
+                               terms=True)
+    e = _errors(t, s.d, 0.0)[0]
+    _within("O", o[at - short:at], t["o"], 2.0 ** -8 * np.abs(t["o"]) + (2 * (2.0 ** -8 + e) + 2.0 ** -16) * t["abs_o"])
+    _within("LSE", lse[:, at - short:at], t["lse"], e + 2.0 ** -22 * (1 + np.abs(t["lse"])))

@@ -28,5 +28,6 @@ def test_capped_scores_keep_their_own_precision(tmp_path):
 
 
 def test_plan_stays_within_its_bounds(tmp_path):
-    """Starts that fall by so much that the groups' sum passes 32 bits, and anything else."""
+    """Starts that fall by so much that the groups' sum passes 32 bits, windows up to the largest number before
+    position 0, and anything else."""
     _native(tmp_path, "paged_plan")
