@@ -178,7 +178,7 @@ struct RangeQWalk {
     const int i = base + lane;
     bool l = false, p = false;
     if (i <= last) {
-      const int4 r = __ldg(tiles + i);
+      const int4 r = tiles[i];
       l = sees(r, k0, k1) && (rank < 0 || block_owner(*g, i / g->ntile) == rank);
       p = !(r.z <= k0 && r.w >= k1) || k1 - k0 < kTile;
     }
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     __syncthreads();
     int count = 0, first = nq, last = -1;
     for (int i = threadIdx.x; i < nq; i += C::THREADS) {
-      if (RangeQWalk::sees(__ldg(walk.tiles + i), k0, k0 + klen) &&
+      if (RangeQWalk::sees(walk.tiles[i], k0, k0 + klen) &&
           (!STEP || block_owner(g, i / g.ntile) == walk.rank)) {
         ++count;
         first = min(first, i);
@@ -443,8 +443,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
       const int head0 = kvh * a.G + (MASK ? split * a.mask.per_split : 0);
       auto look_up_mark = [&]() {
         if constexpr (MASK)
-          marked = __ldg(a.mask.bad + (static_cast<int64_t>(b) * a.hq + head0 + walk.hk) * g.nblocks * g.ntile +
-                         walk.x);
+          marked = a.mask.bad[(static_cast<int64_t>(b) * a.hq + head0 + walk.hk) * g.nblocks * g.ntile + walk.x];
       };
       if constexpr (MASK) {
         walk.fetch(lane);

@@ -177,7 +177,9 @@ int kernel_ready(int smem, int min_regs) {
 }
 
 // A launch whose blocks may start, up to previous_launch_wait, while the kernel
-// before it in the stream still runs (next_launch_go there).
+// before it in the stream still runs (next_launch_go there).  What that kernel writes is
+// read by plain loads: the read-only path (__ldg) asks for data that is constant while
+// the reader runs, and may be moved ahead of the wait.
 template <typename... Params, typename... Args>
 int launch_dependent(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                      const Args&... args) {

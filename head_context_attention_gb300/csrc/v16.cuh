@@ -140,7 +140,7 @@ template <int THREADS, bool FINITE = false>
 __device__ __forceinline__ void v16_copy(const VArgs& v) {
   unsigned m = 0, bad = 0;
   for (int i = threadIdx.x; i < v.max_blocks; i += THREADS) {
-    const unsigned s = __ldg(v.shares + i);
+    const unsigned s = v.shares[i];
     m = max(m, FINITE ? s & 0x7FFFu : s);
     bad |= s & 0x8000u;
   }

@@ -1,5 +1,6 @@
 """Host-side checks of the masked and the paged attention where they once went wrong."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -31,3 +32,16 @@ def test_plan_stays_within_its_bounds(tmp_path):
     """Starts that fall by so much that the groups' sum passes 32 bits, windows up to the largest number before
     position 0, and anything else."""
     _native(tmp_path, "paged_plan")
+
+
+def test_data_of_the_launch_before_is_read_by_plain_loads():
+    """A kernel that starts while the launch before it runs waits, then reads what that launch wrote; the read-only path
+    would ask for data that is constant from its start on."""
+    written = {"attn_bwd.cu": ("tiles", "mask.bad"), "attn_fwd.cu": ("tiles",), "mask_fwd.cu": ("tiles", "v_amax"),
+               "v16.cuh": ("shares", "amax"), "paged_attn.cu": ("a.groups", "a.prefix", "a.count")}
+    for name, fields in written.items():
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        for call in re.finditer(r"__ldg\(([^;]*);", text):
+            for field in fields:
+                assert not re.search(rf"\b{re.escape(field)}\b", call.group(1)), f"{name}: {call.group(0)}"
