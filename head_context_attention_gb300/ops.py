@@ -359,9 +359,16 @@ def loong_attn_bias_bwd(desc, bias, q, k, v, o, o_res, lse, dout, dq, dk, dv, dt
         _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dtable), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
+def _single(name, x):
+    """x for a float of the ABI, whose 0 stands for something else: refused where it would become that."""
+    if x != 0 and ctypes.c_float(x).value == 0:
+        raise ValueError(f"{name} is below what single precision holds, not {x}")
+    return x
+
+
 def make_mask(key_range=None, score_cap=0.0):
     """loong_attn_mask; keeps the tensor it points at."""
-    m = LoongAttnMask(None if key_range is None else key_range.data_ptr(), score_cap)
+    m = LoongAttnMask(None if key_range is None else key_range.data_ptr(), _single("score_cap", score_cap))
     m.keep = key_range
     return m
 
@@ -873,10 +880,15 @@ def _row_stride(name, t, heads, d):
     return ss
 
 
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=256, typed=True)
 def _paged_problem(*fields):
     """(descriptor, workspace bytes), checked."""
     desc = LoongPagedDesc(*fields)
+    names = dict(zip((n for n, _ in LoongPagedDesc._fields_), fields))
+    _single("scale", names["softmax_scale"])
+    _single("score_cap", names["score_cap"])
+    if desc.window != names["window"]:
+        raise ValueError(f"window must fit 32 bits, not {names['window']}")
     _check("loong_paged_check", loong_paged_check(desc))
     return desc, loong_paged_attn_workspace_size(desc)
 

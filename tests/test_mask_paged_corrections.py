@@ -5,9 +5,16 @@ import shutil
 import subprocess
 
 import pytest
+import torch
+
+from head_context_attention_gb300 import inputs, ops
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "..", "head_context_attention_gb300", "csrc")
+W = inputs.WORKLOADS["tiny-gqa-s1k"]
+# q, k_pages, v_pages, table, lens, starts: on the host, where a call that is fine so far ends
+_PAGED = (torch.zeros(1, 4, 64, dtype=torch.bfloat16), *[torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)] * 2,
+          torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
 
 
 def _native(tmp_path, name):
@@ -45,3 +52,31 @@ def test_data_of_the_launch_before_is_read_by_plain_loads():
         for call in re.finditer(r"__ldg\(([^;]*);", text):
             for field in fields:
                 assert not re.search(rf"\b{re.escape(field)}\b", call.group(1)), f"{name}: {call.group(0)}"
+
+
+@pytest.mark.parametrize("value", [1e-46, -1e-46, 5e-324])
+def test_a_number_that_vanishes_in_single_precision_is_refused(loong_lib, value):
+    """0 would stand for no cap, or for the default scale."""
+    x = inputs.make_inputs(W)
+    with pytest.raises(ValueError, match="score_cap"):
+        ops.make_mask(None, value)
+    with pytest.raises(ValueError, match="score_cap"):
+        ops.attn_mask_fwd(W, x["q"], x["k"], x["v"], score_cap=value)
+    for kw in ({"score_cap": value}, {"scale": value}):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            ops.paged_attn(*_PAGED, **kw)
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 32 + 5])
+def test_a_window_beyond_32_bits_is_refused(loong_lib, window):
+    """Its low 32 bits would be taken."""
+    with pytest.raises(ValueError, match="window"):
+        ops.paged_attn(*_PAGED, window=window)
+
+
+def test_a_window_is_a_whole_number(loong_lib):
+    for _ in range(2):
+        with pytest.raises(TypeError):
+            ops.paged_attn(*_PAGED, window=8.0)
+        with pytest.raises(ValueError, match="CUDA device"):
+            ops.paged_attn(*_PAGED, window=8)
