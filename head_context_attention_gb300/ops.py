@@ -651,6 +651,7 @@ def document_ranges(lengths, seqlen, prefix=None, window=0, causal=True, device=
     that is not causal."""
     if window < 0 or (prefix is not None and (window or not causal)):
         raise ValueError("window must not be negative, and a prefix goes with neither a window nor causal=False")
+    window = min(window, seqlen)   # wider ones leave as much, and sums with it stay within 32 bits
     out = torch.zeros((len(lengths), seqlen, 2), dtype=torch.int32)
     for b, docs in enumerate(lengths):
         if any(n < 0 for n in docs) or sum(docs) > seqlen:

@@ -80,3 +80,16 @@ def test_a_window_is_a_whole_number(loong_lib):
             ops.paged_attn(*_PAGED, window=8.0)
         with pytest.raises(ValueError, match="CUDA device"):
             ops.paged_attn(*_PAGED, window=8)
+
+
+@pytest.mark.parametrize("window", [12, 13, 2 ** 31 - 13, 2 ** 31 - 1, 2 ** 31, 2 ** 40])
+@pytest.mark.parametrize("causal", [True, False])
+def test_document_ranges_with_a_window_wider_than_any_document(window, causal):
+    lengths = [[4, 1, 0, 5], [], [12]]
+    assert torch.equal(ops.document_ranges(lengths, 12, window=window, causal=causal),
+                       ops.document_ranges(lengths, 12, causal=causal))
+
+
+def test_document_ranges_with_a_prefix_longer_than_any_document():
+    assert torch.equal(ops.document_ranges([[4, 8]], 12, prefix=[[2 ** 40, 2 ** 31]]),
+                       ops.document_ranges([[4, 8]], 12, causal=False))
