@@ -1,6 +1,6 @@
 """The masked and the paged attention where a loose tolerance or a small problem would
 hide a fault: caps far above the scores, windows near 2^31, walks long enough for the
-backward's flushes.
+backward's flushes, long sequences.
 
 Tolerances as in test_gpu_mask_attn and test_gpu_paged_attn but for the cap's part: a
 capped logit is off by at most 2^-19 of itself (caps above 64), |logit| <= min(L, cap), so dx = (d + 4)
@@ -25,7 +25,7 @@ from head_context_attention_gb300 import inputs, ops
 from oracle import mask as omask
 from tests.helpers import to64
 from tests.test_gpu_checked import _library
-from tests.test_gpu_mask_attn import _run, _sees, _within
+from tests.test_gpu_mask_attn import _pack, _run, _sees, _unpack, _within
 from tests.test_gpu_paged_attn import _Setup
 
 pytestmark = pytest.mark.gpu
@@ -218,3 +218,41 @@ def test_backward_flushes(cuda_device, S, hq, d, cap, splits):
         some = slice(at, at + 1000)
         _norms(o=(o[0, rows][some], t["o"][rows][some]), dq=(dq[0, rows][some], t["dq"][rows][some]),
                dk=(dk[0, rows][some], t["dk"][rows][some]), dv=(dv[0, rows][some], t["dv"][rows][some]))
+
+
+@pytest.mark.parametrize("d,cap", [(64, 25.0), (128, 0.0)])
+@pytest.mark.parametrize("layout", [ops.LAYOUT_NATURAL, ops.LAYOUT_RANK_MAJOR])
+def test_long_sequence_of_documents(cuda_device, d, cap, layout):
+    """131,072 tokens of packed documents up to 9,000 long, every one of them up to the last token: a short document
+    whole, of a long one the rows and keys at its end, which see or are seen by rows of it alone."""
+    S, hq, hkv = 131072, 4, 2
+    w = inputs.Workload("long", S, hq, hkv, d, 2, 8, 4, 2, True)
+    x = inputs.make_inputs(w, device="cuda")
+    rng = np.random.default_rng(6)
+    lengths = []
+    while sum(lengths) < S - 1000:
+        lengths.append(int(rng.integers(1, 9000)))
+    lengths = lengths[:-1]
+    r = ops.document_ranges([lengths], S)
+    out = _run(w, x if layout == ops.LAYOUT_NATURAL else _pack(w, x), r, cap, layout=layout)
+    if layout == ops.LAYOUT_RANK_MAJOR:
+        out = [t if i == 1 else _unpack(w, t) for i, t in enumerate(out)]
+    o, lse, dq, dk, dv = out
+    starts = np.concatenate([[0], np.cumsum(lengths)])
+    for a, b in zip(starts[:-1], starts[1:]):
+        a, b = int(a), int(b)
+        first = max(a, b - 256)   # causal: the keys from here on are seen by the rows from here on alone
+        n = b - first
+        see = omask.sees(np.tile([0, b - a], (n, 1)), b - a, True, first=first - a)
+        t = omask.forward_backward(to64(x["q"][0, first:b]), to64(x["k"][0, a:b]), to64(x["v"][0, a:b]),
+                                   to64(x["do"][0, first:b]), see, ops.default_scale(d), cap, terms=True)
+        for name in list(t):
+            if name[-2:] in ("dk", "dv"):
+                t[name] = t[name][first - a:]
+        _check_rows(t, d, cap, o[0, first:b], lse[0][:, first:b], dq[0, first:b], dk[0, first:b], dv[0, first:b])
+        if n == 256:
+            _norms(o=(o[0, first:b], t["o"]), dq=(dq[0, first:b], t["dq"]), dk=(dk[0, first:b], t["dk"]),
+                   dv=(dv[0, first:b], t["dv"]))
+    pad = int(starts[-1])
+    assert bool((o[0, pad:] == 0).all()) and bool(torch.isneginf(lse[0][:, pad:]).all())
+    assert all(bool((g[0, pad:] == 0).all()) for g in (dq, dk, dv))
