@@ -27,10 +27,6 @@ constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 1216;                  // of a launch that strides over its data: 8 per SM
 constexpr int kSms = 152;                         // workspace sizes do not ask the device
 constexpr int64_t kMaxSeqlen = int64_t{1} << 30;  // a tile past the last token still has a 32-bit number
-// A capped logit is at most the cap; up to 2^20 the softmax's reference, rounded to
-// 24 bits, is off by at most 2^-3 in log2 units, which fp16 P has room for.
-constexpr float kMinCap = 9.5367432e-7f, kMaxCap = 1048576.f;        // 2^-20, 2^20
-constexpr float kMinScale = 5.9604645e-8f, kMaxScale = 16777216.f;  // 2^-24, 2^24
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -222,12 +218,7 @@ int check_mask(const loong_attn_desc* d, const loong_attn_mask* m) {
   if (st != LOONG_OK) return st;
   if (!m || !std::isfinite(m->score_cap) || m->score_cap < 0.f) return LOONG_ERR_INVALID_ARG;
   if (d->seqlen > kMaxSeqlen || d->hq > 65535 || d->batch > 65535) return LOONG_ERR_UNSUPPORTED;
-  if (m->score_cap > 0.f) {
-    if (m->score_cap < kMinCap || m->score_cap > kMaxCap) return LOONG_ERR_UNSUPPORTED;
-    if (d->softmax_scale > 0.f && (d->softmax_scale < kMinScale || d->softmax_scale > kMaxScale))
-      return LOONG_ERR_UNSUPPORTED;
-  }
-  return LOONG_OK;
+  return score_cap_fits(d->softmax_scale, m->score_cap) ? LOONG_OK : LOONG_ERR_UNSUPPORTED;
 }
 
 // In FUSED mode the walks do not follow the ring, so where the layout does not either

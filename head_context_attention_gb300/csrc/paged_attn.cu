@@ -7,10 +7,11 @@
 //   i's sequence, its K and V at row j mod page of page table[sequence][j / page]
 //
 // Two launches, the second's blocks starting while the first runs.  paged_prep_kernel
-// writes the new keys and values into their pages and lays the work out (block 0): a group is up to SLOTS * (128 / G) new tokens of a
-// sequence, G query heads to a kv head; with a kv head it makes an item, whose rows
-// (token by token, the kv head's G query heads each) fill SLOTS blocks of 128 rows of
-// the matrix instructions, and its 128-key tiles are the units of work.
+// writes the new keys and values into their pages and lays the work out (block 0,
+// paged_plan.h): a group is up to SLOTS * (128 / G) new tokens of a sequence, G query
+// heads to a kv head; with a kv head it makes an item, whose rows (token by token, the kv
+// head's G query heads each) fill SLOTS blocks of 128 rows of the matrix instructions,
+// and its 128-key tiles are the units of work.
 // paged_attn_kernel runs one block an SM; block c takes units [U c / blocks, U (c + 1) /
 // blocks) of the whole list, whatever the sequences' lengths: the long axis is split
 // where the rows are few, and every SM streams the same number of keys.  A block
@@ -20,8 +21,9 @@
 // the keys, so the result does not depend on who is last.
 //
 // One kernel for both ends: with one new token the rows are few and memory is the
-// bound (a 128 x 128 score tile costs the matrix instructions a fifth of what its 64
-// KB of K and V take to arrive); with a chunk two blocks of rows share every K and V
+// bound (a 128 x 128 score tile takes the matrix instructions, most of whose rows are
+// then empty, 0.45 of the time in which its 64 KB of K and V arrive: 0.67 and 1.48 us an
+// SM at head dimension 128); with a chunk two blocks of rows share every K and V
 // tile, and the matrix instructions and the softmax between them are the bound.
 //
 // Warps: 4 * SLOTS softmax warps (a row in every lane), a TMA warp, an MMA warp.  As
@@ -38,7 +40,7 @@
 //
 // Measured, both launches: the next token after 131,071 (32 + 8 heads of 128) 100 us, 5.3
 // TB/s; of 61 sequences of 64 to 16,000 keys (64 + 8 heads) 135 us, 5.1 TB/s; 2,048 new
-// tokens over 32K keys (32 + 8 heads) 0.79 ms, 1.35 PFLOP/s, with capped scores 1.18.
+// tokens over 32K keys (32 + 8 heads) 0.79 ms, 1.35 PFLOP/s, with capped scores 1.22.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -67,8 +69,6 @@ constexpr float kSumBound = 256.0f;        // 2^threshold: the largest P let thr
 constexpr int kItemUnits = 4;
 constexpr int kMaxSequences = 4096;
 constexpr int kPrepThreads = 1024;
-constexpr float kMinCap = 9.5367432e-7f, kMaxCap = 1048576.f;        // 2^-20, 2^20
-constexpr float kMinScale = 5.9604645e-8f, kMaxScale = 16777216.f;  // 2^-24, 2^24
 
 template <int D, int SLOTS>
 struct PagedCfg {
@@ -150,7 +150,8 @@ __device__ __forceinline__ T block_scan(T x, T* total) {
 }
 
 __device__ __forceinline__ SequenceCut sequence(const PagedArgs& a, int b) {
-  return cut_sequence(a.starts[b], a.starts[b + 1], a.lens[b], a.tokens, static_cast<int64_t>(a.max_pages) << a.page_log2);
+  const int64_t room = static_cast<int64_t>(a.max_pages) << a.page_log2;
+  return cut_sequence(a.starts[b], a.starts[b + 1], a.lens[b], a.tokens, room);
 }
 
 // The groups and the units before each: an item's tiles, and kItemUnits.
@@ -573,7 +574,8 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
             }
             // noted before they are cleared: another warp that finds them cleared
             // finds them noted
-            if (lane < 4) atomicOr(&bad_v[st][lane], lane == 0 ? bad[0] : lane == 1 ? bad[1] : lane == 2 ? bad[2] : bad[3]);
+            if (lane < 4)
+              atomicOr(&bad_v[st][lane], lane == 0 ? bad[0] : lane == 1 ? bad[1] : lane == 2 ? bad[2] : bad[3]);
             __threadfence_block();
             __syncwarp();
 #pragma unroll
@@ -719,7 +721,8 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(ov[v4 * 8 + 2 * e]) * inv, __uint_as_float(ov[v4 * 8 + 2 * e + 1]) * inv);
+                w[e] = pack_bf16(__uint_as_float(ov[v4 * 8 + 2 * e]) * inv,
+                                 __uint_as_float(ov[v4 * 8 + 2 * e + 1]) * inv);
               reinterpret_cast<uint4*>(orow + cb * 32)[v4] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
@@ -793,7 +796,8 @@ __global__ void __launch_bounds__(PagedCfg<D, SLOTS>::THREADS, 1)
         const float inv = rl != 0.f ? 1.f / rl : 0.f;
         reinterpret_cast<uint2*>(a.o + (tok2 * a.hq + head2) * D)[part4] =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (part4 == 0) a.lse[static_cast<int64_t>(head2) * a.tokens + tok2] = l != 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
+        if (part4 == 0)
+          a.lse[static_cast<int64_t>(head2) * a.tokens + tok2] = l != 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
       }
       __syncwarp();
     }
@@ -853,12 +857,7 @@ int check_paged(const loong_paged_desc* d) {
   if ((static_cast<int64_t>(d->num_pages) + 1) * d->page_size > (1 << 30) ||
       static_cast<int64_t>(d->max_pages) * d->page_size > (1 << 30) || d->tokens > (1 << 30))
     return LOONG_ERR_UNSUPPORTED;
-  if (d->score_cap > 0.f) {
-    if (d->score_cap < kMinCap || d->score_cap > kMaxCap) return LOONG_ERR_UNSUPPORTED;
-    if (d->softmax_scale > 0.f && (d->softmax_scale < kMinScale || d->softmax_scale > kMaxScale))
-      return LOONG_ERR_UNSUPPORTED;
-  }
-  return LOONG_OK;
+  return score_cap_fits(d->softmax_scale, d->score_cap) ? LOONG_OK : LOONG_ERR_UNSUPPORTED;
 }
 
 // Two slots of 128 rows share a tile of keys where the new tokens of a sequence fill

@@ -29,8 +29,16 @@ struct ScoreCap {
 // The shorter polynomial's coefficients, of x = inv s.
 constexpr float kTanhHalf[3] = {-0.33326460635391786f, 0.1318586029707108f, -0.04422924520882877f};
 
-// scale and cap as the entry points let them through (2^-24 .. 2^24 and 2^-20 ..
-// 2^20).  The coefficients that count have to be normal numbers: the longer polynomial's
+// What the entry points let through: no cap (0), or caps of 2^-20 .. 2^20 and scales, where
+// given, of 2^-24 .. 2^24.  A capped logit is at most the cap; up to 2^20 the softmax's
+// reference, rounded to 24 bits, is off by at most 2^-3 in log2 units, which fp16 P has
+// room for.
+inline bool score_cap_fits(float scale, float cap) {
+  const bool scale_fits = !(scale > 0.f) || (scale >= 0x1p-24f && scale <= 0x1p24f);
+  return !(cap > 0.f) || (cap >= 0x1p-20f && cap <= 0x1p20f && scale_fits);
+}
+
+// The coefficients that count have to be normal numbers: the longer polynomial's
 // highest is about 2^-8 inv^10, so it is for inv above 2^-11, the shorter one's 2^-5
 // inv^6, above 2^-20.  Below, s (1 - y / 3) is left, to which the next term adds less than
 // 2^-26 up to |x| = 2^-6.  Above inv = 2^11 inv^10 may pass the largest number.
