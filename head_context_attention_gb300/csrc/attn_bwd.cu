@@ -117,7 +117,9 @@ struct BwdArgs {
   float* dq_acc;      // fp32, the layout of Q
   __nv_bfloat16* dk;  // FUSED outputs
   __nv_bfloat16* dv;
-  float* dk_acc;      // fp32 accumulators, the layout of K (zeroed by the launcher)
+  // fp32 accumulators, the layout of K, zeroed by the launcher; FUSED with a mask: not, the
+  // first flush writes them (and where a group's heads are split the last one, the blocks' parts)
+  float* dk_acc;
   float* dv_acc;
   BiasView bias;      // BIAS: the bias by distance
   float* dbias_part;  // BIAS: [blocks][compute warps][G][intervals], zeroed
@@ -159,7 +161,7 @@ struct BwdPiece {
 // and dO by the producer, in the tiles that the launch before marked.  Instead the
 // row's own P is NaN, for those that see it.
 // Where key tiles do not fill the SMs, the query heads of a group go to several blocks.
-// 32 + 8 heads of 128: 16K tokens in one piece 4.98 ms (K2's rate), capped 5.9; 64K in
+// 32 + 8 heads of 128: 16K tokens in one piece 4.98 ms (K2's rate), capped 5.5; 64K in
 // documents of about 8K 14.7 ms.
 enum BwdVariant { kBwdPlain, kBwdBias, kBwdMask, kBwdCap };
 
@@ -513,7 +515,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             for (int r0 = 0; r0 < kTile; r0 += 32) {
               unsigned m = __ballot_sync(0xffffffffu, !(fabsf(lse_row[r0 + lane]) < INFINITY) || r0 + lane >= qlen);
               for (; m; m &= m - 1) {
-                const int at = s * C::TILE_BYTES + (line >> 3) * C::ATOM_BYTES + (r0 + __ffs(m) - 1) * 128 + (line & 7) * 16;
+                const int at =
+                    s * C::TILE_BYTES + (line >> 3) * C::ATOM_BYTES + (r0 + __ffs(m) - 1) * 128 + (line & 7) * 16;
                 if (D == 64 || lane < 16) *reinterpret_cast<uint4*>(sQ + at) = make_uint4(0, 0, 0, 0);
                 if (D == 64 || lane >= 16) *reinterpret_cast<uint4*>(sdO + at) = make_uint4(0, 0, 0, 0);
               }
@@ -1296,8 +1299,8 @@ int launch_bwd_v(const loong_attn_desc& d, const void* q, const void* k, const v
 }  // namespace
 
 int launch_bwd(const loong_attn_desc& d, const void* q, const void* k, const void* v, const void* o,
-               const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, float* dq_acc, float* dvec,
-               float* dk_acc, float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias,
+               const void* o_res, const float* lse, const void* dout, void* dq, void* dk, void* dv, float* dq_acc,
+               float* dvec, float* dk_acc, float* dv_acc, cudaStream_t stream, void* kv_recv, const BiasView* bias,
                float* dbias_part, const MaskView* mask) {
   const int64_t q_elems = d.batch * d.seqlen * d.hq * d.head_dim;
   const int64_t kv_elems = d.batch * d.seqlen * d.hkv * d.head_dim;

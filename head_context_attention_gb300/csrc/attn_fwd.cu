@@ -149,14 +149,13 @@ static_assert(kSumBound == float(1 << int(kPBias + kRescaleThreshold)), "sum bou
 constexpr float kMaxMiddle = 32.0f;  // log2 units
 
 // MASK (only where STEP; mask_fwd.cu is the rest) gives every query a range of keys and may
-// cap the scores (softcap.cuh; scale_log2 is then the cap's).  A block walks the tiles between the first and the
-// last key that any of its rows sees (RangeWalk), which the launch before summed up
-// for it; a block whose rows see nothing in a step leaves it out.  A softmax warp some of
-// whose rows do not see a whole tile masks it by four words of bits a row.  Columns of
-// masked keys are replaced, so what the keys hold does not matter; V, whose rows a
-// product adds up with P = 0, is 0 in its copy where it is not finite, and where
-// there was such a value (v_amax[1]) the scores of its key become NaN for the rows
-// that see it.
+// cap the scores (softcap.cuh).  A block walks the tiles between the first and the last
+// key that any of its rows sees (RangeWalk), which the launch before summed up for it;
+// a block whose rows see nothing in a step leaves it out.  A softmax warp some of whose
+// rows do not see a whole tile masks it by four words of bits a row.  Columns of masked
+// keys are replaced, so what the keys hold does not matter; V, whose rows a product adds
+// up with P = 0, is 0 in its copy where it is not finite, and where there was such a
+// value (v_amax[1]) the scores of its key become NaN for the rows that see it.
 // Pairs of heads and of tiles are formed as with a bias.
 enum FwdVariant { kFwdPlain, kFwdBias, kFwdMask, kFwdCap };
 
@@ -166,7 +165,6 @@ struct FwdPiece {
   int step;      // kPieceStep: row r of the piece has passed the boundary up to column r + step
 };
 
-//
 // With a cap the softmax warps cap a tile where it lies in tensor memory first (softcap.cuh).
 //
 // SLOTS = 1 (with BIAS): one head's query tile per block, where even such blocks do

@@ -12,12 +12,12 @@
 // last Q K^T of this one is done, on their way while the softmax warps still write this
 // one's rows.  32 + 8 heads of 128, a block an item and here: 32K tokens in documents of
 // about 4K 1.34 and 1.18 ms, of about 256 490 and 422 us, 16K in one with a cap 2.41 and
-// 2.24 ms, and where one round of blocks does it nothing (2 x 1990 tokens of 6 + 3 heads
-// of 64 54 us).  Items go by their place first, all kv heads of all sequences at one, so that
-// the light ones come last; a kv head after the other took 1.25 ms, prefixes of 2 x 4K
-// with 16 heads 275 us for 228.  What bounds an item is the softmax's exponentials
-// (1.70 PFLOP/s at 32K in one piece, as without a mask) and, short, its ends: first scores
-// and last rows, some 4 us that nothing else of the SM's covers.
+// 2.24 ms, and where one round of blocks does it nothing.  Items go by their place first,
+// all kv heads of all sequences at one, so that the light ones come last; a kv head after
+// the other took 1.25 ms, prefixes of 2 x 4K with 16 heads 275 us for 228.
+// What bounds an item is the softmax's exponentials (1.70 PFLOP/s at 32K in one piece, as
+// without a mask) and, short, its ends: first scores and last rows, some 4 us that nothing
+// else of the SM's covers.
 // SLOTS = 1: one head's tile an item, where even those do not fill the SMs.
 //
 // An item walks the key tiles between the first and the last key that any of its rows

@@ -7,9 +7,10 @@
 // far above the scores.
 //
 // Scores within the polynomials' reach (score_cap.h) are formed in pairs: 7 paired
-// operations for two scores up to |inv s| = 1, 5 up to 1/2, where most are; the fp32 pipe
-// takes 14 and 10 cycles for them, the matrix instructions 8 at head dimension 128,
-// exponentials and sums 6.  (A third polynomial up to 1/4: 4 % for the forward where
+// operations for two scores up to |inv s| = 1, 5 up to 1/2, where most are.  The fp32 pipe
+// takes 14 and 10 cycles for them and 6 for exponentials and sums, the matrix instructions 16
+// for both products at head dimension 128, so it is not a pipe's rate that the cap costs
+// (cap_tile).  (A third polynomial up to 1/4: 4 % for the forward where
 // scores stay there, 3 % against it elsewhere and in the backward.)  A warp whose scores
 // pass 1 takes 1 - 2 / (1 + e^2x), two more special functions a score, and under caps above
 // 64 the shorter polynomial for those of them below 1/2.  (For every cap: 12 % for the
@@ -96,11 +97,13 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreCap& cap
 // tangent beside it in front of the exponentials, did not fit the instruction cache:
 // forward of 32 + 8 heads of 128, 16K tokens, scores of deviation 3, 3.03-3.81 ms by how
 // it was arranged, as a loop 2.56, with the shorter polynomial beside the longer 2.32
-// (without a cap, on the same scores, 1.57).  The difference is the fp32 pipe's 1,280
-// cycles for two slots' polynomials, which no other work of the chain from scores to
-// scores covers (0.58 ms), and the way through tensor memory (0.24).  Four more warps for
-// the cap alone, 2.63: the softmax warps then have 176 registers for 216, and every tile
-// one more barrier on its way.
+// (without a cap, on the same scores, 1.57), on blocks that stay 2.24.  What is left is a chain:
+// a warp takes its 32 rows of a tile through cap, exponentials and packing by itself, two
+// such warps a scheduler, and a slot's next scores wait for it.  The polynomials lengthen it by
+// 1,280 cycles for two slots (0.58 ms) and the way through tensor memory as well (0.24), while
+// no pipe is full: the matrix instructions take 2,048 cycles for the two slots, 40 % of the
+// time, the fp32 pipe is busy about as long.  Four more warps for the cap alone, 2.63: the
+// softmax warps then have 176 registers for 216, and every tile one more barrier on its way.
 // masked: seen(c) has a bit for each of columns c .. c + 31.
 template <int N, typename Seen>
 __device__ __forceinline__ void cap_tile(uint32_t t, const ScoreCap& cap, bool counts, bool masked, Seen&& seen) {

@@ -19,9 +19,10 @@
  *     pointer (pinned or not) or another device's memory is refused with
  *     LOONG_ERR_INVALID_ARG before any work is enqueued.  The
  *     library allocates no device memory, keeps no state between calls except a
- *     cached device query, a loaded tensor-map encoder, one device error word
- *     and (STEPWISE_COPY) one side stream with its events per device, and
- *     synchronises only in loong_get_device_status.
+ *     cached device query, which kernels have their launch attributes set, a
+ *     loaded tensor-map encoder, one device error word and (STEPWISE_COPY) one
+ *     side stream with its events per device, and synchronises only in
+ *     loong_get_device_status.
  *   - All work is enqueued asynchronously on `stream` (0 = legacy default).
  *     Calls (or replays of captured ones) that may run at the same time need
  *     workspaces of their own.
@@ -436,8 +437,8 @@ LOONG_API int loong_attn_mask_check(const loong_attn_desc* desc, const loong_att
  * Device workspace, in bytes, of loong_attn_mask_fwd (pass 0) or
  * loong_attn_mask_bwd (pass 1); 0 for invalid arguments.  Host-only.
  * loong_attn_workspace_size's, then 16 bytes for every 128-token query tile of a
- * block; for the forward 1,216 words more, for the backward a byte for every
- * query tile and head.  Each part starts on a 256-byte boundary.  A FUSED
+ * block; for the forward 1,216 words and one word more, for the backward a byte
+ * for every query tile and head.  Each part starts on a 256-byte boundary.  A FUSED
  * descriptor with the NATURAL layout counts as one of cp = hp = 1, one block.
  * Where a FUSED backward's key tiles of 128 (of all blocks, kv heads and sequences)
  * are 76 or fewer, the query heads of a group go to up to 152 / tiles blocks, each
@@ -597,7 +598,8 @@ LOONG_API size_t loong_paged_attn_workspace_size(const loong_paged_desc* desc);
  *               the keys up to its own.
  *   starts      int32 [batch + 1], starting anywhere from 0, not falling.
  *   o, lse      bf16 [tokens][hq][head_dim] and fp32 [hq][tokens] (natural log of
- *               the softmax denominator), contiguous.
+ *               the softmax denominator), contiguous.  They must not overlap what
+ *               is read, nor k and v the pages.
  * The arrays are read on the device, so a captured call may be replayed on other
  * lengths, tables and starts.  Pages that two new tokens share (the same place
  * written twice) hold either's row.  A page outside the pool is read as zeros and
