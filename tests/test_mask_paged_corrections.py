@@ -54,7 +54,7 @@ def test_data_of_the_launch_before_is_read_by_plain_loads():
                 assert not re.search(rf"\b{re.escape(field)}\b", call.group(1)), f"{name}: {call.group(0)}"
 
 
-@pytest.mark.parametrize("value", [1e-46, -1e-46, 5e-324])
+@pytest.mark.parametrize("value", [1e-46, -1e-46, 5e-324, 2.0 ** -150])
 def test_a_number_that_vanishes_in_single_precision_is_refused(loong_lib, value):
     """0 would stand for no cap, or for the default scale."""
     x = inputs.make_inputs(W)
@@ -93,3 +93,8 @@ def test_document_ranges_with_a_window_wider_than_any_document(window, causal):
 def test_document_ranges_with_a_prefix_longer_than_any_document():
     assert torch.equal(ops.document_ranges([[4, 8]], 12, prefix=[[2 ** 40, 2 ** 31]]),
                        ops.document_ranges([[4, 8]], 12, causal=False))
+
+
+def test_the_smallest_numbers_are_the_library_s_to_judge(loong_lib):
+    for value in (2.0 ** -149, 1.01 * 2.0 ** -150):
+        assert ops.loong_attn_mask_check(ops.make_desc(W), ops.make_mask(None, value)) == ops.LOONG_ERR_UNSUPPORTED
